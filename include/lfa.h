@@ -337,6 +337,115 @@ int lfa_launches_per_forward(lfa_handle h);
  * environment variable LFA_FORWARD_PATH=generic before lfa_create forces the generic path. */
 const char* lfa_forward_path(lfa_handle h);
 
+/* ---- token operators: decay attention, rotary positions, group norm ---------------------------
+ * The causal, token-by-token companion of the Nystrom attention and what stands around it in a layer.
+ * These calls take no handle. Tensors of tokens are [B][heads][N][d] in the config's dtype with strides
+ * of the caller's choice for batch, head and token (in elements; the channels are contiguous), so the
+ * layout a projection leaves ([B][N][heads][d], or slices of one packed tensor) needs no copy; three
+ * zeros mean contiguous [B][heads][N][d]. Strides of dimensions larger than 1 are positive multiples of
+ * 16 bytes, pointers are 16-byte aligned, and an output's elements may not share memory with each other
+ * or, unless stated, with any input. Everything else follows the conventions at the top of this file:
+ * work is only enqueued on `stream`, on the current device; argument errors (LFA_ERR_INVALID_ARG, for
+ * sizes or dtypes outside the documented ranges LFA_ERR_UNSUPPORTED) come before any launch; results
+ * are bit-identical from call to call. Calls that overlap on the GPU need workspaces of their own. */
+
+/* Linear attention with a decay per head. Per (batch, head) unit, for t = 0 .. length-1,
+ *   S_t = exp(log_decay[head]) S_{t-1} + k_t v_t^T,   o_t = scale q_t S_t,
+ * with S_{-1} = S0 [dk][dv] (zero if NULL): sum_{j<=t} decay^(t-j) (q_t . k_j) v_j plus S0's part. There is
+ * no normaliser. q, k have dk channels, v, o have dv; log_decay is device fp32 [heads], at most 0 in
+ * use (-inf: only the token itself). States are fp32 [B][heads][dk][dv], contiguous.
+ * Arithmetic: fp32 tensors on CUDA cores in fp32. bf16 tensors: the token products are bf16-operand
+ * tensor-core products with fp32 accumulation, in which the decayed q.k weights and the state that q
+ * meets are rounded to bf16 once; the carried state is fp32 and takes k's decayed rows as the sum of
+ * two bf16 parts (about 2^-17 relative), so it stays fp32-accurate over any length. */
+typedef struct {
+  int B, heads;
+  int N;           /* tokens per sequence (with `lengths`: the padded length) */
+  int dk, dv;      /* 8 .. 128: multiples of 8 (bf16) or 4 (fp32) */
+  int dtype;       /* lfa_dtype of q, k, v, o and their gradients */
+  float scale;     /* finite */
+  long long q_stride[3], k_stride[3], v_stride[3], o_stride[3];   /* batch, head, token */
+} lfa_decay_config;
+
+/* Bytes of device workspace (256-byte aligned, overwritten) of lfa_decay_forward (backward = 0) or
+ * lfa_decay_backward (backward = 1); at least 256; 0 for a config that these calls refuse. */
+size_t lfa_decay_workspace_size(const lfa_decay_config* cfg, int backward);
+
+/* Outputs O and, if S_out is not NULL, the state after each sequence's last token. lengths: device int32
+ * [B] or NULL (all N); values are clamped to [0, N]; rows of O behind a sequence's end are left as they
+ * were, and inputs there are not used, whatever they hold. S_out may be S0 itself (a state carried from
+ * prompt piece to prompt piece); a sequence of length 0 gives S_out = S0. */
+lfa_status lfa_decay_forward(const lfa_decay_config* cfg, const void* Q, const void* K, const void* V,
+                             const float* log_decay, const float* S0, const int* lengths, void* O,
+                             float* S_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of <dO, O> + <dS_out, S_out>: dQ, dK, dV (strides of Q, K, V in cfg) and, if dS0 is not NULL,
+ * dS0; dO has cfg's o_stride; dS_out may be NULL (zero). Rows behind a sequence's end
+ * are left as they were in dQ, dK, dV and not used in dO. The decays get no gradient. Nothing is kept from
+ * the forward call. */
+lfa_status lfa_decay_backward(const lfa_decay_config* cfg, const void* Q, const void* K, const void* V,
+                              const float* log_decay, const float* S0, const int* lengths, const void* dO,
+                              const float* dS_out, void* dQ, void* dK, void* dV, float* dS0, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* One token of every row: S is updated in place and o = scale q S (cfg.N = 1; token strides unused).
+ * S: fp32 [n_slots][heads][dk][dv]; row b uses S[slots[b]] (device int32 [B]; NULL: S[b], n_slots >= B).
+ * A row whose slot is outside [0, n_slots) or is also the slot of an earlier row of the call changes no
+ * state and gets o = 0 (negative slots mark padding rows). All arithmetic is fp32. */
+lfa_status lfa_decay_step(const lfa_decay_config* cfg, const void* q, const void* k, const void* v,
+                          const float* log_decay, float* S, const int* slots, int n_slots, void* o, void* stream);
+
+/* LFA_OK, or LFA_ERR_TIMEOUT once after a bounded device-side wait of a decay call on the current device
+ * expired (its outputs are invalid). Synchronises `stream`. */
+lfa_status lfa_decay_status(void* stream);
+
+/* Rotary positions: channel pairs (a, b) of the first `rot` channels of every head turn by
+ * th = positions[batch][token] * freqs[i]:  (a, b) -> mscale (a cos th - b sin th, a sin th + b cos th).
+ * Pair i is channels (i, i + rot/2), or (2i, 2i + 1) with `interleaved`; the other channels are copied.
+ * inverse = 1 turns by -th, which is the transpose: the gradient of the call with inverse = 0.
+ * positions: device int32 [B][N]; freqs: device fp64 [rot/2] in radians per position. Angles are reduced
+ * in 64 bits, so they hold for any int32 position. x2 / y2 (heads2 > 0, else NULL) is a second tensor at the
+ * same positions (k beside q). y may be x (and y2 x2) with the same strides: in place. */
+typedef struct {
+  int B, N;
+  int d;                 /* channels per head: 8 .. 256, multiple of 8 (bf16) or 4 (fp32) */
+  int rot;               /* rotated channels: even, 2 .. min(d, 128) */
+  int heads, heads2;     /* >= 1, >= 0 */
+  int dtype;
+  int interleaved, inverse;
+  float mscale;          /* finite */
+  long long x_stride[3], x2_stride[3], y_stride[3], y2_stride[3];
+} lfa_rotary_config;
+lfa_status lfa_rotary(const lfa_rotary_config* cfg, const void* x, const void* x2, const int* positions,
+                      const double* freqs, void* y, void* y2, void* stream);
+
+/* Group norm with an activation, channels last: x [B][N][C] contiguous (N = H*W tokens of one sample;
+ * N = 1 normalises every token by itself), groups of C/groups neighbouring channels,
+ *   y = act((x - mean) / sqrt(var + eps) * gamma + beta), mean and population variance per (sample, group).
+ * gamma, beta: device fp32 [C], both or neither; mean, rstd: fp32 [B][groups] outputs (NULL: not stored) that
+ * the backward call reads. Statistics, the activation and all sums are fp32. */
+typedef enum { LFA_ACT_NONE = 0, LFA_ACT_SILU = 1, LFA_ACT_GELU = 2 /* exact (erf) */ } lfa_act;
+typedef struct {
+  int B, N, C;
+  int groups;            /* divides C */
+  int dtype;
+  int act;
+  float eps;             /* > 0 */
+} lfa_norm_config;
+
+/* Bytes of device workspace (256-byte aligned, overwritten) of lfa_group_norm (backward = 0) or its backward
+ * (1); at least 256; 0 for a config that these calls refuse. */
+size_t lfa_group_norm_workspace_size(const lfa_norm_config* cfg, int backward);
+/* y may be x. */
+lfa_status lfa_group_norm(const lfa_norm_config* cfg, const void* x, const float* gamma, const float* beta,
+                          void* y, float* mean, float* rstd, void* workspace, size_t workspace_bytes,
+                          void* stream);
+/* dx from dy, and dgamma, dbeta (fp32 [C]; both NULL when gamma is). dx may be dy. */
+lfa_status lfa_group_norm_backward(const lfa_norm_config* cfg, const void* x, const void* dy, const float* mean,
+                                   const float* rstd, const float* gamma, const float* beta, void* dx,
+                                   float* dgamma, float* dbeta, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif

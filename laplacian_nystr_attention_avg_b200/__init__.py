@@ -5,4 +5,4 @@ The compute path is the C-ABI library ``liblfa.so`` built from ``csrc/``;
 library is opened on first use and a missing library is an error, never a
 fallback.
 """
-__all__ = ["inputs", "lfa"]
+__all__ = ["decay", "inputs", "lfa"]

@@ -1,0 +1,110 @@
+// Internal declarations of the token operators (decay attention, rotary positions, group norm): kernel
+// argument blocks, filled by lfa_token_api.cu, and the launchers of lfa_decay.cu and lfa_token_ops.cu.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "lfa.h"
+
+namespace lfa {
+
+constexpr int kDecayChunk = 128;   // tokens per chunk of the prompt form; segments are whole chunks
+constexpr int kDecayMaxD = 128;    // largest dk, dv
+
+// One causal run over a unit's tokens: O_i = sum over j up to i of decay^(i-j) (x_i . y_j) z_j plus what the
+// state from before contributes (rev: from the last token backwards). The carried state R is the sum of
+// y_j z_j^T already decayed up to the token at hand: R = decay S_{t-1} (rev: decay G_{t+1}).
+struct DecayJob {
+  const void* X;
+  const void* Y;
+  const void* Z;
+  void* O;
+  long long xs[3], ys[3], zs[3], os[3];   // strides in elements: batch, head, token
+  const float* init;    // [units][..] state before the run, or null (zero)
+  float* fin;           // state after the run, or null
+  int da, db;           // channels of X, Y and of Z, O
+  int rev;              // runs from the last token to the first
+  int trans;            // the state is stored [db][da] instead of [da][db]
+  int init_decays;      // R_0 = decay^init_decays * init
+  int fin_sub;          // fin is decay^-fin_sub times the R after the last token
+  float c_inter, c_intra, c_state;   // factors of the state's part, of the chunk's own, of y z^T in the state
+};
+
+struct DecayArgs {
+  int B, heads, N;
+  const float* log_decay;   // [heads]
+  const int* lengths;       // [B] or null
+  int segs, seg_chunks;     // segments per unit, chunks per segment
+  float* seg_state;         // segs > 1: [njobs or 2][units][segs][dk*dv] states before each segment
+  int njobs;
+  DecayJob job[3];
+};
+
+struct DecayStepArgs {
+  int B, heads, dk, dv;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  long long qs[2], ks[2], vs[2], os[2];   // batch, head
+  const float* log_decay;
+  float* S;
+  const int* slots;
+  int n_slots;
+  float scale;
+};
+
+struct RotaryArgs {
+  int B, N, d, rot, heads, heads2, interleaved, inverse;
+  const void* x;
+  const void* x2;
+  void* y;
+  void* y2;
+  long long xs[3], x2s[3], ys[3], y2s[3];
+  const int* positions;
+  const double* freqs;
+  float mscale;
+};
+
+struct NormArgs {
+  int B, N, C, G, act;
+  float eps;
+  const void* x;
+  const void* dy;
+  void* y;          // forward output, or dx
+  const float* gamma;
+  const float* beta;
+  float* mean;      // [B][G]
+  float* rstd;
+  float* dgamma;
+  float* dbeta;
+  float* ws;        // backward: channel sums
+};
+
+cudaError_t launch_decay(const DecayArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_decay_step(const DecayStepArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t st);
+size_t norm_workspace_floats(int B, int N, int C, int G, int backward);
+cudaError_t launch_norm(const NormArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_norm_backward(const NormArgs& a, int dtype, cudaStream_t st);
+
+// ---- small device helpers shared by the two files -------------------------------------------------
+// decays below exp(-1e4) are zero to every power but 0; the bound keeps 0 * inf out of exp(n ld)
+__device__ __forceinline__ float decay_log(float ld) { return ld < -1e4f ? -1e4f : ld; }
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+}  // namespace lfa

@@ -1,0 +1,331 @@
+"""GPU tests of the decay attention calls (lfa_decay_forward, lfa_decay_backward, lfa_decay_step) against the
+dense causal form in 64 bits (tests/token_ref.py).
+
+Tolerances. T denotes the same form on absolute values (|q|, |k|, |v|, |S0|): the sum that every rounding
+is relative to.
+  * fp32: every output is a sum of products whose worst-case rounding is (terms) 2^-24 T: at most 128 products
+    of channels, 128 tokens within a chunk and one addition per chunk, plus 16 for the factors (expf and
+    expm1f within 2 units, their argument's rounding 2^-24 |n log_decay|, at most 88 of which leave a
+    number above fp32's range of underflow), so bound (128 + 128 + N/32 + 16 + 88) 2^-24 T.
+  * bf16: the output's own rounding 2^-8 |o| (half a step of bf16), one bf16 rounding (2^-8) of each weight
+    decay^(i-j) q_i.k_j or of the state that q meets: 2^-8 T in the worst case, plus the fp32 bound. Normwise,
+    for independent random terms the errors add as their squares do and the terms' squares sum to the
+    output's, so |err| <= sqrt(2) 2^-8 |o| (taken with 10 % for the finite sample).
+  * states of bf16 tensors: fp32 sums of exact products of v with k's decayed rows split in two bf16 parts
+    (2^-16 at most), so 2^-16 T plus the fp32 bound; normwise 2^-16 likewise.
+"""
+import math
+
+import pytest
+import torch
+
+from laplacian_nystr_attention_avg_b200 import decay
+from tests import token_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _mk(shape, dtype, g, order="bhnd"):
+    B, H, N, d = shape
+    if order == "bhnd":
+        return torch.randn(shape, generator=g, device="cuda").to(dtype)
+    if order == "bnhd":
+        return torch.randn((B, N, H, d), generator=g, device="cuda").to(dtype).transpose(1, 2)
+    # "packed": a slice of a wider tensor, as one projection for q, k, v leaves it
+    return torch.randn((B, N, H, 3 * d), generator=g, device="cuda").to(dtype)[..., d:2 * d].transpose(1, 2)
+
+
+def _log_decay(H, kind="mixed"):
+    vals = {"mixed": [-0.03, -2.0 ** -12, -0.7, 0.0, -8.0, -float("inf")], "slow": [-2.0 ** -10],
+            "one": [0.0]}[kind]
+    return torch.tensor([vals[i % len(vals)] for i in range(H)], dtype=F32, device="cuda")
+
+
+def _poison(t, lengths):
+    """NaN and infinities on the rows behind each sequence's end."""
+    if lengths is not None:
+        for b, L in enumerate(lengths.tolist()):
+            t[b, :, max(0, L):] = float("nan")
+            t[b, :, max(0, L) + 1::2] = float("inf")
+
+
+def _inputs(B, H, N, dk, dv, dtype, order="bhnd", state=True, lengths=None, kind="mixed", seed=0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    q, k, v = _mk((B, H, N, dk), dtype, g, order), _mk((B, H, N, dk), dtype, g, order), _mk((B, H, N, dv), dtype, g, order)
+    S0 = torch.randn((B, H, dk, dv), generator=g, device="cuda") if state else None
+    L = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    for t in (q, k, v):
+        _poison(t, L)
+    return q, k, v, _log_decay(H, kind), S0, L, g
+
+
+def _clean(t, L):
+    t = t.double()
+    if L is not None:
+        for b, n in enumerate(L.tolist()):
+            t[b, :, max(0, n):] = 0
+    return t
+
+
+def _f32_bound(N, T):
+    return (128 + 128 + N / 32 + 16 + 88) * 2.0 ** -24 * T + 1e-37
+
+
+def _check_rows(got, ref, T, N, dtype, what):
+    err = (got.double() - ref).abs()
+    bound = _f32_bound(N, T)
+    if dtype == BF:
+        bound = bound + 2.0 ** -8 * ref.abs() + 2.0 ** -8 * T * (1 + 2.0 ** -8)
+    assert torch.isfinite(got).all(), what
+    bad = err > bound
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} over the bound, worst {float((err / bound).max()):.3g}"
+    if dtype == BF and ref.numel() >= 4096:
+        rel = float(err.norm() / ref.norm())
+        assert rel <= 1.1 * math.sqrt(2) * 2.0 ** -8, f"{what}: normwise {rel:.2e}"
+
+
+def _check_state(got, ref, T, N, dtype, what):
+    err = (got.double() - ref).abs()
+    bound = _f32_bound(N, T) + (2.0 ** -16 * T if dtype == BF else 0.0)
+    assert torch.isfinite(got).all(), what
+    assert not (err > bound).any(), f"{what}: worst {float((err / bound).max()):.3g} of the bound"
+    assert float(err.norm() / ref.norm().clamp(min=1e-30)) <= (2.0 ** -16 if dtype == BF else 2e-6), what
+
+
+def _run_forward(B, H, N, dk, dv, dtype, order="bhnd", state=True, lengths=None, kind="mixed", seed=0):
+    q, k, v, ld, S0, L, _ = _inputs(B, H, N, dk, dv, dtype, order, state, lengths, kind, seed)
+    scale = dk ** -0.5
+    O = torch.full_like(v, 7.0)
+    o, S = decay.decay_forward(q, k, v, ld, S0=S0, lengths=L, O=O, return_state=True)
+    assert decay.decay_status() == 0
+    q, k, v = (_clean(t, L) for t in (q, k, v))
+    ro, rS = R.decay_forward(q, k, v, ld, scale, None if S0 is None else S0.double(), L)
+    To, TS = R.decay_forward(q.abs(), k.abs(), v.abs(), ld, scale, None if S0 is None else S0.double().abs(), L)
+    for b in range(B):
+        n = N if L is None else max(0, min(N, int(L[b])))
+        assert (o[b, :, n:] == 7.0).all(), "rows behind the end were written"
+        _check_rows(o[b, :, :n], ro[b, :, :n], To[b, :, :n], N, dtype, f"o[{b}]")
+    _check_state(S, rS, TS, N, dtype, "S")
+
+
+SIZES = [(8, 8), (16, 64), (64, 64), (40, 128), (128, 128), (72, 24)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [1, 2, 31, 33, 127, 128, 129, 257, 640])
+def test_forward_lengths(N, dtype):
+    _run_forward(2, 6, N, 64, 64, dtype, seed=N)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv", SIZES)
+@pytest.mark.parametrize("order,state", [("bhnd", False), ("bnhd", True), ("packed", True)])
+def test_forward_sizes(dk, dv, order, state, dtype):
+    _run_forward(2, 3, 300, dk, dv, dtype, order, state, seed=dk + dv)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [32, 128])
+def test_forward_ragged_padding_holds_anything(d, dtype):
+    _run_forward(7, 6, 400, d, d, dtype, "bnhd", True, [0, 1, 400, 128, 129, 255, 77], seed=d)
+    _run_forward(2, 2, 200, d, d, dtype, "bhnd", False, [-3, 1000], seed=d + 1)   # clamped to [0, N]
+
+
+def test_fp32_channels_of_four():
+    _run_forward(1, 2, 70, 12, 20, F32)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,H,N,d", [(1, 1, 9000, 64), (1, 2, 5000, 128), (3, 2, 2500, 32)])
+def test_forward_long(B, H, N, d, dtype):
+    """Few units over long sequences: the work is split along the sequence."""
+    lengths = None if B == 1 else [N, 1300, 1]
+    _run_forward(B, H, N, d, d, dtype, "bhnd", True, lengths, "slow", seed=N)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_pieces_equal_the_whole(dtype):
+    """A sequence in pieces, the state handed on in place, against the sequence at once: same bounds."""
+    q, k, v, ld, S0, _, _ = _inputs(1, 4, 700, 64, 48, dtype, "bnhd")
+    S = S0.clone()
+    parts = []
+    for a, b in ((0, 1), (1, 130), (130, 131), (131, 700)):
+        o, S = decay.decay_forward(q[:, :, a:b], k[:, :, a:b], v[:, :, a:b], ld, S0=S, S_out=S)
+        parts.append(o)
+    o = torch.cat(parts, 2)
+    ro, rS = R.decay_forward(q.double(), k.double(), v.double(), ld, 64 ** -0.5, S0.double(), None)
+    To, TS = R.decay_forward(q.double().abs(), k.double().abs(), v.double().abs(), ld, 64 ** -0.5, S0.double().abs(), None)
+    _check_rows(o, ro, To, 700, dtype, "o")
+    _check_state(S, rS, TS, 700, dtype, "S")
+
+
+def _run_backward(B, H, N, dk, dv, dtype, order="bhnd", state=True, lengths=None, kind="mixed", seed=0):
+    q, k, v, ld, S0, L, g = _inputs(B, H, N, dk, dv, dtype, order, state, lengths, kind, seed)
+    dO = _mk((B, H, N, dv), dtype, g, "bnhd")
+    _poison(dO, L)
+    dS = torch.randn((B, H, dk, dv), generator=g, device="cuda") if state else None
+    scale = dk ** -0.5
+    outs = [torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device="cuda").fill_(7.0) for t in (q, k, v)]
+    dq, dk_, dv_, dS0 = decay.decay_backward(q, k, v, ld, dO, S0=S0, lengths=L, dS_out=dS, dQ=outs[0], dK=outs[1],
+                                             dV=outs[2], return_state=True)
+    assert decay.decay_status() == 0
+    q, k, v, dO = (_clean(t, L) for t in (q, k, v, dO))
+    S0d = None if S0 is None else S0.double()
+    dSd = None if dS is None else dS.double()
+    ref = R.decay_grads(q, k, v, ld, scale, S0d, L, dO, dSd)
+    T = R.decay_grads(q.abs(), k.abs(), v.abs(), ld, scale, None if S0 is None else S0d.abs(), L, dO.abs(),
+                      None if dS is None else dSd.abs())
+    for name, got, r, t in (("dq", dq, ref[0], T[0]), ("dk", dk_, ref[1], T[1]), ("dv", dv_, ref[2], T[2])):
+        for b in range(B):
+            n = N if L is None else max(0, min(N, int(L[b])))
+            assert (got[b, :, n:] == 7.0).all(), f"{name}: rows behind the end were written"
+            _check_rows(got[b, :, :n], r[b, :, :n], t[b, :, :n], N, dtype, f"{name}[{b}]")
+    _check_state(dS0, ref[3], T[3], N, dtype, "dS0")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [1, 2, 33, 128, 129, 257, 640])
+def test_backward_lengths(N, dtype):
+    _run_backward(2, 6, N, 64, 64, dtype, seed=N)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv", SIZES)
+@pytest.mark.parametrize("order,state", [("bhnd", False), ("packed", True)])
+def test_backward_sizes(dk, dv, order, state, dtype):
+    _run_backward(2, 3, 300, dk, dv, dtype, order, state, seed=dk + dv)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [32, 128])
+def test_backward_ragged_padding_holds_anything(d, dtype):
+    _run_backward(7, 6, 400, d, d, dtype, "bnhd", True, [0, 1, 400, 128, 129, 255, 77], seed=d)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,H,N,d", [(1, 1, 6000, 64), (1, 2, 3500, 128), (3, 1, 2500, 32)])
+def test_backward_long(B, H, N, d, dtype):
+    lengths = None if B == 1 else [N, 1300, 1]
+    _run_backward(B, H, N, d, d, dtype, "bhnd", True, lengths, "slow", seed=N)
+
+
+def test_gradients_against_differences():
+    """O and S are linear in each of q, k, v, S0, so a difference of step 1 is the derivative itself: it must
+    agree with <gradient, direction> up to the fp32 rounding of both sides."""
+    q, k, v, ld, S0, _, g = _inputs(2, 3, 200, 32, 48, F32)
+    dO = _mk(v.shape, F32, g)
+    dS = torch.randn(S0.shape, generator=g, device="cuda")
+
+    def loss(q, k, v, S0):
+        o, S = decay.decay_forward(q, k, v, ld, S0=S0, return_state=True)
+        return float((o.double() * dO).sum() + (S.double() * dS).sum())
+
+    at = [q, k, v, S0]
+    grads = decay.decay_backward(q, k, v, ld, dO, S0=S0, dS_out=dS, return_state=True)
+    base = loss(*at)
+    To, TS = R.decay_forward(*(2 * t.double().abs() for t in (q, k, v)), ld, 32 ** -0.5, 2 * S0.double().abs(), None)
+    # The roundings of different outputs are independent, each at most 64 2^-24 (the longest chain of a
+    # T-sized output is far shorter on average) of T |dO|: their sum over the outputs has a standard deviation
+    # below the root of the sum of squares. Six of those, for the two forwards and the gradient's own sum.
+    each = torch.cat([(To * dO.abs()).flatten(), (TS * dS.abs()).flatten()])
+    tol = 6 * 64 * 2.0 ** -24 * float(each.norm())
+    for i in range(4):
+        u = torch.randn(at[i].shape, generator=g, device="cuda")
+        moved = [t + u if j == i else t for j, t in enumerate(at)]
+        diff = loss(*moved) - base
+        want = float((grads[i].double() * (moved[i].double() - at[i].double())).sum())
+        assert abs(diff - want) <= tol, (i, diff, want)
+        assert abs(want) > 2 * tol, "the direction shows nothing"
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,H,dk,dv", [(1, 1, 8, 8), (1, 8, 64, 64), (33, 3, 128, 128), (5, 2, 40, 72), (300, 1, 24, 16)])
+def test_step(B, H, dk, dv, dtype):
+    g = torch.Generator("cuda").manual_seed(B)
+    q, k, v = (torch.randn((B, H, d), generator=g, device="cuda").to(dtype) for d in (dk, dk, dv))
+    n = B + 4
+    S = torch.randn((n, H, dk, dv), generator=g, device="cuda")
+    slots = torch.randperm(n, generator=g, device="cuda")[:B].to(torch.int32)
+    ld = _log_decay(H)
+    S1 = S.clone()
+    o = decay.decay_step(q, k, v, ld, S1, slots=slots)
+    at = slots.long()
+    lam = R.decays(ld, torch.tensor(1, device="cuda"))[:, None, None]
+    ref = S.double().clone()
+    ref[at] = lam * S.double()[at] + k.double()[..., None] * v.double()[..., None, :]
+    T = lam * S.double()[at].abs() + k.double().abs()[..., None] * v.double().abs()[..., None, :]
+    assert ((S1.double()[at] - ref[at]).abs() <= 4 * 2.0 ** -24 * T + 1e-37).all()
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert torch.equal(S1[rest], S[rest])
+    ro = dk ** -0.5 * (q.double()[..., None, :] @ ref[at]).squeeze(-2)
+    To = dk ** -0.5 * (q.double().abs()[..., None, :] @ T).squeeze(-2)
+    bound = (dk + 8) * 2.0 ** -24 * To + (2.0 ** -8 * ro.abs() if dtype == BF else 0) + 1e-37
+    assert ((o.double() - ro).abs() <= bound).all()
+
+
+def test_step_slots_that_are_padding_or_named_twice():
+    B, H, d = 6, 2, 16
+    g = torch.Generator("cuda").manual_seed(1)
+    q, k, v = (torch.randn((B, H, d), generator=g, device="cuda") for _ in range(3))
+    S = torch.randn((4, H, d, d), generator=g, device="cuda")
+    ld = _log_decay(H)
+    slots = torch.tensor([2, -1, 0, 2, 4, 0], dtype=torch.int32, device="cuda")
+    S1 = S.clone()
+    o = decay.decay_step(q, k, v, ld, S1, slots=slots)
+    S2 = S.clone()
+    o2 = decay.decay_step(q[[0, 2]].contiguous(), k[[0, 2]].contiguous(), v[[0, 2]].contiguous(), ld, S2,
+                          slots=torch.tensor([2, 0], dtype=torch.int32, device="cuda"))
+    assert torch.equal(S1, S2) and torch.equal(o[[0, 2]], o2)
+    assert (o[[1, 3, 4, 5]] == 0).all()
+
+
+def test_steps_equal_the_prompt_form():
+    q, k, v, ld, S0, _, _ = _inputs(2, 4, 20, 32, 64, F32)
+    S = S0.clone()
+    rows = [decay.decay_step(q[:, :, t], k[:, :, t], v[:, :, t], ld, S) for t in range(20)]
+    ro, rS = R.decay_forward(q.double(), k.double(), v.double(), ld, 32 ** -0.5, S0.double(), None)
+    To, TS = R.decay_forward(q.double().abs(), k.double().abs(), v.double().abs(), ld, 32 ** -0.5, S0.double().abs(), None)
+    _check_rows(torch.stack(rows, 2), ro, To, 20, F32, "o")
+    _check_state(S, rS, TS, 20, F32, "S")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_repeated_calls_are_bit_identical(dtype):
+    q, k, v, ld, S0, _, g = _inputs(2, 3, 1500, 64, 64, dtype)
+    dO = _mk(v.shape, dtype, g)
+    a = decay.decay_forward(q, k, v, ld, S0=S0, return_state=True) + decay.decay_backward(
+        q, k, v, ld, dO, S0=S0, return_state=True)
+    for _ in range(5):
+        b = decay.decay_forward(q, k, v, ld, S0=S0, return_state=True) + decay.decay_backward(
+            q, k, v, ld, dO, S0=S0, return_state=True)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_other_stream_and_graph(dtype):
+    q, k, v, ld, S0, _, g = _inputs(1, 4, 2000, 64, 64, dtype)
+    dO = _mk(v.shape, dtype, g)
+    want = decay.decay_forward(q, k, v, ld, S0=S0, return_state=True) + decay.decay_backward(q, k, v, ld, dO, S0=S0)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = decay.decay_forward(q, k, v, ld, S0=S0, return_state=True, stream=s) + decay.decay_backward(
+        q, k, v, ld, dO, S0=S0, stream=s.cuda_stream)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got) if a is not None)
+    # two graphs, replayed in turn
+    graphs, outs = [], []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(decay.decay_forward(q, k, v, ld, S0=S0, return_state=True) +
+                        decay.decay_backward(q, k, v, ld, dO, S0=S0))
+        graphs.append(gr)
+    for _ in range(3):
+        for gr in graphs:
+            gr.replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(a, b) for a, b in zip(want, o) if a is not None)

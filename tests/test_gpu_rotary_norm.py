@@ -1,0 +1,308 @@
+"""GPU tests of lfa_rotary and lfa_group_norm / lfa_group_norm_backward against 64-bit forms
+(tests/token_ref.py), and of the layer that decay attention, rotary and norm make up.
+
+Tolerances.
+  * rotary: y = mscale (a c - b s): three fp32 roundings, the cosine's and sine's own error (the reduced angle
+    is rounded to fp32, 2^-24 of at most pi, sincospif adds 2 units: 2^-22 absolute), so 8 * 2^-24 *
+    mscale (|a| + |b|); bf16 adds half a step, 2^-8 |y|.
+  * group norm: the mean of n values is within c 2^-24 of mean|x| with c = 64 (sums run over short chains that
+    are joined in trees), the variance about it likewise, so xhat is within c 2^-24 (|x| + mean|x|) rstd plus c
+    2^-24 |xhat|; gamma and the activation (slope at most 1.13, expf / erff within 4 units) carry that on; bf16
+    adds 2^-8 |y|.
+  * its gradients: sums of n terms in such chains (c 2^-24 of the sum of absolute values), dx adds the same
+    for each of its three terms; bf16 adds 2^-8 |dx|.
+"""
+import pytest
+import torch
+
+from laplacian_nystr_attention_avg_b200 import decay
+from tests import token_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+
+
+def _tok(B, H, N, d, dtype, g, order):
+    t = torch.randn((B, H, N, d) if order == "bhnd" else (B, N, H, d), generator=g, device="cuda").to(dtype)
+    return t if order == "bhnd" else t.transpose(1, 2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d,rot", [(8, 2), (64, 64), (128, 96), (128, 128), (72, 20), (40, 6), (256, 128)])
+@pytest.mark.parametrize("B,N,H,H2,order", [(1, 1, 1, 0, "bhnd"), (3, 37, 5, 2, "bnhd")])
+def test_rotary(B, N, H, H2, order, d, rot, layout, dtype):
+    g = torch.Generator("cuda").manual_seed(d + rot)
+    x, x2 = _tok(B, H, N, d, dtype, g, order), (_tok(B, H2, N, d, dtype, g, order) if H2 else None)
+    pos = torch.randint(0, 2 ** 31 - 1, (B, N), generator=g, device="cuda").to(torch.int32)
+    pos[0, 0] = 0
+    if N > 2:
+        pos[:, 1], pos[:, 2] = 2 ** 31 - 1, -5
+    freqs, _ = decay.rotary_frequencies(rot)
+    for inverse in (False, True):
+        y, y2 = decay.rotary(x, pos, freqs, x2=x2, layout=layout, mscale=1.25, inverse=inverse)
+        for src, out in ((x, y), (x2, y2)):
+            if src is None:
+                assert out is None
+                continue
+            ref = R.rotate(src.double(), pos, freqs, layout == "interleaved", 1.25, inverse)
+            T = 1.25 * (src.double().abs() + R.rotate(src.double().abs(), torch.zeros_like(pos), freqs, False, 1.0, False).amax(-1, keepdim=True))
+            bound = 8 * U * T + (2.0 ** -8 * ref.abs() if dtype == BF else 0)
+            assert ((out.double() - ref).abs() <= bound).all()
+            assert torch.equal(out[..., rot:], src[..., rot:])
+        z, z2 = x.clone(), None if x2 is None else x2.clone()
+        decay.rotary(z, pos, freqs, x2=z2, layout=layout, mscale=1.25, inverse=inverse, out=z, out2=z2)   # in place
+        assert torch.equal(z, y) and (z2 is None or torch.equal(z2, y2))
+
+
+def test_rotary_inverse_is_the_transpose():
+    """<rotary(x), u> = <x, rotary(u, inverse)> for every x and u; the rotation is linear, so this is its gradient."""
+    g = torch.Generator("cuda").manual_seed(3)
+    x, u = _tok(2, 3, 50, 64, F32, g, "bnhd"), _tok(2, 3, 50, 64, F32, g, "bhnd")
+    pos = torch.randint(0, 10 ** 6, (2, 50), generator=g, device="cuda").to(torch.int32)
+    freqs, ms = decay.rotary_frequencies(48, scaling="ramp", factor=8.0, context=4096)
+    for layout in ("half", "interleaved"):
+        y, _ = decay.rotary(x, pos, freqs, layout=layout, mscale=ms)
+        w, _ = decay.rotary(u, pos, freqs, layout=layout, mscale=ms, inverse=True)
+        a, b = float((y.double() * u).sum()), float((x.double() * w).sum())
+        assert abs(a - b) <= 32 * U * float((y.double() * u).abs().sum())
+        assert abs(a) > 1.0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rotary_many_tokens_and_heads(dtype):
+    g = torch.Generator("cuda").manual_seed(4)
+    x = _tok(2, 33, 1001, 64, dtype, g, "bnhd")
+    pos = torch.arange(2002, device="cuda", dtype=torch.int32).view(2, 1001)
+    freqs, _ = decay.rotary_frequencies(64)
+    y, _ = decay.rotary(x, pos, freqs)
+    ref = R.rotate(x.double(), pos, freqs, False, 1.0, False)
+    bound = 8 * U * 2 * x.double().abs().amax(-1, keepdim=True) + (2.0 ** -8 * ref.abs() if dtype == BF else 0)
+    assert ((y.double() - ref).abs() <= bound).all()
+
+
+# ---- group norm ---------------------------------------------------------------------------------------
+
+C_SUM = 64
+SHAPES = [(1, 1, 8, 1), (1, 1, 8, 8), (5, 1, 64, 4), (777, 1, 1024, 16), (3, 49, 40, 4), (2, 3136, 64, 32), (2, 784, 320, 32),
+          (3, 130, 10, 1), (2, 257, 72, 9), (1, 6000, 24, 3), (4, 2, 2304, 32), (2, 1000, 512, 1), (1, 12544, 256, 8)]
+
+
+def _norm_inputs(B, N, C, dtype, affine, offset, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = (torch.randn((B, N, C), generator=g, device="cuda") + offset).to(dtype)
+    gamma = 1 + 0.3 * torch.randn((C,), generator=g, device="cuda") if affine else None
+    beta = 0.3 * torch.randn((C,), generator=g, device="cuda") if affine else None
+    return x, gamma, beta, g
+
+
+def _d(t):
+    return None if t is None else t.double()
+
+
+def _xhat_error(x, groups, eps):
+    """Bound on the error of xhat, and xhat, elementwise in 64 bits."""
+    g = x.reshape(x.shape[0], x.shape[1], groups, -1)
+    mean = g.mean((1, 3), keepdim=True)
+    rstd = (((g - mean) ** 2).mean((1, 3), keepdim=True) + eps) ** -0.5
+    xh = (g - mean) * rstd
+    err = C_SUM * U * ((g.abs() + g.abs().mean((1, 3), keepdim=True)) * rstd + xh.abs())
+    # an error e of the mean moves the variance by e^2 only; the rounding of x - mean moves it like xhat
+    err = err + xh.abs() * C_SUM * U * (g.abs().mean((1, 3), keepdim=True) * rstd)
+    return err.reshape(x.shape), xh.reshape(x.shape), mean, rstd
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("B,N,C,G", SHAPES)
+def test_group_norm(B, N, C, G, act, dtype):
+    affine = (B + N) % 2 == 1 or act != "none"
+    x, gamma, beta, _ = _norm_inputs(B, N, C, dtype, affine, 0.5, C + N)
+    y, mean, rstd = decay.group_norm(x, G, gamma, beta, eps=1e-5, act=act)
+    ref, rm, rr = R.group_norm(x.double(), G, _d(gamma), _d(beta), 1e-5, act)
+    err, xh, _, _ = _xhat_error(x.double(), G, 1e-5)
+    scale = 1.0 if gamma is None else gamma.double().abs()
+    z = xh * scale + (0 if beta is None else beta.double().abs())
+    bound = 1.13 * (err * scale + 4 * U * z.abs()) + 16 * U * (z.abs() + ref.abs()) + (2.0 ** -8 * ref.abs() if dtype == BF else 0) + 1e-30
+    bad = (y.double() - ref).abs() > bound
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, worst {float(((y.double() - ref).abs() / bound).max()):.3g}"
+    ma = x.double().abs().reshape(B, N, G, -1).mean((1, 3))
+    assert ((mean.double() - rm).abs() <= C_SUM * U * ma).all()
+    assert ((rstd.double() - rr).abs() <= C_SUM * U * rr * (1 + ma * rr)).all()
+    z = x.clone()
+    decay.group_norm(z, G, gamma, beta, act=act, out=z)     # in place
+    assert torch.equal(z, y)
+
+
+def test_group_norm_of_values_far_from_zero():
+    """mean 1000, deviation 1, in fp32: a difference of sums of squares would lose everything."""
+    x, gamma, beta, _ = _norm_inputs(2, 500, 64, F32, True, 1000.0, 1)
+    y, mean, rstd = decay.group_norm(x, 8, gamma, beta)
+    ref, rm, rr = R.group_norm(x.double(), 8, _d(gamma), _d(beta), 1e-5, "none")
+    err, _, _, _ = _xhat_error(x.double(), 8, 1e-5)
+    assert ((y.double() - ref).abs() <= err * gamma.double().abs() + 16 * U * (ref.abs() + 1)).all()
+
+
+def test_group_norm_of_constant_groups():
+    x = torch.full((2, 30, 16), 3.0, device="cuda")
+    y, mean, rstd = decay.group_norm(x, 4, act="none", eps=1e-5)
+    assert (y == 0).all() and (mean == 3).all()
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-6)
+
+
+def _norm_grads(x, dy, G, gamma, beta, eps, act):
+    leaves = [t.double().requires_grad_() for t in (x, gamma, beta) if t is not None]
+    ga, be = (leaves[1], leaves[2]) if gamma is not None else (None, None)
+    y, _, _ = R.group_norm(leaves[0], G, ga, be, eps, act)
+    return torch.autograd.grad((y * dy.double()).sum(), leaves)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("B,N,C,G", SHAPES)
+def test_group_norm_backward(B, N, C, G, act, dtype):
+    affine = (B + N) % 2 == 1 or act != "none"
+    if N * (C // G) < 8:
+        affine = False
+    x, gamma, beta, g = _norm_inputs(B, N, C, dtype, affine, 0.5, C + N)
+    dy = torch.randn((B, N, C), generator=g, device="cuda").to(dtype)
+    _, mean, rstd = decay.group_norm(x, G, gamma, beta, act=act)
+    dx, dgamma, dbeta = decay.group_norm_backward(x, dy, mean, rstd, G, gamma, beta, act=act)
+    grads = _norm_grads(x, dy, G, gamma, beta, 1e-5, act)
+    err, xh, _, rs = _xhat_error(x.double(), G, 1e-5)
+    sc = torch.ones(C, dtype=torch.float64, device="cuda") if gamma is None else gamma.double().abs()
+    # dz = dy act'(z) with |act''| <= 0.8 on an error of z, and |act'| <= 1.13
+    edz = dy.double().abs() * (0.8 * (err * sc + 4 * U * (xh.abs() * sc + 1)) + 8 * U * 1.13)
+    adz = 1.13 * dy.double().abs()
+
+    def grouped(t):
+        return t.reshape(B, N, G, -1)
+
+    gz, egz = grouped(adz * sc), grouped(edz * sc + 2 * U * adz * sc)
+    m1, em1 = gz.mean((1, 3), keepdim=True), egz.mean((1, 3), keepdim=True)
+    gx, egx = gz * grouped(xh).abs(), egz * grouped(xh).abs() + gz * grouped(err)
+    m2, em2 = gx.mean((1, 3), keepdim=True), egx.mean((1, 3), keepdim=True)
+    size = gz + m1 + grouped(xh).abs() * m2
+    bound = rs * (egz + em1 + grouped(xh).abs() * em2 + grouped(err) * m2 + C_SUM * U * size)
+    bound = bound + C_SUM * U * (1 + grouped(x.double().abs()).mean((1, 3), keepdim=True) * rs) * rs * size
+    bound = bound.reshape(x.shape) + (2.0 ** -8 * grads[0].abs() if dtype == BF else 0) + 1e-30
+    bad = (dx.double() - grads[0]).abs() > bound
+    assert not bad.any(), f"dx: {int(bad.sum())}, worst {float(((dx.double() - grads[0]).abs() / bound).max()):.3g}"
+    if gamma is None:
+        assert dgamma is None and dbeta is None
+    else:
+        eb = edz.sum((0, 1)) + C_SUM * U * adz.sum((0, 1))
+        eg = (edz * xh.abs() + adz * err).sum((0, 1)) + C_SUM * U * (adz * xh.abs()).sum((0, 1))
+        assert ((dbeta.double() - grads[2]).abs() <= eb).all()
+        assert ((dgamma.double() - grads[1]).abs() <= eg).all()
+    d2 = dy.clone()
+    _, dg2, db2 = decay.group_norm_backward(x, d2, mean, rstd, G, gamma, beta, act=act, dx=d2)   # in place of dy
+    assert torch.equal(d2, dx)
+    if gamma is not None:
+        assert torch.equal(dg2, dgamma) and torch.equal(db2, dbeta)
+
+
+def test_group_norm_gradient_against_differences():
+    x, gamma, beta, g = _norm_inputs(2, 40, 24, F32, True, 0.5, 5)
+    dy = torch.randn(x.shape, generator=g, device="cuda")
+    _, mean, rstd = decay.group_norm(x, 3, gamma, beta, act="silu")
+    grads = decay.group_norm_backward(x, dy, mean, rstd, 3, gamma, beta, act="silu")
+    at, h = [x, gamma, beta], 2.0 ** -6
+    for i in range(3):
+        u = torch.randn(at[i].shape, generator=g, device="cuda")
+
+        def loss(sign):
+            a = [t + sign * h * u if j == i else t for j, t in enumerate(at)]
+            return float((decay.group_norm(a[0], 3, a[1], a[2], act="silu")[0].double() * dy).sum())
+
+        diff = (loss(1) - loss(-1)) / (2 * h)
+        want = float((grads[i].double() * u).sum())
+        n = float(u.norm())
+        # the step's third-order term: h^2 / 6 times a third derivative of the size of the gradient's own
+        # terms (|u|^3 summed), and the loss's rounding 2^-24 sqrt(terms) / h
+        assert abs(diff - want) <= h * h * n * float(dy.norm()) + 2.0 ** -20 / h * float(dy.norm()), i
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_repeated_calls_graph_and_stream(dtype):
+    x, gamma, beta, g = _norm_inputs(3, 700, 96, dtype, True, 0.5, 6)
+    dy = torch.randn(x.shape, generator=g, device="cuda").to(dtype)
+
+    def both(stream=None):
+        y, m, r = decay.group_norm(x, 8, gamma, beta, act="gelu", stream=stream)
+        return (y, m, r) + decay.group_norm_backward(x, dy, m, r, 8, gamma, beta, act="gelu", stream=stream)
+
+    want = both()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = both(s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = both()
+    for _ in range(3):
+        gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+# ---- the layer -----------------------------------------------------------------------------------------
+
+def _layer(B, N, H, dk, dv, seed=0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    ld = -0.02 * torch.arange(1, H + 1, device="cuda", dtype=F32)
+    gamma, beta = 1 + 0.1 * torch.randn(H * dv, generator=g, device="cuda"), 0.1 * torch.randn(H * dv, generator=g, device="cuda")
+    freqs, ms = decay.rotary_frequencies(dk // 2, scaling="ntk", factor=4.0)
+    mod = decay.DecayAttention(ld, gamma, beta, freqs, mscale=ms, layout="interleaved")
+    q, k, v = (torch.randn((B, N, H, d), generator=g, device="cuda") for d in (dk, dk, dv))
+    pos = (torch.arange(N, device="cuda") + 100000).to(torch.int32).expand(B, N).contiguous()
+    return mod, q, k, v, pos, g
+
+
+def _layer_ref(mod, q, k, v, pos, S0, gamma, beta):
+    B, N, H, dv = v.shape
+    qr, kr = (R.rotate(t.transpose(1, 2), pos, mod.freqs, True, mod.mscale, False) for t in (q, k))
+    o, S = R.decay_forward(qr, kr, v.transpose(1, 2), mod.log_decay, q.shape[3] ** -0.5, S0, None)
+    y, _, _ = R.group_norm(o.transpose(1, 2).reshape(B * N, 1, H * dv), H, gamma, beta, mod.eps, mod.act)
+    return y.reshape(B, N, H * dv), S
+
+
+def test_layer_prompt_steps_and_gradients_fp32():
+    """Prompt, then single tokens from its state, then the gradients of the prompt: against the 64-bit layer.
+    Everything is fp32; the norm divides by the deviation of a token's head, so the tolerance is 2^-24 times a
+    few hundred roundings times the largest ratio of that division: 1e-3 of the output's own size."""
+    B, N, H, dk, dv = 2, 150, 4, 32, 64
+    mod, q, k, v, pos, g = _layer(B, N + 3, H, dk, dv)
+    S0 = torch.randn((B, H, dk, dv), generator=g, device="cuda")
+    cut = [t[:, :N].contiguous() for t in (q, k, v)]
+    y, S, saved = mod.forward(*cut, pos[:, :N].contiguous(), S0=S0)
+    leaves = [t.double().requires_grad_() for t in (*cut, S0, mod.gamma, mod.beta)]
+    ry, rS = _layer_ref(mod, *leaves[:3], pos[:, :N], leaves[3], leaves[4], leaves[5])
+    assert ((y.double() - ry).abs().max() <= 1e-3 * ry.abs().max())
+    assert float((y.double() - ry.detach()).norm() / ry.detach().norm()) <= 1e-5
+    dy, dS = torch.randn(y.shape, generator=g, device="cuda"), torch.randn(S.shape, generator=g, device="cuda")
+    want = torch.autograd.grad((ry * dy).sum() + (rS * dS).sum(), leaves)
+    got = mod.backward(saved, dy, dS)
+    for a, b in zip(got, want):
+        assert float((a.double() - b).norm() / b.norm()) <= 1e-4
+    fy, _ = _layer_ref(mod, q.double(), k.double(), v.double(), pos, S0.double(), mod.gamma.double(), mod.beta.double())
+    for t in range(N, N + 3):
+        yt = mod.step(q[:, t], k[:, t], v[:, t], S, pos[:, t].contiguous())
+        assert float((yt.double() - fy[:, t]).norm() / fy[:, t].norm()) <= 1e-5
+
+
+def test_layer_bf16_ragged_runs_and_trains():
+    B, N, H, dk, dv = 3, 200, 4, 64, 64
+    mod, q, k, v, pos, g = _layer(B, N, H, dk, dv, 1)
+    q, k, v = (t.to(BF) for t in (q, k, v))
+    lengths = torch.tensor([200, 0, 131], dtype=torch.int32, device="cuda")
+    for stream in (None, torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        y, S, saved = mod.forward(q, k, v, pos, lengths=lengths, stream=stream)
+        grads = mod.backward(saved, torch.ones_like(y), stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.isfinite(t).all() for t in (y, S, *grads))
+        assert (grads[0][1] == 0).all() and (grads[0][2, 131:] == 0).all()
