@@ -18,13 +18,6 @@
 namespace lfa {
 namespace {
 
-// r exp(x), rounded once for x near 0 and to a relative few 2^-24 everywhere
-struct Decay {
-  float em, mul;
-  __device__ explicit Decay(float x) : em(x > -0.5f ? expm1f(x) : 0.f), mul(x > -0.5f ? 1.f : expf(x)) {}
-  __device__ __forceinline__ float operator()(float r) const { return fmaf(em, r, mul * r); }
-};
-
 // ---- CUDA-core run (fp32 arithmetic throughout) ------------------------------------------------------
 constexpr int kCC = 32;          // tokens per step
 constexpr int kCB = 64;          // columns of Z a CTA takes
@@ -60,12 +53,6 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float4 v
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-__device__ __forceinline__ int unit_length(const DecayArgs& a, int b) {
-  if (!a.lengths) return a.N;
-  const int l = a.lengths[b];
-  return l < 0 ? 0 : (l > a.N ? a.N : l);
-}
-
 // grid: (units, column slices, jobs)
 template <typename T>
 __global__ void __launch_bounds__(kCT) k_decay_core(const __grid_constant__ DecayArgs a) {
@@ -76,7 +63,7 @@ __global__ void __launch_bounds__(kCT) k_decay_core(const __grid_constant__ Deca
   if (c0 >= jb.db) return;
   const int da = jb.da, nb = min(kCB, jb.db - c0);
   const float ld = decay_log(a.log_decay[h]);
-  const int L = unit_length(a, b);
+  const int L = unit_length(a.lengths, b, a.N);
   const T* X = static_cast<const T*>(jb.X) + b * jb.xs[0] + h * jb.xs[1];
   const T* Y = static_cast<const T*>(jb.Y) + b * jb.ys[0] + h * jb.ys[1];
   const T* Z = static_cast<const T*>(jb.Z) + b * jb.zs[0] + h * jb.zs[1] + c0;
@@ -279,7 +266,7 @@ cudaError_t run_core(const DecayArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_decay(const DecayArgs& a, int dtype, cudaStream_t st) {
-  return dtype == LFA_BF16 ? run_core<__nv_bfloat16>(a, st) : run_core<float>(a, st);
+  return dtype == LFA_BF16 ? launch_decay_tc(a, st) : run_core<float>(a, st);
 }
 
 cudaError_t launch_decay_step(const DecayStepArgs& a, int dtype, cudaStream_t st) {

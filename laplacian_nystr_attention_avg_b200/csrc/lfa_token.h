@@ -36,11 +36,17 @@ struct DecayArgs {
   int B, heads, N;
   const float* log_decay;   // [heads]
   const int* lengths;       // [B] or null
-  int segs, seg_chunks;     // segments per unit, chunks per segment
-  float* seg_state;         // segs > 1: [njobs or 2][units][segs][dk*dv] states before each segment
+  float* ws;                // device workspace
   int njobs;
   DecayJob job[3];
 };
+
+// How a call's units are cut along the sequence: segs segments of seg_chunks chunks.
+struct DecaySplit {
+  int segs, seg_chunks;
+};
+DecaySplit decay_split(int B, int heads, int N, int njobs, int dtype);
+size_t decay_workspace_floats(int B, int heads, int N, int dk, int dv, int njobs, int dtype);
 
 struct DecayStepArgs {
   int B, heads, dk, dv;
@@ -84,6 +90,8 @@ struct NormArgs {
 };
 
 cudaError_t launch_decay(const DecayArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st);
+cudaError_t decay_take_status(int* out, cudaStream_t st);
 cudaError_t launch_decay_step(const DecayStepArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t st);
 size_t norm_workspace_floats(int B, int N, int C, int G, int backward);
@@ -93,6 +101,20 @@ cudaError_t launch_norm_backward(const NormArgs& a, int dtype, cudaStream_t st);
 // ---- small device helpers shared by the two files -------------------------------------------------
 // decays below exp(-1e4) are zero to every power but 0; the bound keeps 0 * inf out of exp(n ld)
 __device__ __forceinline__ float decay_log(float ld) { return ld < -1e4f ? -1e4f : ld; }
+
+
+// r exp(x), rounded once for x near 0 and to a relative few 2^-24 everywhere
+struct Decay {
+  float em, mul;
+  __device__ explicit Decay(float x) : em(x > -0.5f ? expm1f(x) : 0.f), mul(x > -0.5f ? 1.f : expf(x)) {}
+  __device__ __forceinline__ float operator()(float r) const { return fmaf(em, r, mul * r); }
+};
+
+__device__ __forceinline__ int unit_length(const int* lengths, int b, int N) {
+  if (!lengths) return N;
+  const int l = lengths[b];
+  return l < 0 ? 0 : (l > N ? N : l);
+}
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v);

@@ -64,9 +64,9 @@ void set3(long long* to, const long long* from) { memcpy(to, from, 3 * sizeof(lo
 extern "C" {
 
 size_t lfa_decay_workspace_size(const lfa_decay_config* cfg, int backward) {
-  (void)backward;
   if (check(cfg) != LFA_OK) return 0;
-  return 256;
+  const size_t n = 4 * lfa::decay_workspace_floats(cfg->B, cfg->heads, cfg->N, cfg->dk, cfg->dv, backward ? 3 : 1, cfg->dtype);
+  return n < 256 ? 256 : (n + 255) / 256 * 256;
 }
 
 lfa_status lfa_decay_forward(const lfa_decay_config* c, const void* Q, const void* K, const void* V,
@@ -92,7 +92,7 @@ lfa_status lfa_decay_forward(const lfa_decay_config* c, const void* Q, const voi
   a.log_decay = log_decay;
   a.lengths = lengths;
   a.njobs = 1;
-  a.segs = 1;
+  a.ws = static_cast<float*>(workspace);
   j.X = Q;
   j.Y = K;
   j.Z = V;
@@ -140,7 +140,7 @@ lfa_status lfa_decay_backward(const lfa_decay_config* c, const void* Q, const vo
   a.log_decay = log_decay;
   a.lengths = lengths;
   a.njobs = 3;
-  a.segs = 1;
+  a.ws = static_cast<float*>(workspace);
   for (int i = 0; i < 3; ++i) {   // dQ, dK, dV
     DecayJob& j = a.job[i];
     j.X = i == 0 ? dO : i == 1 ? V : K;
@@ -202,7 +202,9 @@ lfa_status lfa_decay_step(const lfa_decay_config* c, const void* q, const void* 
 }
 
 lfa_status lfa_decay_status(void* stream) {
-  return cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) == cudaSuccess ? LFA_OK : LFA_ERR_CUDA;
+  int status = 0;
+  if (lfa::decay_take_status(&status, static_cast<cudaStream_t>(stream)) != cudaSuccess) return LFA_ERR_CUDA;
+  return status ? LFA_ERR_TIMEOUT : LFA_OK;
 }
 
 lfa_status lfa_rotary(const lfa_rotary_config* c, const void* x, const void* x2, const int* positions,
