@@ -7,8 +7,8 @@
 //   Oz = P z,  Ox = x bf16(R)               (M 128, N db; K 128 and K da)
 //   O  = Oz + c_inter l^i Ox                (epilogue warps, fp32, rounded once)
 //   D  = (y c_state l^(n-j))^T z            (M da, N db, K 128 tokens), R' = l^n R + D   (state warps)
-// The decayed rows of y enter as two bf16 parts (value and remainder, two products), so that D is within about
-// 2^-17; D starts from zero in every chunk and is added to R by CUDA cores, since tensor-core accumulation
+// The decayed rows of y enter as three bf16 parts (value and remainders, three products), which hold all 24 bits
+// of them; D starts from zero in every chunk and is added to R by CUDA cores, since tensor-core accumulation
 // truncates and would drift over thousands of chunks. All widths are padded to DP = 64 or 128 by TMA's zero fill.
 //
 // Warps: 4 for P, 8 for the state (thread = one row of R, half the columns), 4 for the epilogue, one thread each
@@ -43,6 +43,7 @@ struct TcJob {
   float* fin;
   float* local;           // state kernel: sums of each segment, [units][segs]
   int da, db, rev, trans, init_decays, fin_sub;
+  int wide;               // O's rows are whole, aligned 32-byte sectors
   float c_inter, c_intra, c_state;
 };
 struct TcArgs {
@@ -54,15 +55,17 @@ struct TcArgs {
 
 template <int DP, bool STATE>
 struct Cfg {
-  static constexpr int kTile = DP / 64 * kPanelB;          // bytes of a token tile
-  static constexpr int kStage = (STATE ? 2 : 3) * kTile;   // [x] y z
-  static constexpr int kStages = DP == 64 ? 3 : (STATE ? 2 : 1);
-  static constexpr int kOffP = kStages * kStage;
-  static constexpr int kOffHi = kOffP + (STATE ? 0 : 2 * kPanelB);
-  static constexpr int kOffLo = kOffHi + kTile;
-  static constexpr int kOffR = kOffLo + kTile;
+  static constexpr int kTile = DP / 64 * kPanelB;          // bytes of a token tile, one ring slot
+  static constexpr int kPer = STATE ? 2 : 3;               // tiles of a chunk: y, [x], z
+  static constexpr int kSlots = DP == 64 ? (STATE ? 6 : 12) : (STATE ? 6 : 5);
+  // y's decayed rows are formed in steps of kStep tokens, one 16-byte vector per state thread and part
+  static constexpr int kStep = 2048 / DP;
+  static constexpr int kSteps = kC / kStep;
+  static constexpr int kPart = kStep * DP * 2;             // bytes of one part of a step
+  static constexpr int kOffPart = kSlots * kTile;          // 2 buffers of 3 parts
+  static constexpr int kOffR = kOffPart + 6 * kPart;
   static constexpr int kOffBar = kOffR + (STATE ? 0 : DP * DP * 2);
-  static constexpr int kOffPw = kOffBar + 256;
+  static constexpr int kOffPw = kOffBar + 320;
   static constexpr int kSmem = kOffPw + 4 * (kC + 4) + 1024;   // + alignment of the base to 1024
   static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
   // warps
@@ -71,12 +74,15 @@ struct Cfg {
   static constexpr int kLoad = STATE ? 8 : 16;
   static constexpr int kMma = kLoad + 1;
   static constexpr int kThreads = 32 * (kMma + 1);
-  // tensor memory columns
+  // tensor memory columns; P (bf16 pairs) takes the first half of S's columns, row by row as S is read
   static constexpr int kTs = 0, kToz = STATE ? 0 : kC, kTox = kToz + (STATE ? 0 : DP), kTd = kTox + (STATE ? 0 : DP);
   static constexpr int kTmem = STATE ? DP : 512;
 };
-enum Bar { kFull = 0, kEmpty = 3, kSFull = 6, kPReady, kKdReady, kDFull, kRbReady, kXDone, kOFull, kOFree, kFin, kNumBars };
-static_assert(kNumBars * 8 <= 192, "barriers overlap the TMEM slot");
+enum Bar {
+  kFull = 0, kEmpty = 12, kSFull = 24, kPReady, kKdReady, kPartFree = kKdReady + 2, kDFull = kPartFree + 2, kRbReady,
+  kXDone, kOFull, kOFree, kFin, kNumBars
+};
+static_assert(kNumBars * 8 <= 304, "barriers overlap the TMEM slot");
 
 struct Waiter {
   uint64_t* bars;
@@ -108,6 +114,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// one 32-byte store (a whole sector)
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -131,25 +143,14 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
 
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffBar + 192);
-  volatile int* gave_up = reinterpret_cast<volatile int*>(sm + C::kOffBar + 200);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffBar + 304);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(sm + C::kOffBar + 308);
   float* pw = reinterpret_cast<float*>(sm + C::kOffPw);   // l^0 .. l^128
   const float ld = decay_log(a.log_decay[h]);
   const Waiter wait{bars, gave_up};
   if (t == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(bars + kFull + i, 1);
-      mbar_init(bars + kEmpty + i, 1);
-    }
-    mbar_init(bars + kSFull, 1);
-    mbar_init(bars + kPReady, 4);
-    mbar_init(bars + kKdReady, 8);
-    mbar_init(bars + kDFull, 1);
-    mbar_init(bars + kRbReady, 8);
-    mbar_init(bars + kXDone, 1);
-    mbar_init(bars + kOFull, 1);
-    mbar_init(bars + kOFree, 4);
-    mbar_init(bars + kFin, 1);
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(bars + i, i == kPReady || i == kOFree ? 4 : (i >= kKdReady && i < kPartFree) || i == kRbReady ? 8 : 1);
     mbar_init_fence();
     *gave_up = 0;
   }
@@ -165,52 +166,39 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
 
   if (warp == C::kLoad) {
     if (lane == 0) {
-      int k = 0;
-      for (; k < n; ++k) {
-        const int s = k % C::kStages;
-        if (k >= C::kStages) wait(kEmpty + s, k / C::kStages - 1);
+      const int total = n * C::kPer;
+      int g = 0;
+      for (; g < total; ++g) {   // y, [x], z of every chunk in turn, one ring slot each
+        const int s = g % C::kSlots, w = g % C::kPer;
+        if (g >= C::kSlots) wait(kEmpty + s, g / C::kSlots - 1);
         if (*gave_up) break;
-        unsigned char* st = sm + s * C::kStage;
-        const int tok = chunk(k) * kC;
-        mbar_expect_tx(bars + kFull + s, C::kStage);
-        for (int p = 0; p < DP / 64; ++p) {
-          if (!STATE) tma_load_4d(st + 2 * C::kTile + p * kPanelB, &jb.x, 64 * p, tok, h, b, bars + kFull + s);
-          tma_load_4d(st + p * kPanelB, &jb.y, 64 * p, tok, h, b, bars + kFull + s);
-          tma_load_4d(st + C::kTile + p * kPanelB, &jb.z, 64 * p, tok, h, b, bars + kFull + s);
-        }
+        const CUtensorMap* m = w == 0 ? &jb.y : w == C::kPer - 1 ? &jb.z : &jb.x;
+        mbar_expect_tx(bars + kFull + s, C::kTile);
+        for (int p = 0; p < DP / 64; ++p)
+          tma_load_4d(sm + s * C::kTile + p * kPanelB, m, 64 * p, chunk(g / C::kPer) * kC, h, b, bars + kFull + s);
       }
-      for (int i = max(0, k - C::kStages); i < k; ++i) wait.drain(kFull + i % C::kStages, i / C::kStages);
+      for (int i = max(0, g - C::kSlots); i < g; ++i) wait.drain(kFull + i % C::kSlots, i / C::kSlots);
     }
   } else if (warp == C::kMma) {
     if (lane == 0) {
-      const uint32_t base = smem_u32(sm), hi = base + C::kOffHi, lo = base + C::kOffLo, rb = base + C::kOffR,
-                     pp = base + C::kOffP;
+      const uint32_t base = smem_u32(sm), parts = base + C::kOffPart, rb = base + C::kOffR;
       constexpr uint32_t id_s = idesc(1, kC, kC, 0, 0), id_o = idesc(1, kC, DP, 0, 1), id_d = idesc(1, DP, DP, 1, 1);
       for (int k = 0; k < n; ++k) {
-        const int s = k % C::kStages;
-        const uint32_t y = base + s * C::kStage, z = y + C::kTile, x = z + C::kTile;
-        wait(kFull + s, k / C::kStages);
-        tc_fence_after();
+        const int gy = k * C::kPer, gx = gy + 1, gz = gy + C::kPer - 1;
+        const int sy = gy % C::kSlots, sx = gx % C::kSlots, sz = gz % C::kSlots;
+        const uint32_t y = base + sy * C::kTile, x = base + sx * C::kTile, z = base + sz * C::kTile;
+        const bool carry = STATE || ends || k < n - 1;
         if (!STATE) {
+          wait(kFull + sy, gy / C::kSlots);
+          wait(kFull + sx, gx / C::kSlots);
+          if (k > 0) wait(kOFull, k - 1);   // P of the chunk before has been used
+          tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk) {
             const uint32_t off = (kk >> 2) * kPanelB + (kk & 3) * 32;
             mma_bf16(tmem + C::kTs, desc_sw128(x + off, 16, 1024), desc_sw128(y + off, 16, 1024), id_s, kk > 0);
           }
           mma_commit(bars + kSFull);
-        }
-        wait(kKdReady, k);
-        tc_fence_after();
-        if (STATE || ends || k < n - 1) {
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int kk = 0; kk < kC / 16; ++kk)
-              mma_bf16(tmem + C::kTd, desc_sw128((p ? lo : hi) + kk * 2048, kPanelB, 1024),
-                       desc_sw128(z + kk * 2048, kPanelB, 1024), id_d, p + kk > 0);
-          mma_commit(bars + kDFull);
-        }
-        if (!STATE) {
           wait(kRbReady, k);
           if (k > 0) wait(kOFree, k - 1);
           tc_fence_after();
@@ -219,15 +207,34 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
             mma_bf16(tmem + C::kTox, desc_sw128(x + (kk >> 2) * kPanelB + (kk & 3) * 32, 16, 1024),
                      desc_sw128(rb + kk * 2048, DP * 128, 1024), id_o, kk > 0);
           mma_commit(bars + kXDone);
+          mma_commit(bars + kEmpty + sx);
+        }
+        wait(kFull + sz, gz / C::kSlots);
+        for (int s = 0; s < C::kSteps; ++s) {
+          const int g = k * C::kSteps + s, buf = g & 1;
+          wait(kKdReady + buf, g >> 1);
+          tc_fence_after();
+          if (carry) {
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+              for (int kk = 0; kk < C::kStep / 16; ++kk)
+                mma_bf16(tmem + C::kTd, desc_sw128(parts + (3 * buf + p) * C::kPart + kk * 2048, C::kStep * 128, 1024),
+                         desc_sw128(z + (s * C::kStep + 16 * kk) * 128, kPanelB, 1024), id_d, s + p + kk > 0);
+          }
+          mma_commit(bars + kPartFree + buf);
+        }
+        if (carry) mma_commit(bars + kDFull);
+        mma_commit(bars + kEmpty + sy);
+        if (!STATE) {
           wait(kPReady, k);
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kC / 16; ++kk)
-            mma_bf16(tmem + C::kToz, desc_sw128(pp + (kk >> 2) * kPanelB + (kk & 3) * 32, 16, 1024),
-                     desc_sw128(z + kk * 2048, kPanelB, 1024), id_o, kk > 0);
+            mma_bf16_ta(tmem + C::kToz, tmem + C::kTs + 8 * kk, desc_sw128(z + kk * 2048, kPanelB, 1024), id_o, kk > 0);
           mma_commit(bars + kOFull);
         }
-        mma_commit(bars + kEmpty + s);
+        mma_commit(bars + kEmpty + sz);
       }
       mma_commit(bars + kFin);
       wait.drain(kFin, 0);
@@ -235,32 +242,31 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   } else if (!STATE && warp < C::kS0) {
     // P warps: thread = token row i of the chunk
     const int q = warp & 3, i = 32 * q + lane;
-    unsigned char* prow = sm + C::kOffP;
-    // the other side of the diagonal blocks stays zero
-    for (int cb = 0; cb < 4; ++cb)
-      if (jb.rev ? cb < q : cb > q)
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(prow + (cb >> 1) * kPanelB + sw128(i, (cb & 1) * 4 + c)) = make_uint4(0, 0, 0, 0);
+    const uint32_t srow = tmem + C::kTs + ((uint32_t)(32 * q) << 16);
     for (int k = 0; k < n; ++k) {
       const int nv = valid(chunk(k));
       wait(kSFull, k);
-      if (k > 0) wait(kOFull, k - 1);
       tc_fence_after();
-      for (int cb = jb.rev ? q : 0; cb <= (jb.rev ? 3 : q); ++cb) {
-        float v[32];
-        tmem_ld32(tmem + C::kTs + 32 * cb + ((uint32_t)(32 * q) << 16), v);
+#pragma unroll 1
+      for (int cb = 0; cb < 4; ++cb) {
+        uint32_t w[16];
+        if (jb.rev ? cb >= q : cb <= q) {
+          float v[32];
+          tmem_ld32(srow + 32 * cb, v);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const int j = 32 * cb + c, e = jb.rev ? j - i : i - j;
-          v[c] = (e >= 0 && j < nv) ? v[c] * (jb.c_intra * pw[e & 127]) : 0.f;
+          for (int c = 0; c < 32; ++c) {
+            const int j = 32 * cb + c, e = jb.rev ? j - i : i - j;
+            v[c] = (e >= 0 && j < nv) ? v[c] * (jb.c_intra * pw[e & 127]) : 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) w[c] = pack2(v[2 * c], v[2 * c + 1]);
+        } else {   // the other side of the diagonal
+#pragma unroll
+          for (int c = 0; c < 16; ++c) w[c] = 0;
         }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(prow + (cb >> 1) * kPanelB + sw128(i, (cb & 1) * 4 + c)) =
-              make_uint4(pack2(v[8 * c], v[8 * c + 1]), pack2(v[8 * c + 2], v[8 * c + 3]),
-                         pack2(v[8 * c + 4], v[8 * c + 5]), pack2(v[8 * c + 6], v[8 * c + 7]));
+        tmem_st16(srow + 16 * cb, w);   // columns of S that this warp has read
       }
-      fence_async_smem();
+      tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + kPReady);
@@ -285,14 +291,19 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
           __syncwarp();
           if (lane == 0) mbar_arrive(bars + kOFree);
         }
+        uint32_t w[16];
 #pragma unroll
-        for (int g = 0; g < 32; g += 8) {
-          if (i < nv && c0 + g < jb.db) {
-            uint32_t w[4];
+        for (int e2 = 0; e2 < 16; ++e2) w[e2] = pack2(fmaf(f, x[2 * e2], z[2 * e2]), fmaf(f, x[2 * e2 + 1], z[2 * e2 + 1]));
+        if (i < nv) {
 #pragma unroll
-            for (int e2 = 0; e2 < 4; ++e2)
-              w[e2] = pack2(fmaf(f, x[g + 2 * e2], z[g + 2 * e2]), fmaf(f, x[g + 2 * e2 + 1], z[g + 2 * e2 + 1]));
-            *reinterpret_cast<uint4*>(row + c0 + g) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int g = 0; g < 32; g += 16) {
+            if (jb.wide && c0 + g < jb.db) {
+              st_global_32(row + c0 + g, w + g / 2);
+            } else {
+              if (c0 + g < jb.db) *reinterpret_cast<uint4*>(row + c0 + g) = make_uint4(w[g / 2], w[g / 2 + 1], w[g / 2 + 2], w[g / 2 + 3]);
+              if (c0 + g + 8 < jb.db)
+                *reinterpret_cast<uint4*>(row + c0 + g + 8) = make_uint4(w[g / 2 + 4], w[g / 2 + 5], w[g / 2 + 6], w[g / 2 + 7]);
+            }
           }
         }
       }
@@ -331,40 +342,8 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       tc_fence_before();
     };
     for (int k = 0; k < n; ++k) {
-      const int c = chunk(k), nv = valid(c), s = k % C::kStages, sub = (!STATE && c == nch - 1) ? jb.fin_sub : 0;
+      const int c = chunk(k), nv = valid(c), sub = (!STATE && c == nch - 1) ? jb.fin_sub : 0;
       if (k > 0) update(k - 1);
-      wait(kFull + s, k / C::kStages);
-      unsigned char* y = sm + s * C::kStage;
-      constexpr int CH = DP / 8, RS = 256 / CH;   // 16-byte chunks per row, rows per pass
-      const int ch = ts % CH;
-      const uint32_t poff = (ch >> 3) * kPanelB;
-#pragma unroll 4
-      for (int i = 0; i < kC / RS; ++i) {
-        const int r = ts / CH + i * RS;
-        const uint32_t off = poff + sw128(r, ch & 7);
-        const uint4 v = *reinterpret_cast<const uint4*>(y + off);
-        uint4 vh = make_uint4(0, 0, 0, 0), vl = vh;
-        if (r < nv) {
-          const float w = jb.c_state * pw[(jb.rev ? r + 1 : nv - r) - sub];
-          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-          uint32_t oh[4], ol[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f0 = bf_lo(in[e]) * w, f1 = bf_hi(in[e]) * w;
-            oh[e] = pack2(f0, f1);
-            ol[e] = pack2(f0 - bf_lo(oh[e]), f1 - bf_hi(oh[e]));
-          }
-          vh = make_uint4(oh[0], oh[1], oh[2], oh[3]);
-          vl = make_uint4(ol[0], ol[1], ol[2], ol[3]);
-        } else {   // rows behind the sequence's end may hold anything
-          *reinterpret_cast<uint4*>(y + C::kTile + off) = make_uint4(0, 0, 0, 0);
-        }
-        *reinterpret_cast<uint4*>(sm + C::kOffHi + off) = vh;
-        *reinterpret_cast<uint4*>(sm + C::kOffLo + off) = vl;
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + kKdReady);
       if (!STATE) {
         if (k > 0) wait(kXDone, k - 1);
         if (live) {
@@ -378,6 +357,43 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + kRbReady);
+      }
+      const int gy = k * C::kPer, gz = gy + C::kPer - 1;
+      unsigned char* y = sm + (gy % C::kSlots) * C::kTile;
+      unsigned char* z = sm + (gz % C::kSlots) * C::kTile;
+      wait(kFull + gy % C::kSlots, gy / C::kSlots);
+      if (nv < kC) wait(kFull + gz % C::kSlots, gz / C::kSlots);
+      constexpr int CH = DP / 8;   // 16-byte vectors of a row
+      const int ch = ts % CH, rr = ts / CH;
+      for (int st = 0; st < C::kSteps; ++st) {
+        const int g = k * C::kSteps + st, buf = g & 1, r = st * C::kStep + rr;
+        const uint32_t off = (ch >> 3) * kPanelB + sw128(r, ch & 7);
+        const uint4 v = *reinterpret_cast<const uint4*>(y + off);
+        uint32_t o[3][4] = {};
+        if (r < nv) {
+          const float w = jb.c_state * pw[(jb.rev ? r + 1 : nv - r) - sub];
+          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float f0 = bf_lo(in[e]) * w, f1 = bf_hi(in[e]) * w;
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+              o[p][e] = pack2(f0, f1);
+              f0 -= bf_lo(o[p][e]);
+              f1 -= bf_hi(o[p][e]);
+            }
+          }
+        } else {   // rows behind the sequence's end may hold anything
+          *reinterpret_cast<uint4*>(z + off) = make_uint4(0, 0, 0, 0);
+        }
+        if (g >= 2) wait(kPartFree + buf, (g >> 1) - 1);
+        unsigned char* d = sm + C::kOffPart + 3 * buf * C::kPart + (ch >> 3) * (C::kStep * 128) + sw128(rr, ch & 7);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(d + p * C::kPart) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + kKdReady + buf);
       }
     }
     if (STATE || ends) {
@@ -556,6 +572,7 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
     o.init = j.init;
     o.seg_init = a.ws + (i == 0 ? 0 : states);
     o.fin = j.fin;
+    o.wide = j.db % 16 == 0 && (reinterpret_cast<uintptr_t>(j.O) & 31u) == 0 && (j.os[0] | j.os[1] | j.os[2]) % 16 == 0;
     o.da = j.da;
     o.db = j.db;
     o.rev = j.rev;
