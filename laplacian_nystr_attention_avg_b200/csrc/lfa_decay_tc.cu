@@ -7,13 +7,14 @@
 //   Oz = P z,  Ox = x bf16(R)               (M 128, N db; K 128 and K da)
 //   O  = Oz + c_inter l^i Ox                (epilogue warps, fp32, rounded once)
 //   D  = (y c_state l^(n-j))^T z            (M da, N db, K 128 tokens), R' = l^n R + D   (state warps)
-// The decayed rows of y enter as three bf16 parts (value and remainders, three products), which hold all 24 bits
-// of them; D starts from zero in every chunk and is added to R by CUDA cores, since tensor-core accumulation
-// truncates and would drift over thousands of chunks. All widths are padded to DP = 64 or 128 by TMA's zero fill.
+// The decayed rows of y enter as bf16 parts (value and remainders, one product each): two parts (2^-17) where R
+// only meets x, whose products are rounded to bf16 anyway, three (2^-25) where the run's state is returned. D
+// starts from zero in every chunk and is added to R by CUDA cores: tensor-core accumulation truncates and would
+// drift over thousands of chunks. All widths are padded to DP = 64 or 128 by TMA's zero fill.
 //
-// Warps: 4 for P, 8 for the state (thread = one row of R, half the columns), 4 for the epilogue, one thread each
-// to issue TMA loads and tensor-core products. Every hand-over is an mbarrier; every wait is bounded (on expiry
-// the device's status word is set, the CTA stops waiting for anything and drains what it has in flight).
+// Warps: 4 for P, 4 for y's decayed rows, 8 for R and the epilogue, one thread each to issue TMA loads and
+// tensor-core products. Every hand-over is an mbarrier; every wait is bounded (on expiry the device's status
+// word is set, the CTA stops waiting for anything and drains what it has in flight).
 //
 // Few units over long sequences: segments run at once. k_decay_tc<.., true> sums up each segment's own
 // state, k_decay_prefix carries them over the segments, and the main kernel starts every segment from its state.
@@ -44,6 +45,7 @@ struct TcJob {
   float* local;           // state kernel: sums of each segment, [units][segs]
   int da, db, rev, trans, init_decays, fin_sub;
   int wide;               // O's rows are whole, aligned 32-byte sectors
+  int parts;              // bf16 parts of y's decayed rows: 3 where a state is returned, else 2
   float c_inter, c_intra, c_state;
 };
 struct TcArgs {
@@ -57,30 +59,34 @@ template <int DP, bool STATE>
 struct Cfg {
   static constexpr int kTile = DP / 64 * kPanelB;          // bytes of a token tile, one ring slot
   static constexpr int kPer = STATE ? 2 : 3;               // tiles of a chunk: y, [x], z
-  static constexpr int kSlots = DP == 64 ? (STATE ? 6 : 12) : (STATE ? 6 : 5);
-  // y's decayed rows are formed in steps of kStep tokens, one 16-byte vector per state thread and part
-  static constexpr int kStep = 2048 / DP;
+  static constexpr int kSlots = DP == 64 ? (STATE ? 8 : 9) : (STATE ? 5 : 4);
+  // y's decayed rows are formed in steps of kStep tokens: four 16-byte vectors per thread
+  static constexpr int kStep = 4096 / DP;
   static constexpr int kSteps = kC / kStep;
   static constexpr int kPart = kStep * DP * 2;             // bytes of one part of a step
   static constexpr int kOffPart = kSlots * kTile;          // 2 buffers of 3 parts
   static constexpr int kOffR = kOffPart + 6 * kPart;
   static constexpr int kOffBar = kOffR + (STATE ? 0 : DP * DP * 2);
   static constexpr int kOffPw = kOffBar + 320;
-  static constexpr int kSmem = kOffPw + 4 * (kC + 4) + 1024;   // + alignment of the base to 1024
+  static constexpr int kOffWt = kOffPw + 4 * (kC + 4 + 32 + kC + 32);
+  static constexpr int kSmem = kOffWt + 16 * (kC + 1) + 1024;   // + alignment of the base to 1024
   static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
-  // warps
-  static constexpr int kS0 = STATE ? 0 : 4;   // state warps (the P warps come before them)
-  static constexpr int kE0 = kS0 + 8;
-  static constexpr int kLoad = STATE ? 8 : 16;
+  // warps: 4 for P (not STATE), 4 for y's decayed rows, 8 for the state and the epilogue, loads, products
+  static constexpr int kY0 = STATE ? 0 : 4;
+  static constexpr int kR0 = kY0 + 4;
+  static constexpr int kLoad = kR0 + 8;
   static constexpr int kMma = kLoad + 1;
   static constexpr int kThreads = 32 * (kMma + 1);
+  // 576 threads have 96 registers each; with 64 of them R, the state warps take 24 more from the P warps (16 each)
+  // and the y warps (32 each): 128 (80 + 64) + 256 120 + 64 96 = 576 96
+  static constexpr bool kSplitRegs = DP == 128 && !STATE;
   // tensor memory columns; P (bf16 pairs) takes the first half of S's columns, row by row as S is read
   static constexpr int kTs = 0, kToz = STATE ? 0 : kC, kTox = kToz + (STATE ? 0 : DP), kTd = kTox + (STATE ? 0 : DP);
   static constexpr int kTmem = STATE ? DP : 512;
 };
 enum Bar {
-  kFull = 0, kEmpty = 12, kSFull = 24, kPReady, kKdReady, kPartFree = kKdReady + 2, kDFull = kPartFree + 2, kRbReady,
-  kXDone, kOFull, kOFree, kFin, kNumBars
+  kFull = 0, kEmpty = 9, kSFull = 18, kPReady, kYdReady, kPartFree = kYdReady + 2, kDFull = kPartFree + 2, kDRead,
+  kRbReady, kXDone, kOFull, kOFree, kFin, kNumBars
 };
 static_assert(kNumBars * 8 <= 304, "barriers overlap the TMEM slot");
 
@@ -114,6 +120,19 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// y w for a pair y of bf16 and w = w.x + w.y + w.z in bf16 parts, as a + b + c in bf16: a = y w.x rounded, its
+// remainder y w.x - a is a bf16 itself (8 by 8 bits make 16), and so on down; about 2^-25 of y w is left out
+__device__ __forceinline__ __nv_bfloat162 as_b2(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); }
+__device__ __forceinline__ uint32_t as_u(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+__device__ __forceinline__ void split3(uint32_t y, const uint4& w, uint32_t& a, uint32_t& b, uint32_t& c) {
+  const __nv_bfloat162 y2 = as_b2(y), wx = as_b2(w.x), wy = as_b2(w.y), wz = as_b2(w.z);
+  const __nv_bfloat162 hi = __hmul2(y2, wx), rem = __hfma2(y2, wx, __hneg2(hi));
+  const __nv_bfloat162 mid = __hfma2(y2, wy, rem);
+  a = as_u(hi);
+  b = as_u(mid);
+  c = as_u(__hfma2(y2, wz, __hfma2(y2, wy, __hsub2(rem, mid))));
+}
+
 // one 32-byte store (a whole sector)
 __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
@@ -121,7 +140,67 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
                : "memory");
 }
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// The P warps of a run of n chunks: P = c_intra l^|i-j| S on the causal side, in bf16, over S's own columns
+// (thread = token row i; block cb of S's columns is read before P's block cb goes over columns read earlier).
+// l^|i-j| is l^(distance of i to the block) pb[c] beside the diagonal block. nv0: valid tokens of the first chunk,
+// where a reverse run finds its sequence's ragged end (forwards, columns behind the end are above the diagonal).
+template <bool REV>
+__device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bars, uint32_t ts, const float* pw,
+                                        const float* pb, int nv0) {
+  const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, i = 32 * q + lane;
+  const uint32_t srow = ts + ((uint32_t)(32 * q) << 16);
+  const float* pd = pw + (REV ? -lane : lane);   // pw is zero for 31 exponents below 0
+  for (int k = 0; k < n; ++k) {
+    wait(kSFull, k);
+    tc_fence_after();
+#pragma unroll 1
+    for (int cb = 0; cb < 4; ++cb) {
+      uint32_t w[16];
+      if (REV ? cb >= q : cb <= q) {
+        uint32_t v[32];
+        tmem_ld32_async(srow + 32 * cb, v);
+        if (cb == q) {
+          float p[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) p[c] = pd[REV ? c : -c];
+          tmem_wait_ld(v);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float x = __uint_as_float(v[c]) * p[c];
+            v[c] = (REV ? c >= lane : c <= lane) ? __float_as_uint(x) : 0u;
+          }
+        } else {
+          const float f = pw[REV ? 32 * cb - i : i - 32 * cb - 31];
+          tmem_wait_ld(v);
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 p = *reinterpret_cast<const float4*>(pb + c);
+            v[c] = __float_as_uint(__uint_as_float(v[c]) * (f * p.x));
+            v[c + 1] = __float_as_uint(__uint_as_float(v[c + 1]) * (f * p.y));
+            v[c + 2] = __float_as_uint(__uint_as_float(v[c + 2]) * (f * p.z));
+            v[c + 3] = __float_as_uint(__uint_as_float(v[c + 3]) * (f * p.w));
+          }
+        }
+        if (REV && k == 0 && nv0 < 32 * cb + 32) {   // columns of tokens behind the end may hold anything
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (32 * cb + c >= nv0) v[c] = 0;
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) w[c] = pack2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+      } else {   // the other side of the diagonal
+#pragma unroll
+        for (int c = 0; c < 16; ++c) w[c] = 0;
+      }
+      tmem_st16(srow + 16 * cb, w);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + kPReady);
+  }
+}
 
 template <int DP, bool STATE>
 __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const __grid_constant__ TcArgs a) {
@@ -132,36 +211,53 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   const int L = unit_length(a.lengths, b, a.N), nch = (L + kC - 1) / kC;
   const int c_lo = seg * a.seg_chunks, c_hi = min(c_lo + a.seg_chunks, nch), n = c_hi - c_lo;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const size_t dd = (size_t)jb.da * jb.db;
+  const int da = jb.da, db = jb.db;
+  const bool rev = jb.rev;
+  const size_t dd = (size_t)da * db;
   if (n <= 0) {
     if (!STATE && L == 0 && seg == 0 && jb.fin)
       for (size_t e = t; e < dd; e += C::kThreads) jb.fin[u * dd + e] = jb.init ? jb.init[u * dd + e] : 0.f;
     return;
   }
-  if (STATE && (jb.rev ? seg == 0 : c_hi == nch)) return;   // nothing follows this segment
-  const bool ends = !STATE && jb.fin && (jb.rev ? seg == 0 : c_hi == nch);
+  if (STATE && (rev ? seg == 0 : c_hi == nch)) return;   // nothing follows this segment
+  const bool ends = !STATE && jb.fin && (rev ? seg == 0 : c_hi == nch);
 
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffBar + 304);
   volatile int* gave_up = reinterpret_cast<volatile int*>(sm + C::kOffBar + 308);
   float* pw = reinterpret_cast<float*>(sm + C::kOffPw);   // l^0 .. l^128
+  float* pb = pw + kC + 4;                                 // rev: l^c, else l^(31-c), c = 0 .. 31
+  float* pi = pb + 32 + 32;                                // c_intra l^0 .. c_intra l^127 after 32 zeros
+  uint4* wt = reinterpret_cast<uint4*>(sm + C::kOffWt);   // c_state l^n as three bf16 parts, each twice in a word
   const float ld = decay_log(a.log_decay[h]);
   const Waiter wait{bars, gave_up};
   if (t == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bars + i, i == kPReady || i == kOFree ? 4 : (i >= kKdReady && i < kPartFree) || i == kRbReady ? 8 : 1);
+      mbar_init(bars + i, i == kPReady || (i >= kYdReady && i < kPartFree) ? 4
+                          : i == kDRead || i == kRbReady || i == kOFree    ? 8
+                                                                           : 1);
     mbar_init_fence();
     *gave_up = 0;
   }
   if (warp == C::kMma) tmem_alloc(tmem_slot, C::kTmem);
-  for (int i = t; i <= kC; i += C::kThreads) pw[i] = expf(ld * i);
+  for (int i = t; i <= kC; i += C::kThreads) {
+    const float w = expf(ld * i);
+    pw[i] = w;
+    if (i < 32) {
+      pb[rev ? i : 31 - i] = w;
+      pi[i - 32] = 0.f;
+    }
+    if (i < kC) pi[i] = jb.c_intra * w;
+    const float f = jb.c_state * w, f1 = f - bf_lo(pack2(f, f)), f2 = f1 - bf_lo(pack2(f1, f1));
+    wt[i] = make_uint4(pack2(f, f), pack2(f1, f1), pack2(f2, f2), 0u);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // chunk of step k, and its valid tokens
-  auto chunk = [&](int k) { return jb.rev ? c_hi - 1 - k : c_lo + k; };
+  auto chunk = [&](int k) { return rev ? c_hi - 1 - k : c_lo + k; };
   auto valid = [&](int c) { return min(kC, L - c * kC); };
 
   if (warp == C::kLoad) {
@@ -181,12 +277,17 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
     }
   } else if (warp == C::kMma) {
     if (lane == 0) {
-      const uint32_t base = smem_u32(sm), parts = base + C::kOffPart, rb = base + C::kOffR;
+      // descriptors of the ring's first slot, R and the parts; an offset of b bytes adds b / 16
+      const uint32_t base = smem_u32(sm);
+      const uint64_t d_k = desc_sw128(base, 16, 1024), d_mn = desc_sw128(base, kPanelB, 1024),
+                     d_rb = desc_sw128(base + C::kOffR, DP * 128, 1024),
+                     d_part = desc_sw128(base + C::kOffPart, C::kStep * 128, 1024);
       constexpr uint32_t id_s = idesc(1, kC, kC, 0, 0), id_o = idesc(1, kC, DP, 0, 1), id_d = idesc(1, DP, DP, 1, 1);
+      const bool third = jb.parts == 3;
       for (int k = 0; k < n; ++k) {
         const int gy = k * C::kPer, gx = gy + 1, gz = gy + C::kPer - 1;
         const int sy = gy % C::kSlots, sx = gx % C::kSlots, sz = gz % C::kSlots;
-        const uint32_t y = base + sy * C::kTile, x = base + sx * C::kTile, z = base + sz * C::kTile;
+        const uint64_t y = d_k + sy * (C::kTile / 16), x = d_k + sx * (C::kTile / 16), z = d_mn + sz * (C::kTile / 16);
         const bool carry = STATE || ends || k < n - 1;
         if (!STATE) {
           wait(kFull + sy, gy / C::kSlots);
@@ -195,43 +296,46 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kPanelB + (kk & 3) * 32;
-            mma_bf16(tmem + C::kTs, desc_sw128(x + off, 16, 1024), desc_sw128(y + off, 16, 1024), id_s, kk > 0);
+            const int off = ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16;
+            mma_bf16(tmem + C::kTs, x + off, y + off, id_s, kk > 0);
           }
           mma_commit(bars + kSFull);
-          wait(kRbReady, k);
-          if (k > 0) wait(kOFree, k - 1);
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            mma_bf16(tmem + C::kTox, desc_sw128(x + (kk >> 2) * kPanelB + (kk & 3) * 32, 16, 1024),
-                     desc_sw128(rb + kk * 2048, DP * 128, 1024), id_o, kk > 0);
-          mma_commit(bars + kXDone);
-          mma_commit(bars + kEmpty + sx);
         }
         wait(kFull + sz, gz / C::kSlots);
+        if (k > 0) wait(kDRead, k - 1);
+#pragma unroll 1
         for (int s = 0; s < C::kSteps; ++s) {
           const int g = k * C::kSteps + s, buf = g & 1;
-          wait(kKdReady + buf, g >> 1);
+          wait(kYdReady + buf, g >> 1);
           tc_fence_after();
           if (carry) {
 #pragma unroll
             for (int p = 0; p < 3; ++p)
+              if (p < 2 || third) {
 #pragma unroll
-              for (int kk = 0; kk < C::kStep / 16; ++kk)
-                mma_bf16(tmem + C::kTd, desc_sw128(parts + (3 * buf + p) * C::kPart + kk * 2048, C::kStep * 128, 1024),
-                         desc_sw128(z + (s * C::kStep + 16 * kk) * 128, kPanelB, 1024), id_d, s + p + kk > 0);
+                for (int kk = 0; kk < C::kStep / 16; ++kk)
+                  mma_bf16(tmem + C::kTd, d_part + (3 * buf + p) * (C::kPart / 16) + kk * 128,
+                           z + (s * C::kStep + 16 * kk) * 8, id_d, s + p + kk > 0);
+              }
           }
           mma_commit(bars + kPartFree + buf);
         }
         if (carry) mma_commit(bars + kDFull);
         mma_commit(bars + kEmpty + sy);
         if (!STATE) {
+          wait(kRbReady, k);
+          if (k > 0) wait(kOFree, k - 1);
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < DP / 16; ++kk)
+            mma_bf16(tmem + C::kTox, x + ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16, d_rb + kk * 128, id_o, kk > 0);
+          mma_commit(bars + kXDone);
+          mma_commit(bars + kEmpty + sx);
           wait(kPReady, k);
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kC / 16; ++kk)
-            mma_bf16_ta(tmem + C::kToz, tmem + C::kTs + 8 * kk, desc_sw128(z + kk * 2048, kPanelB, 1024), id_o, kk > 0);
+            mma_bf16_ta(tmem + C::kToz, tmem + C::kTs + 8 * kk, z + kk * 128, id_o, kk > 0);
           mma_commit(bars + kOFull);
         }
         mma_commit(bars + kEmpty + sz);
@@ -239,92 +343,77 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       mma_commit(bars + kFin);
       wait.drain(kFin, 0);
     }
-  } else if (!STATE && warp < C::kS0) {
-    // P warps: thread = token row i of the chunk
-    const int q = warp & 3, i = 32 * q + lane;
-    const uint32_t srow = tmem + C::kTs + ((uint32_t)(32 * q) << 16);
+  } else if (!STATE && warp < C::kY0) {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (rev)
+      weights<true>(n, wait, bars, tmem + C::kTs, pi, pb, L - (c_hi - 1) * kC);
+    else
+      weights<false>(n, wait, bars, tmem + C::kTs, pi, pb, kC);
+  } else if (warp < C::kR0) {
+    // y's decayed rows, in steps of kStep tokens into one of two buffers
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    const int ty = t - 32 * C::kY0;
+    constexpr int CH = DP / 8, RS = 128 / CH;   // 16-byte vectors of a row, rows per pass
+    const int ch = ty % CH, rr = ty / CH;
+    const bool third = jb.parts == 3;
     for (int k = 0; k < n; ++k) {
-      const int nv = valid(chunk(k));
-      wait(kSFull, k);
-      tc_fence_after();
+      const int c = chunk(k), nv = valid(c), sub = (!STATE && c == nch - 1) ? jb.fin_sub : 0;
+      const int gy = k * C::kPer, gz = gy + C::kPer - 1;
+      const unsigned char* y = sm + (gy % C::kSlots) * C::kTile + (ch >> 3) * kPanelB;
+      unsigned char* z = sm + (gz % C::kSlots) * C::kTile + (ch >> 3) * kPanelB;
+      const uint4* w0 = wt + (rev ? 1 : nv) - sub;   // row r has weight w0[r] (rev) or w0[-r]
+      wait(kFull + gy % C::kSlots, gy / C::kSlots);
+      if (nv < kC) wait(kFull + gz % C::kSlots, gz / C::kSlots);
 #pragma unroll 1
-      for (int cb = 0; cb < 4; ++cb) {
-        uint32_t w[16];
-        if (jb.rev ? cb >= q : cb <= q) {
-          float v[32];
-          tmem_ld32(srow + 32 * cb, v);
+      for (int st = 0; st < C::kSteps; ++st) {
+        const int g = k * C::kSteps + st, buf = g & 1;
+        uint4 v[4];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int j = 32 * cb + c, e = jb.rev ? j - i : i - j;
-            v[c] = (e >= 0 && j < nv) ? v[c] * (jb.c_intra * pw[e & 127]) : 0.f;
+        for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const uint4*>(y + sw128(st * C::kStep + rr + e * RS, ch & 7));
+        if (g >= 2) wait(kPartFree + buf, (g >> 1) - 1);
+        unsigned char* d = sm + C::kOffPart + 3 * buf * C::kPart + (ch >> 3) * (C::kStep * 128);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = st * C::kStep + rr + e * RS;
+          uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0, o2 = o0;
+          if (r < nv) {
+            const uint4 w = w0[rev ? r : -r];
+            split3(v[e].x, w, o0.x, o1.x, o2.x);
+            split3(v[e].y, w, o0.y, o1.y, o2.y);
+            split3(v[e].z, w, o0.z, o1.z, o2.z);
+            split3(v[e].w, w, o0.w, o1.w, o2.w);
+          } else {   // rows behind the sequence's end may hold anything
+            *reinterpret_cast<uint4*>(z + sw128(r, ch & 7)) = make_uint4(0, 0, 0, 0);
           }
-#pragma unroll
-          for (int c = 0; c < 16; ++c) w[c] = pack2(v[2 * c], v[2 * c + 1]);
-        } else {   // the other side of the diagonal
-#pragma unroll
-          for (int c = 0; c < 16; ++c) w[c] = 0;
+          unsigned char* p = d + sw128(rr + e * RS, ch & 7);
+          *reinterpret_cast<uint4*>(p) = o0;
+          *reinterpret_cast<uint4*>(p + C::kPart) = o1;
+          if (third) *reinterpret_cast<uint4*>(p + 2 * C::kPart) = o2;
         }
-        tmem_st16(srow + 16 * cb, w);   // columns of S that this warp has read
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + kPReady);
-    }
-  } else if (!STATE && warp >= C::kE0) {
-    // epilogue: thread = token row
-    const int q = warp & 3, i = 32 * q + lane;
-    __nv_bfloat16* O = jb.O + b * jb.os[0] + h * jb.os[1];
-    for (int k = 0; k < n; ++k) {
-      const int c = chunk(k), nv = valid(c), e = jb.rev ? nv - 1 - i : i;
-      const float f = e >= 0 ? jb.c_inter * pw[e] : 0.f;
-      wait(kOFull, k);
-      tc_fence_after();
-      __nv_bfloat16* row = O + (long long)(c * kC + i) * jb.os[2];
-#pragma unroll 1
-      for (int c0 = 0; c0 < DP; c0 += 32) {
-        float z[32], x[32];
-        tmem_ld32(tmem + C::kToz + c0 + ((uint32_t)(32 * q) << 16), z);
-        tmem_ld32(tmem + C::kTox + c0 + ((uint32_t)(32 * q) << 16), x);
-        if (c0 + 32 >= DP) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars + kOFree);
-        }
-        uint32_t w[16];
-#pragma unroll
-        for (int e2 = 0; e2 < 16; ++e2) w[e2] = pack2(fmaf(f, x[2 * e2], z[2 * e2]), fmaf(f, x[2 * e2 + 1], z[2 * e2 + 1]));
-        if (i < nv) {
-#pragma unroll
-          for (int g = 0; g < 32; g += 16) {
-            if (jb.wide && c0 + g < jb.db) {
-              st_global_32(row + c0 + g, w + g / 2);
-            } else {
-              if (c0 + g < jb.db) *reinterpret_cast<uint4*>(row + c0 + g) = make_uint4(w[g / 2], w[g / 2 + 1], w[g / 2 + 2], w[g / 2 + 3]);
-              if (c0 + g + 8 < jb.db)
-                *reinterpret_cast<uint4*>(row + c0 + g + 8) = make_uint4(w[g / 2 + 4], w[g / 2 + 5], w[g / 2 + 6], w[g / 2 + 7]);
-            }
-          }
-        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + kYdReady + buf);
       }
     }
-  } else if (warp >= C::kS0 && warp < C::kE0) {
-    // state warps: R row and half of its columns per thread (DP 64: M = 64 puts row 16 q + lane in lane < 16)
+  } else if (warp < C::kLoad) {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+    // state and epilogue: R row and half of its columns per thread (DP 64: M = 64 puts row 16 q + lane in
+    // lane < 16); in the epilogue thread = token row, the same half of O's columns
     constexpr int NR = DP / 2;
-    const int ts = t - 32 * C::kS0, q = warp & 3, half = (warp - C::kS0) >> 2;
-    const bool live = DP == 128 || lane < 16;
-    const int row = DP == 128 ? 32 * q + lane : 16 * q + lane, col = half * NR;
+    const int q = warp & 3, half = (warp - C::kR0) >> 2, i = 32 * q + lane;
+    const bool live = DP == 128 || lane < 16, trans = jb.trans;
+    const int row = DP == 128 ? i : 16 * q + lane, col = half * NR;
+    const uint32_t quad = tmem + ((uint32_t)(32 * q) << 16) + col;
     float R[NR];
     {
-      const float* src = a.segs > 1 ? jb.seg_init : jb.init;
-      if (STATE) src = nullptr;
+      const float* src = STATE ? nullptr : a.segs > 1 ? jb.seg_init : jb.init;
       const float f0 = (a.segs > 1 || !jb.init_decays) ? 1.f : expf(ld);
       const size_t at = (a.segs > 1 ? (size_t)u * a.segs + seg : (size_t)u) * dd;
 #pragma unroll
       for (int c = 0; c < NR; ++c) {
         R[c] = 0.f;
-        if (src && live && row < jb.da && col + c < jb.db)
-          R[c] = f0 * src[at + (jb.trans ? (size_t)(col + c) * jb.da + row : (size_t)row * jb.db + col + c)];
+        if (src && live && row < da && col + c < db)
+          R[c] = f0 * src[at + (trans ? (size_t)(col + c) * da + row : (size_t)row * db + col + c)];
       }
     }
     auto update = [&](int k) {   // R after the chunk of step k
@@ -333,16 +422,57 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       wait(kDFull, k);
       tc_fence_after();
 #pragma unroll
-      for (int c0 = 0; c0 < NR; c0 += 32) {
-        float d[32];
-        tmem_ld32(tmem + C::kTd + col + c0 + ((uint32_t)(32 * q) << 16), d);
+      for (int c0 = 0; c0 < NR; c0 += 16) {
+        float d[16];
+        tmem_ld16(quad + C::kTd + c0, d);
+        if (c0 + 16 == NR) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + kDRead);
+        }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) R[c0 + e] = dec(R[c0 + e]) + d[e];
+        for (int e = 0; e < 16; ++e) R[c0 + e] = dec(R[c0 + e]) + d[e];
       }
-      tc_fence_before();
+    };
+    const long long ts = jb.os[2];
+    __nv_bfloat16* O = STATE ? nullptr : jb.O + b * jb.os[0] + h * jb.os[1] + col;
+    const bool wide = jb.wide;
+    const float c_inter = jb.c_inter;
+    auto epilogue = [&](int k) {
+      const int c = chunk(k), nv = valid(c), e = rev ? nv - 1 - i : i;
+      const float f = e >= 0 ? c_inter * pw[e] : 0.f;
+      wait(kOFull, k);
+      tc_fence_after();
+      __nv_bfloat16* o = O + (long long)(c * kC + i) * ts;
+#pragma unroll 1
+      for (int c0 = 0; c0 < NR; c0 += 16) {
+        uint32_t z[16], x[16];
+        tmem_ld16_async(quad + C::kToz + c0, z);
+        tmem_ld16_async(quad + C::kTox + c0, x);
+        tmem_wait_ld16(z);
+        tmem_wait_ld16(x);
+        if (c0 + 16 == NR) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + kOFree);
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+          w[g] = pack2(fmaf(f, __uint_as_float(x[2 * g]), __uint_as_float(z[2 * g])),
+                       fmaf(f, __uint_as_float(x[2 * g + 1]), __uint_as_float(z[2 * g + 1])));
+        if (i < nv) {
+          const int left = db - col - c0;
+          if (wide && left > 0) {
+            st_global_32(o + c0, w);
+          } else {
+            if (left > 0) *reinterpret_cast<uint4*>(o + c0) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (left > 8) *reinterpret_cast<uint4*>(o + c0 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+      }
     };
     for (int k = 0; k < n; ++k) {
-      const int c = chunk(k), nv = valid(c), sub = (!STATE && c == nch - 1) ? jb.fin_sub : 0;
       if (k > 0) update(k - 1);
       if (!STATE) {
         if (k > 0) wait(kXDone, k - 1);
@@ -357,53 +487,17 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + kRbReady);
-      }
-      const int gy = k * C::kPer, gz = gy + C::kPer - 1;
-      unsigned char* y = sm + (gy % C::kSlots) * C::kTile;
-      unsigned char* z = sm + (gz % C::kSlots) * C::kTile;
-      wait(kFull + gy % C::kSlots, gy / C::kSlots);
-      if (nv < kC) wait(kFull + gz % C::kSlots, gz / C::kSlots);
-      constexpr int CH = DP / 8;   // 16-byte vectors of a row
-      const int ch = ts % CH, rr = ts / CH;
-      for (int st = 0; st < C::kSteps; ++st) {
-        const int g = k * C::kSteps + st, buf = g & 1, r = st * C::kStep + rr;
-        const uint32_t off = (ch >> 3) * kPanelB + sw128(r, ch & 7);
-        const uint4 v = *reinterpret_cast<const uint4*>(y + off);
-        uint32_t o[3][4] = {};
-        if (r < nv) {
-          const float w = jb.c_state * pw[(jb.rev ? r + 1 : nv - r) - sub];
-          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float f0 = bf_lo(in[e]) * w, f1 = bf_hi(in[e]) * w;
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
-              o[p][e] = pack2(f0, f1);
-              f0 -= bf_lo(o[p][e]);
-              f1 -= bf_hi(o[p][e]);
-            }
-          }
-        } else {   // rows behind the sequence's end may hold anything
-          *reinterpret_cast<uint4*>(z + off) = make_uint4(0, 0, 0, 0);
-        }
-        if (g >= 2) wait(kPartFree + buf, (g >> 1) - 1);
-        unsigned char* d = sm + C::kOffPart + 3 * buf * C::kPart + (ch >> 3) * (C::kStep * 128) + sw128(rr, ch & 7);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(d + p * C::kPart) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
-        fence_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + kKdReady + buf);
+        if (k > 0) epilogue(k - 1);
       }
     }
+    if (!STATE) epilogue(n - 1);
     if (STATE || ends) {
       update(n - 1);
       float* dst = STATE ? jb.local + ((size_t)u * a.segs + seg) * dd : jb.fin + u * dd;
-      const bool tr = !STATE && jb.trans;
-      if (live && row < jb.da) {
+      if (live && row < da) {
 #pragma unroll
         for (int c = 0; c < NR; ++c)
-          if (col + c < jb.db) dst[tr ? (size_t)(col + c) * jb.da + row : (size_t)row * jb.db + col + c] = R[c];
+          if (col + c < db) dst[!STATE && trans ? (size_t)(col + c) * da + row : (size_t)row * db + col + c] = R[c];
       }
     }
   }
@@ -546,6 +640,7 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
       o.rev = j.rev;
       o.c_state = j.c_state;
       o.local = a.ws + i * states;
+      o.parts = j.fin ? 3 : 2;
       p.init[i] = j.init;
       p.rev[i] = j.rev;
       p.init_decays[i] = j.init_decays;
@@ -579,6 +674,7 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
     o.trans = j.trans;
     o.init_decays = j.init_decays;
     o.fin_sub = j.fin_sub;
+    o.parts = j.fin ? 3 : 2;
     o.c_inter = j.c_inter;
     o.c_intra = j.c_intra;
     o.c_state = j.c_state;
