@@ -12,8 +12,8 @@
 // starts from zero in every chunk and is added to R by CUDA cores: tensor-core accumulation truncates and would
 // drift over thousands of chunks. All widths are padded to DP = 64 or 128 by TMA's zero fill.
 //
-// Warps: 4 for P, 4 for y's decayed rows, 8 for R and the epilogue, one thread each to issue TMA loads and
-// tensor-core products. Every hand-over is an mbarrier; every wait is bounded (on expiry the device's status
+// Warps: 4 for P, 4 for y's decayed rows, 8 for R and the epilogue, one thread each to issue TMA loads, the products
+// of the state and those of the output. Every hand-over is an mbarrier; every wait is bounded (on expiry the device's status
 // word is set, the CTA stops waiting for anything and drains what it has in flight).
 //
 // Few units over long sequences: segments run at once. k_decay_tc<.., true> sums up each segment's own
@@ -71,14 +71,15 @@ struct Cfg {
   static constexpr int kOffWt = kOffPw + 4 * (kC + 4 + 32 + kC + 32);
   static constexpr int kSmem = kOffWt + 16 * (kC + 1) + 1024;   // + alignment of the base to 1024
   static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
-  // warps: 4 for P (not STATE), 4 for y's decayed rows, 8 for the state and the epilogue, loads, products
+  // warps: 4 for P (not STATE), 4 for y's decayed rows, 8 for the state and the epilogue, loads, products (two)
   static constexpr int kY0 = STATE ? 0 : 4;
   static constexpr int kR0 = kY0 + 4;
   static constexpr int kLoad = kR0 + 8;
-  static constexpr int kMma = kLoad + 1;
-  static constexpr int kThreads = 32 * (kMma + 1);
-  // 576 threads have 96 registers each; with 64 of them R, the state warps take 24 more from the P warps (16 each)
-  // and the y warps (32 each): 128 (80 + 64) + 256 120 + 64 96 = 576 96
+  static constexpr int kMma = kLoad + 1;      // products of the state
+  static constexpr int kMmaO = kMma + 1;      // products of the output (not STATE)
+  static constexpr int kThreads = 32 * (STATE ? kMma + 1 : kMmaO + 1);
+  // 608 threads have 96 registers each; with 64 of them R, the state warps take 24 more from the P warps (16 each)
+  // and the y warps (32 each): 128 (80 + 64) + 256 120 + 96 96 = 608 96
   static constexpr bool kSplitRegs = DP == 128 && !STATE;
   // tensor memory columns; P (bf16 pairs) takes the first half of S's columns, row by row as S is read
   static constexpr int kTs = 0, kToz = STATE ? 0 : kC, kTox = kToz + (STATE ? 0 : DP), kTd = kTox + (STATE ? 0 : DP);
@@ -86,7 +87,7 @@ struct Cfg {
 };
 enum Bar {
   kFull = 0, kEmpty = 9, kSFull = 18, kPReady, kYdReady, kPartFree = kYdReady + 2, kDFull = kPartFree + 2, kDRead,
-  kRbReady, kXDone, kOFull, kOFree, kFin, kNumBars
+  kRbReady, kXDone, kOFull, kOFree, kZClean, kFin, kNumBars = kFin + 2
 };
 static_assert(kNumBars * 8 <= 304, "barriers overlap the TMEM slot");
 
@@ -96,7 +97,7 @@ struct Waiter {
   __device__ __forceinline__ void operator()(int bar, uint32_t phase) const {
     if (mbar_try_wait(bars + bar, phase & 1)) return;
     const long long t0 = clock64();
-    while (!mbar_try_wait(bars + bar, phase & 1)) {
+    while (!mbar_try_wait_ns(bars + bar, phase & 1, 2000)) {
       if (*gave_up) return;
       if (clock64() - t0 > kSpinBudget) {
         *gave_up = 1;
@@ -124,13 +125,30 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // remainder y w.x - a is a bf16 itself (8 by 8 bits make 16), and so on down; about 2^-25 of y w is left out
 __device__ __forceinline__ __nv_bfloat162 as_b2(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); }
 __device__ __forceinline__ uint32_t as_u(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+template <bool THIRD>
 __device__ __forceinline__ void split3(uint32_t y, const uint4& w, uint32_t& a, uint32_t& b, uint32_t& c) {
   const __nv_bfloat162 y2 = as_b2(y), wx = as_b2(w.x), wy = as_b2(w.y), wz = as_b2(w.z);
   const __nv_bfloat162 hi = __hmul2(y2, wx), rem = __hfma2(y2, wx, __hneg2(hi));
   const __nv_bfloat162 mid = __hfma2(y2, wy, rem);
   a = as_u(hi);
   b = as_u(mid);
-  c = as_u(__hfma2(y2, wz, __hfma2(y2, wy, __hsub2(rem, mid))));
+  if (THIRD) c = as_u(__hfma2(y2, wz, __hfma2(y2, wy, __hsub2(rem, mid))));
+}
+// four vectors of a thread, RS rows apart (a multiple of 8: the same place in the swizzle), each part PART bytes on
+template <bool THIRD, int RS, int PART>
+__device__ __forceinline__ void split_rows(const uint4 (&v)[4], const uint4 (&w)[4], unsigned char* d) {
+  uint4 o[4][3];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    split3<THIRD>(v[e].x, w[e], o[e][0].x, o[e][1].x, o[e][2].x);
+    split3<THIRD>(v[e].y, w[e], o[e][0].y, o[e][1].y, o[e][2].y);
+    split3<THIRD>(v[e].z, w[e], o[e][0].z, o[e][1].z, o[e][2].z);
+    split3<THIRD>(v[e].w, w[e], o[e][0].w, o[e][1].w, o[e][2].w);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int p = 0; p < (THIRD ? 3 : 2); ++p) *reinterpret_cast<uint4*>(d + e * RS * 128 + p * PART) = o[e][p];
 }
 
 // one 32-byte store (a whole sector)
@@ -139,6 +157,7 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
                "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
+__device__ __forceinline__ uint32_t packf2(uint64_t v) { return pack2(f2_lo(v), f2_hi(v)); }
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 
 // The P warps of a run of n chunks: P = c_intra l^|i-j| S on the causal side, in bf16, over S's own columns
@@ -172,14 +191,16 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
           }
         } else {
           const float f = pw[REV ? 32 * cb - i : i - 32 * cb - 31];
+          const uint64_t ff = f2(f, f);
           tmem_wait_ld(v);
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
-            const float4 p = *reinterpret_cast<const float4*>(pb + c);
-            v[c] = __float_as_uint(__uint_as_float(v[c]) * (f * p.x));
-            v[c + 1] = __float_as_uint(__uint_as_float(v[c + 1]) * (f * p.y));
-            v[c + 2] = __float_as_uint(__uint_as_float(v[c + 2]) * (f * p.z));
-            v[c + 3] = __float_as_uint(__uint_as_float(v[c + 3]) * (f * p.w));
+            const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(pb + c);
+            const uint64_t x = mul2(f2(v[c], v[c + 1]), mul2(ff, p.x)), y = mul2(f2(v[c + 2], v[c + 3]), mul2(ff, p.y));
+            v[c] = (uint32_t)x;
+            v[c + 1] = (uint32_t)(x >> 32);
+            v[c + 2] = (uint32_t)y;
+            v[c + 3] = (uint32_t)(y >> 32);
           }
         }
         if (REV && k == 0 && nv0 < 32 * cb + 32) {   // columns of tokens behind the end may hold anything
@@ -234,9 +255,10 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   const Waiter wait{bars, gave_up};
   if (t == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bars + i, i == kPReady || (i >= kYdReady && i < kPartFree) ? 4
-                          : i == kDRead || i == kRbReady || i == kOFree    ? 8
-                                                                           : 1);
+      mbar_init(bars + i, i >= kEmpty && i < kSFull                                            ? (STATE ? 1 : 2)
+                          : i == kPReady || (i >= kYdReady && i < kPartFree) || i == kZClean ? 4
+                          : i == kDRead || i == kRbReady || i == kOFree                      ? 8
+                                                                                             : 1);
     mbar_init_fence();
     *gave_up = 0;
   }
@@ -275,32 +297,61 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       }
       for (int i = max(0, g - C::kSlots); i < g; ++i) wait.drain(kFull + i % C::kSlots, i / C::kSlots);
     }
-  } else if (warp == C::kMma) {
+  } else if (!STATE && warp == C::kMmaO) {
     if (lane == 0) {
-      // descriptors of the ring's first slot, R and the parts; an offset of b bytes adds b / 16
+      // S, Ox, Oz of every chunk in turn. Descriptors of the ring's first slot and R; b bytes further is + b / 16
       const uint32_t base = smem_u32(sm);
       const uint64_t d_k = desc_sw128(base, 16, 1024), d_mn = desc_sw128(base, kPanelB, 1024),
-                     d_rb = desc_sw128(base + C::kOffR, DP * 128, 1024),
-                     d_part = desc_sw128(base + C::kOffPart, C::kStep * 128, 1024);
-      constexpr uint32_t id_s = idesc(1, kC, kC, 0, 0), id_o = idesc(1, kC, DP, 0, 1), id_d = idesc(1, DP, DP, 1, 1);
-      const bool third = jb.parts == 3;
+                     d_rb = desc_sw128(base + C::kOffR, DP * 128, 1024);
+      constexpr uint32_t id_s = idesc(1, kC, kC, 0, 0), id_o = idesc(1, kC, DP, 0, 1);
       for (int k = 0; k < n; ++k) {
         const int gy = k * C::kPer, gx = gy + 1, gz = gy + C::kPer - 1;
         const int sy = gy % C::kSlots, sx = gx % C::kSlots, sz = gz % C::kSlots;
         const uint64_t y = d_k + sy * (C::kTile / 16), x = d_k + sx * (C::kTile / 16), z = d_mn + sz * (C::kTile / 16);
-        const bool carry = STATE || ends || k < n - 1;
-        if (!STATE) {
-          wait(kFull + sy, gy / C::kSlots);
-          wait(kFull + sx, gx / C::kSlots);
-          if (k > 0) wait(kOFull, k - 1);   // P of the chunk before has been used
-          tc_fence_after();
+        wait(kFull + sy, gy / C::kSlots);
+        wait(kFull + sx, gx / C::kSlots);
+        if (k > 0) wait(kOFull, k - 1);   // P of the chunk before has been used
+        tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk) {
-            const int off = ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16;
-            mma_bf16(tmem + C::kTs, x + off, y + off, id_s, kk > 0);
-          }
-          mma_commit(bars + kSFull);
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          const int off = ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16;
+          mma_bf16(tmem + C::kTs, x + off, y + off, id_s, kk > 0);
         }
+        mma_commit(bars + kSFull);
+        mma_commit(bars + kEmpty + sy);
+        wait(kRbReady, k);
+        if (k > 0) wait(kOFree, k - 1);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_bf16(tmem + C::kTox, x + ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16, d_rb + kk * 128, id_o, kk > 0);
+        mma_commit(bars + kXDone);
+        mma_commit(bars + kEmpty + sx);
+        mma_commit(bars + kEmpty + sx);
+        wait(kFull + sz, gz / C::kSlots);
+        if (valid(chunk(k)) < kC) wait(kZClean, 0);
+        wait(kPReady, k);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kC / 16; ++kk)
+          mma_bf16_ta(tmem + C::kToz, tmem + C::kTs + 8 * kk, z + kk * 128, id_o, kk > 0);
+        mma_commit(bars + kOFull);
+        mma_commit(bars + kEmpty + sz);
+      }
+      mma_commit(bars + kFin);
+      wait.drain(kFin, 0);
+    }
+  } else if (warp == C::kMma) {
+    if (lane == 0) {
+      // D of every chunk: its own thread, so that the state runs ahead of the outputs
+      const uint32_t base = smem_u32(sm);
+      const uint64_t d_mn = desc_sw128(base, kPanelB, 1024), d_part = desc_sw128(base + C::kOffPart, C::kStep * 128, 1024);
+      constexpr uint32_t id_d = idesc(1, DP, DP, 1, 1);
+      const bool third = jb.parts == 3;
+      for (int k = 0; k < n; ++k) {
+        const int gy = k * C::kPer, gz = gy + C::kPer - 1, sy = gy % C::kSlots, sz = gz % C::kSlots;
+        const uint64_t z = d_mn + sz * (C::kTile / 16);
+        const bool carry = STATE || ends || k < n - 1;
         wait(kFull + sz, gz / C::kSlots);
         if (k > 0) wait(kDRead, k - 1);
 #pragma unroll 1
@@ -322,26 +373,10 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
         }
         if (carry) mma_commit(bars + kDFull);
         mma_commit(bars + kEmpty + sy);
-        if (!STATE) {
-          wait(kRbReady, k);
-          if (k > 0) wait(kOFree, k - 1);
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            mma_bf16(tmem + C::kTox, x + ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16, d_rb + kk * 128, id_o, kk > 0);
-          mma_commit(bars + kXDone);
-          mma_commit(bars + kEmpty + sx);
-          wait(kPReady, k);
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kC / 16; ++kk)
-            mma_bf16_ta(tmem + C::kToz, tmem + C::kTs + 8 * kk, z + kk * 128, id_o, kk > 0);
-          mma_commit(bars + kOFull);
-        }
         mma_commit(bars + kEmpty + sz);
       }
-      mma_commit(bars + kFin);
-      wait.drain(kFin, 0);
+      mma_commit(bars + kFin + 1);
+      wait.drain(kFin + 1, 0);
     }
   } else if (!STATE && warp < C::kY0) {
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -367,33 +402,34 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
 #pragma unroll 1
       for (int st = 0; st < C::kSteps; ++st) {
         const int g = k * C::kSteps + st, buf = g & 1;
-        uint4 v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const uint4*>(y + sw128(st * C::kStep + rr + e * RS, ch & 7));
-        if (g >= 2) wait(kPartFree + buf, (g >> 1) - 1);
-        unsigned char* d = sm + C::kOffPart + 3 * buf * C::kPart + (ch >> 3) * (C::kStep * 128);
+        uint4 v[4], w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = st * C::kStep + rr + e * RS;
-          uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0, o2 = o0;
-          if (r < nv) {
-            const uint4 w = w0[rev ? r : -r];
-            split3(v[e].x, w, o0.x, o1.x, o2.x);
-            split3(v[e].y, w, o0.y, o1.y, o2.y);
-            split3(v[e].z, w, o0.z, o1.z, o2.z);
-            split3(v[e].w, w, o0.w, o1.w, o2.w);
-          } else {   // rows behind the sequence's end may hold anything
-            *reinterpret_cast<uint4*>(z + sw128(r, ch & 7)) = make_uint4(0, 0, 0, 0);
-          }
-          unsigned char* p = d + sw128(rr + e * RS, ch & 7);
-          *reinterpret_cast<uint4*>(p) = o0;
-          *reinterpret_cast<uint4*>(p + C::kPart) = o1;
-          if (third) *reinterpret_cast<uint4*>(p + 2 * C::kPart) = o2;
+          v[e] = *reinterpret_cast<const uint4*>(y + sw128(r, ch & 7));
+          w[e] = w0[r < nv ? (rev ? r : -r) : 0];
         }
+        if (nv < kC) {   // rows behind the sequence's end may hold anything
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = st * C::kStep + rr + e * RS;
+            if (r >= nv) {
+              v[e] = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(z + sw128(r, ch & 7)) = v[e];
+            }
+          }
+        }
+        if (g >= 2) wait(kPartFree + buf, (g >> 1) - 1);
+        unsigned char* d = sm + C::kOffPart + 3 * buf * C::kPart + (ch >> 3) * (C::kStep * 128) + sw128(rr, ch & 7);
+        if (third)
+          split_rows<true, RS, C::kPart>(v, w, d);
+        else
+          split_rows<false, RS, C::kPart>(v, w, d);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + kYdReady + buf);
       }
+      if (!STATE && nv < kC && lane == 0) mbar_arrive(bars + kZClean);
     }
   } else if (warp < C::kLoad) {
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
@@ -404,34 +440,42 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
     const bool live = DP == 128 || lane < 16, trans = jb.trans;
     const int row = DP == 128 ? i : 16 * q + lane, col = half * NR;
     const uint32_t quad = tmem + ((uint32_t)(32 * q) << 16) + col;
-    float R[NR];
+    uint64_t R[NR / 2];   // pairs of columns
     {
       const float* src = STATE ? nullptr : a.segs > 1 ? jb.seg_init : jb.init;
       const float f0 = (a.segs > 1 || !jb.init_decays) ? 1.f : expf(ld);
       const size_t at = (a.segs > 1 ? (size_t)u * a.segs + seg : (size_t)u) * dd;
 #pragma unroll
-      for (int c = 0; c < NR; ++c) {
-        R[c] = 0.f;
-        if (src && live && row < da && col + c < db)
-          R[c] = f0 * src[at + (trans ? (size_t)(col + c) * da + row : (size_t)row * db + col + c)];
+      for (int c = 0; c < NR; c += 2) {   // da and db are even
+        float r0 = 0.f, r1 = 0.f;
+        if (src && live && row < da && col + c < db) {
+          r0 = f0 * src[at + (trans ? (size_t)(col + c) * da + row : (size_t)row * db + col + c)];
+          r1 = f0 * src[at + (trans ? (size_t)(col + c + 1) * da + row : (size_t)row * db + col + c + 1)];
+        }
+        R[c / 2] = f2(r0, r1);
       }
     }
     auto update = [&](int k) {   // R after the chunk of step k
       const int c = chunk(k);
       const Decay dec(ld * (valid(c) - (!STATE && c == nch - 1 ? jb.fin_sub : 0)));
+      const uint64_t em = f2(dec.em, dec.em), mu = f2(dec.mul, dec.mul);
       wait(kDFull, k);
       tc_fence_after();
 #pragma unroll
       for (int c0 = 0; c0 < NR; c0 += 16) {
-        float d[16];
-        tmem_ld16(quad + C::kTd + c0, d);
+        uint32_t d[16];
+        tmem_ld16_async(quad + C::kTd + c0, d);
+        tmem_wait_ld16(d);
         if (c0 + 16 == NR) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bars + kDRead);
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) R[c0 + e] = dec(R[c0 + e]) + d[e];
+        for (int e = 0; e < 8; ++e) {
+          const uint64_t r = R[c0 / 2 + e];
+          R[c0 / 2 + e] = add2(fma2(em, r, mul2(mu, r)), f2(d[2 * e], d[2 * e + 1]));
+        }
       }
     };
     const long long ts = jb.os[2];
@@ -441,6 +485,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
     auto epilogue = [&](int k) {
       const int c = chunk(k), nv = valid(c), e = rev ? nv - 1 - i : i;
       const float f = e >= 0 ? c_inter * pw[e] : 0.f;
+      const uint64_t ff = f2(f, f);
       wait(kOFull, k);
       tc_fence_after();
       __nv_bfloat16* o = O + (long long)(c * kC + i) * ts;
@@ -459,8 +504,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
         uint32_t w[8];
 #pragma unroll
         for (int g = 0; g < 8; ++g)
-          w[g] = pack2(fmaf(f, __uint_as_float(x[2 * g]), __uint_as_float(z[2 * g])),
-                       fmaf(f, __uint_as_float(x[2 * g + 1]), __uint_as_float(z[2 * g + 1])));
+          w[g] = packf2(fma2(ff, f2(x[2 * g], x[2 * g + 1]), f2(z[2 * g], z[2 * g + 1])));
         if (i < nv) {
           const int left = db - col - c0;
           if (wide && left > 0) {
@@ -481,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
           for (int g = 0; g < NR; g += 8) {
             const int cc = col + g;
             *reinterpret_cast<uint4*>(sm + C::kOffR + (cc >> 6) * (DP * 128) + sw128(row, (cc & 63) >> 3)) =
-                make_uint4(pack2(R[g], R[g + 1]), pack2(R[g + 2], R[g + 3]), pack2(R[g + 4], R[g + 5]), pack2(R[g + 6], R[g + 7]));
+                make_uint4(packf2(R[g / 2]), packf2(R[g / 2 + 1]), packf2(R[g / 2 + 2]), packf2(R[g / 2 + 3]));
           }
         }
         fence_async_smem();
@@ -496,8 +540,11 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       float* dst = STATE ? jb.local + ((size_t)u * a.segs + seg) * dd : jb.fin + u * dd;
       if (live && row < da) {
 #pragma unroll
-        for (int c = 0; c < NR; ++c)
-          if (col + c < db) dst[!STATE && trans ? (size_t)(col + c) * da + row : (size_t)row * db + col + c] = R[c];
+        for (int c = 0; c < NR; c += 2)
+          if (col + c < db) {
+            dst[!STATE && trans ? (size_t)(col + c) * da + row : (size_t)row * db + col + c] = f2_lo(R[c / 2]);
+            dst[!STATE && trans ? (size_t)(col + c + 1) * da + row : (size_t)row * db + col + c + 1] = f2_hi(R[c / 2]);
+          }
       }
     }
   }
