@@ -8,7 +8,7 @@
 //   O  = Oz + c_inter l^i Ox                (epilogue warps, fp32, rounded once)
 //   D  = (y c_state l^(n-j))^T z            (M da, N db, K 128 tokens), R' = l^n R + D   (state warps)
 // The decayed rows of y enter as bf16 parts (value and remainders, one product each): two parts (2^-17) where R
-// only meets x, whose products are rounded to bf16 anyway, three (2^-25) where the run's state is returned. D
+// only meets x, whose products are rounded to bf16 anyway, three (2^-25) in calls that return a state. D
 // starts from zero in every chunk and is added to R by CUDA cores: tensor-core accumulation truncates and would
 // drift over thousands of chunks. All widths are padded to DP = 64 or 128 by TMA's zero fill.
 //
@@ -45,7 +45,6 @@ struct TcJob {
   float* local;           // state kernel: sums of each segment, [units][segs]
   int da, db, rev, trans, init_decays, fin_sub;
   int wide;               // O's rows are whole, aligned 32-byte sectors
-  int parts;              // bf16 parts of y's decayed rows: 3 where a state is returned, else 2
   float c_inter, c_intra, c_state;
 };
 struct TcArgs {
@@ -55,21 +54,30 @@ struct TcArgs {
   int heads, N, segs, seg_chunks;
 };
 
-template <int DP, bool STATE>
+template <int DP, bool STATE, int PARTS>
 struct Cfg {
-  static constexpr int kTile = DP / 64 * kPanelB;          // bytes of a token tile, one ring slot
-  static constexpr int kPer = STATE ? 2 : 3;               // tiles of a chunk: y, [x], z
-  static constexpr int kSlots = DP == 64 ? (STATE ? 8 : 9) : (STATE ? 5 : 4);
-  // y's decayed rows are formed in steps of kStep tokens: four 16-byte vectors per thread
+  static constexpr int kTile = DP / 64 * kPanelB;   // bytes of a token tile
+  // rings of tiles. At 128 channels five fit: x is done with first (S, then Ox), y and z are held longer
+  static constexpr int kNY = DP == 64 ? 3 : 2;
+  static constexpr int kNX = STATE ? 0 : DP == 64 ? 3 : 1;
+  static constexpr int kNZ = DP == 64 ? 3 : 2;
+  static constexpr int kOffX = kNY * kTile;
+  static constexpr int kOffZ = kOffX + kNX * kTile;
+  static constexpr int kOffPart = kOffZ + kNZ * kTile;
+  // y's decayed rows are formed in steps of kStep tokens, kVec 16-byte vectors per thread, in kBufs buffers of PARTS
+  // parts
   static constexpr int kStep = 4096 / DP;
+  static constexpr int kBufs = DP == 128 && PARTS == 3 && !STATE ? 1 : 2;
   static constexpr int kSteps = kC / kStep;
-  static constexpr int kPart = kStep * DP * 2;             // bytes of one part of a step
-  static constexpr int kOffPart = kSlots * kTile;          // 2 buffers of 3 parts
-  static constexpr int kOffR = kOffPart + 6 * kPart;
+  static constexpr int kVec = kStep * DP / 8 / 128;
+  static constexpr int kPart = kStep * DP * 2;
+  static constexpr int kOffR = kOffPart + kBufs * PARTS * kPart;
   static constexpr int kOffBar = kOffR + (STATE ? 0 : DP * DP * 2);
-  static constexpr int kOffPw = kOffBar + 320;
-  static constexpr int kOffWt = kOffPw + 4 * (kC + 4 + 32 + kC + 32);
-  static constexpr int kSmem = kOffWt + 16 * (kC + 1) + 1024;   // + alignment of the base to 1024
+  static constexpr int kOffPb = kOffBar + 384;
+  static constexpr int kOffPi = kOffPb + 4 * 32;
+  static constexpr int kOffWt = kOffPi + 4 * (32 + kC);
+  static constexpr int kWt = PARTS == 3 ? 16 : 8;
+  static constexpr int kSmem = kOffWt + kWt * (kC + 1);
   static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
   // warps: 4 for P (not STATE), 4 for y's decayed rows, 8 for the state and the epilogue, loads, products (two)
   static constexpr int kY0 = STATE ? 0 : 4;
@@ -78,18 +86,24 @@ struct Cfg {
   static constexpr int kMma = kLoad + 1;      // products of the state
   static constexpr int kMmaO = kMma + 1;      // products of the output (not STATE)
   static constexpr int kThreads = 32 * (STATE ? kMma + 1 : kMmaO + 1);
-  // 608 threads have 96 registers each; with 64 of them R, the state warps take 24 more from the P warps (16 each)
-  // and the y warps (32 each): 128 (80 + 64) + 256 120 + 96 96 = 608 96
-  static constexpr bool kSplitRegs = DP == 128 && !STATE;
-  // tensor memory columns; P (bf16 pairs) takes the first half of S's columns, row by row as S is read
-  static constexpr int kTs = 0, kToz = STATE ? 0 : kC, kTox = kToz + (STATE ? 0 : DP), kTd = kTox + (STATE ? 0 : DP);
+  // 608 threads have 96 registers each; with up to 64 of them R, the state warps take 16 more from the y warps (32
+  // each): 128 64 + 256 112 + 224 96 = 608 96
+  static constexpr bool kSplitRegs = !STATE;
+  // tensor memory columns. DP 64: S, P (bf16 pairs), two sets of Oz and Ox, D. DP 128: no room for all of that; P
+  // goes over the first half of S's columns, row by row as S is read, and there is one set of Oz and Ox
+  static constexpr bool kOwnP = DP == 64;
+  static constexpr int kNO = DP == 64 ? 2 : 1;
+  static constexpr int kTs = 0, kTp = kOwnP ? kC : 0, kToz = STATE ? 0 : kOwnP ? kC + kC / 2 : kC;
+  static constexpr int kTd = STATE ? 0 : kToz + kNO * 2 * DP;
   static constexpr int kTmem = STATE ? DP : 512;
+  static_assert(kTd + DP <= kTmem, "tensor memory");
 };
 enum Bar {
-  kFull = 0, kEmpty = 9, kSFull = 18, kPReady, kYdReady, kPartFree = kYdReady + 2, kDFull = kPartFree + 2, kDRead,
-  kRbReady, kXDone, kOFull, kOFree, kZClean, kFin, kNumBars = kFin + 2
+  kFullY = 0, kFullX = 3, kFullZ = 6, kEmptyY = 9, kEmptyX = 12, kEmptyZ = 15, kSFull = 18, kSRead, kPReady,
+  kYdReady, kPartFree = kYdReady + 2, kDFull = kPartFree + 2, kDRead, kRbReady, kXDone, kOFull, kOFree = kOFull + 2, kZClean = kOFree + 2, kFin,
+  kNumBars = kFin + 2
 };
-static_assert(kNumBars * 8 <= 304, "barriers overlap the TMEM slot");
+static_assert(kNumBars * 8 <= 368, "barriers overlap the TMEM slot");
 
 struct Waiter {
   uint64_t* bars;
@@ -121,34 +135,43 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// y w for a pair y of bf16 and w = w.x + w.y + w.z in bf16 parts, as a + b + c in bf16: a = y w.x rounded, its
-// remainder y w.x - a is a bf16 itself (8 by 8 bits make 16), and so on down; about 2^-25 of y w is left out
+// y w for a pair y of bf16 and w = w.x + w.y + w3 in bf16 parts, as a + b + c in bf16: a = y w.x rounded, its
+// remainder y w.x - a is a bf16 itself (8 by 8 bits make 16), and so on down; about 2^-17 of y w
+// is left out with two parts, 2^-25 with three
 __device__ __forceinline__ __nv_bfloat162 as_b2(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); }
 __device__ __forceinline__ uint32_t as_u(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
-template <bool THIRD>
-__device__ __forceinline__ void split3(uint32_t y, const uint4& w, uint32_t& a, uint32_t& b, uint32_t& c) {
-  const __nv_bfloat162 y2 = as_b2(y), wx = as_b2(w.x), wy = as_b2(w.y), wz = as_b2(w.z);
+template <int PARTS>
+__device__ __forceinline__ void split(uint32_t y, uint2 w, uint32_t w3, uint32_t& a, uint32_t& b, uint32_t& c) {
+  const __nv_bfloat162 y2 = as_b2(y), wx = as_b2(w.x), wy = as_b2(w.y);
   const __nv_bfloat162 hi = __hmul2(y2, wx), rem = __hfma2(y2, wx, __hneg2(hi));
   const __nv_bfloat162 mid = __hfma2(y2, wy, rem);
   a = as_u(hi);
   b = as_u(mid);
-  if (THIRD) c = as_u(__hfma2(y2, wz, __hfma2(y2, wy, __hsub2(rem, mid))));
+  if (PARTS == 3) c = as_u(__hfma2(y2, as_b2(w3), __hfma2(y2, wy, __hsub2(rem, mid))));
 }
-// four vectors of a thread, RS rows apart (a multiple of 8: the same place in the swizzle), each part PART bytes on
-template <bool THIRD, int RS, int PART>
-__device__ __forceinline__ void split_rows(const uint4 (&v)[4], const uint4 (&w)[4], unsigned char* d) {
-  uint4 o[4][3];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    split3<THIRD>(v[e].x, w[e], o[e][0].x, o[e][1].x, o[e][2].x);
-    split3<THIRD>(v[e].y, w[e], o[e][0].y, o[e][1].y, o[e][2].y);
-    split3<THIRD>(v[e].z, w[e], o[e][0].z, o[e][1].z, o[e][2].z);
-    split3<THIRD>(v[e].w, w[e], o[e][0].w, o[e][1].w, o[e][2].w);
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* r) {
+  if constexpr (N == 32) {
+    tmem_ld32_async(at, r);
+    tmem_wait_ld(r);
+  } else {
+    tmem_ld16_async(at, r);
+    tmem_wait_ld16(r);
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-#pragma unroll
-    for (int p = 0; p < (THIRD ? 3 : 2); ++p) *reinterpret_cast<uint4*>(d + e * RS * 128 + p * PART) = o[e][p];
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld2(uint32_t at0, uint32_t* r0, uint32_t at1, uint32_t* r1) {
+  if constexpr (N == 32) {
+    tmem_ld32_async(at0, r0);
+    tmem_ld32_async(at1, r1);
+    tmem_wait_ld(r0);
+    tmem_wait_ld(r1);
+  } else {
+    tmem_ld16_async(at0, r0);
+    tmem_ld16_async(at1, r1);
+    tmem_wait_ld16(r0);
+    tmem_wait_ld16(r1);
+  }
 }
 
 // one 32-byte store (a whole sector)
@@ -160,62 +183,69 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
 __device__ __forceinline__ uint32_t packf2(uint64_t v) { return pack2(f2_lo(v), f2_hi(v)); }
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 
-// The P warps of a run of n chunks: P = c_intra l^|i-j| S on the causal side, in bf16, over S's own columns
-// (thread = token row i; block cb of S's columns is read before P's block cb goes over columns read earlier).
-// l^|i-j| is l^(distance of i to the block) pb[c] beside the diagonal block. nv0: valid tokens of the first chunk,
-// where a reverse run finds its sequence's ragged end (forwards, columns behind the end are above the diagonal).
-template <bool REV>
-__device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bars, uint32_t ts, const float* pw,
+// The P warps of a run of n chunks: P = c_intra l^|i-j| S on the causal side, in bf16 (thread = token row i).
+// pi holds c_intra l^n after 32 zeros; beside the diagonal block l^|i-j| is l^(distance of i to the block) pb[c].
+// nv0: valid tokens of the first chunk, where a reverse run finds its sequence's ragged end (forwards, columns
+// behind the end are above the diagonal).
+template <class C, bool REV>
+__device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bars, uint32_t tmem, const float* pi,
                                         const float* pb, int nv0) {
   const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, i = 32 * q + lane;
-  const uint32_t srow = ts + ((uint32_t)(32 * q) << 16);
-  const float* pd = pw + (REV ? -lane : lane);   // pw is zero for 31 exponents below 0
+  const uint32_t quad = tmem + ((uint32_t)(32 * q) << 16), srow = quad + C::kTs, prow = quad + C::kTp;
+  const float* pd = pi + (REV ? -lane : lane);
+  // the other side of the diagonal is zero: once where P has its own columns, else in every chunk
+  auto zeros = [&]() {
+    uint32_t w[16] = {};
+    for (int cb = REV ? 0 : q + 1; cb < (REV ? q : 4); ++cb) tmem_st16(prow + 16 * cb, w);
+  };
+  if (C::kOwnP) zeros();
+  const int b0 = REV ? q : 0, b1 = REV ? 4 : q + 1;   // blocks of 32 columns
   for (int k = 0; k < n; ++k) {
+    const bool ragged = REV && k == 0 && nv0 < kC;
     wait(kSFull, k);
+    if (C::kOwnP && k > 0) wait(kOFull + (k - 1) % C::kNO, (k - 1) / C::kNO);   // P's columns are free
     tc_fence_after();
 #pragma unroll 1
-    for (int cb = 0; cb < 4; ++cb) {
-      uint32_t w[16];
-      if (REV ? cb >= q : cb <= q) {
-        uint32_t v[32];
-        tmem_ld32_async(srow + 32 * cb, v);
-        if (cb == q) {
-          float p[32];
+    for (int cb = b0; cb < b1; ++cb) {
+      uint32_t v[32];
+      tmem_ld32_async(srow + 32 * cb, v);
+      if (cb == q) {
+        tmem_wait_ld(v);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) p[c] = pd[REV ? c : -c];
-          tmem_wait_ld(v);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float x = __uint_as_float(v[c]) * p[c];
-            v[c] = (REV ? c >= lane : c <= lane) ? __float_as_uint(x) : 0u;
-          }
-        } else {
-          const float f = pw[REV ? 32 * cb - i : i - 32 * cb - 31];
-          const uint64_t ff = f2(f, f);
-          tmem_wait_ld(v);
-#pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(pb + c);
-            const uint64_t x = mul2(f2(v[c], v[c + 1]), mul2(ff, p.x)), y = mul2(f2(v[c + 2], v[c + 3]), mul2(ff, p.y));
-            v[c] = (uint32_t)x;
-            v[c + 1] = (uint32_t)(x >> 32);
-            v[c + 2] = (uint32_t)y;
-            v[c + 3] = (uint32_t)(y >> 32);
-          }
+        for (int c = 0; c < 32; ++c) {
+          const float x = __uint_as_float(v[c]) * pd[REV ? c : -c];
+          v[c] = (REV ? c >= lane : c <= lane) ? __float_as_uint(x) : 0u;
         }
-        if (REV && k == 0 && nv0 < 32 * cb + 32) {   // columns of tokens behind the end may hold anything
+      } else {
+        const float f = pi[REV ? 32 * cb - i : i - 32 * cb - 31];
+        const uint64_t ff = f2(f, f);
+        tmem_wait_ld(v);
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (32 * cb + c >= nv0) v[c] = 0;
+        for (int c = 0; c < 32; c += 4) {
+          const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(pb + c);
+          const uint64_t x = mul2(f2(v[c], v[c + 1]), mul2(ff, p.x)), y = mul2(f2(v[c + 2], v[c + 3]), mul2(ff, p.y));
+          v[c] = (uint32_t)x;
+          v[c + 1] = (uint32_t)(x >> 32);
+          v[c + 2] = (uint32_t)y;
+          v[c + 3] = (uint32_t)(y >> 32);
         }
-#pragma unroll
-        for (int c = 0; c < 16; ++c) w[c] = pack2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
-      } else {   // the other side of the diagonal
-#pragma unroll
-        for (int c = 0; c < 16; ++c) w[c] = 0;
       }
-      tmem_st16(srow + 16 * cb, w);
+      if (C::kOwnP && cb + 1 == b1) {   // S has been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + kSRead);
+      }
+      if (ragged && nv0 < 32 * cb + 32) {   // columns of tokens behind the end may hold anything
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (32 * cb + c >= nv0) v[c] = 0;
+      }
+      uint32_t w[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) w[c] = pack2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+      tmem_st16(prow + 16 * cb, w);   // on S's columns where it has none of its own: on those read before
     }
+    if (!C::kOwnP) zeros();
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
@@ -223,10 +253,10 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
   }
 }
 
-template <int DP, bool STATE>
-__global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const __grid_constant__ TcArgs a) {
-  using C = Cfg<DP, STATE>;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
+template <int DP, bool STATE, int PARTS>
+__global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc(const __grid_constant__ TcArgs a) {
+  using C = Cfg<DP, STATE, PARTS>;
+  extern __shared__ __align__(1024) unsigned char sm[];
   const TcJob& jb = a.job[blockIdx.z];
   const int u = blockIdx.x, seg = blockIdx.y, b = u / a.heads, h = u % a.heads;
   const int L = unit_length(a.lengths, b, a.N), nch = (L + kC - 1) / kC;
@@ -243,36 +273,39 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   if (STATE && (rev ? seg == 0 : c_hi == nch)) return;   // nothing follows this segment
   const bool ends = !STATE && jb.fin && (rev ? seg == 0 : c_hi == nch);
 
-  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  if ((smem_u32(sm) & 1023u) != 0) {   // the swizzle needs it; the declaration asks for it
+    if (t == 0) atomicOr(&g_decay_status, 1);
+    return;
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffBar + 304);
-  volatile int* gave_up = reinterpret_cast<volatile int*>(sm + C::kOffBar + 308);
-  float* pw = reinterpret_cast<float*>(sm + C::kOffPw);   // l^0 .. l^128
-  float* pb = pw + kC + 4;                                 // rev: l^c, else l^(31-c), c = 0 .. 31
-  float* pi = pb + 32 + 32;                                // c_intra l^0 .. c_intra l^127 after 32 zeros
-  uint4* wt = reinterpret_cast<uint4*>(sm + C::kOffWt);   // c_state l^n as three bf16 parts, each twice in a word
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffBar + 368);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(sm + C::kOffBar + 372);
+  float* pb = reinterpret_cast<float*>(sm + C::kOffPb);        // rev: l^c, else l^(31-c), c = 0 .. 31
+  float* pi = reinterpret_cast<float*>(sm + C::kOffPi) + 32;   // c_intra l^0 .. c_intra l^127 after 32 zeros
+  unsigned char* wt = sm + C::kOffWt;                          // c_state l^n in bf16 parts, each twice in a word
   const float ld = decay_log(a.log_decay[h]);
   const Waiter wait{bars, gave_up};
   if (t == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bars + i, i >= kEmpty && i < kSFull                                            ? (STATE ? 1 : 2)
-                          : i == kPReady || (i >= kYdReady && i < kPartFree) || i == kZClean ? 4
-                          : i == kDRead || i == kRbReady || i == kOFree                      ? 8
-                                                                                             : 1);
+      mbar_init(bars + i, i >= kEmptyY && i < kEmptyX                                             ? (STATE ? 4 : 5)
+                          : i >= kEmptyZ && i < kSFull                                            ? (STATE ? 1 : 2)
+                          : i == kSRead || i == kPReady || (i >= kYdReady && i < kPartFree) || i == kZClean ? 4
+                          : i == kDRead || i == kRbReady || (i >= kOFree && i < kZClean)          ? 8
+                                                                                                  : 1);
     mbar_init_fence();
     *gave_up = 0;
   }
   if (warp == C::kMma) tmem_alloc(tmem_slot, C::kTmem);
   for (int i = t; i <= kC; i += C::kThreads) {
     const float w = expf(ld * i);
-    pw[i] = w;
     if (i < 32) {
       pb[rev ? i : 31 - i] = w;
       pi[i - 32] = 0.f;
     }
     if (i < kC) pi[i] = jb.c_intra * w;
     const float f = jb.c_state * w, f1 = f - bf_lo(pack2(f, f)), f2 = f1 - bf_lo(pack2(f1, f1));
-    wt[i] = make_uint4(pack2(f, f), pack2(f1, f1), pack2(f2, f2), 0u);
+    *reinterpret_cast<uint2*>(wt + i * C::kWt) = make_uint2(pack2(f, f), pack2(f1, f1));
+    if (PARTS == 3) *reinterpret_cast<uint32_t*>(wt + i * C::kWt + 8) = pack2(f2, f2);
   }
   tc_fence_before();
   __syncthreads();
@@ -284,158 +317,186 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
 
   if (warp == C::kLoad) {
     if (lane == 0) {
-      const int total = n * C::kPer;
-      int g = 0;
-      for (; g < total; ++g) {   // y, [x], z of every chunk in turn, one ring slot each
-        const int s = g % C::kSlots, w = g % C::kPer;
-        if (g >= C::kSlots) wait(kEmpty + s, g / C::kSlots - 1);
-        if (*gave_up) break;
-        const CUtensorMap* m = w == 0 ? &jb.y : w == C::kPer - 1 ? &jb.z : &jb.x;
-        mbar_expect_tx(bars + kFull + s, C::kTile);
+      // y, z, x of every chunk in turn, each tensor in a ring of its own
+      auto load = [&](const CUtensorMap* m, int off, int ring, int full, int empty, int k) {
+        const int s = k % ring;
+        if (k >= ring) wait(empty + s, k / ring - 1);
+        if (*gave_up) return false;
+        mbar_expect_tx(bars + full + s, C::kTile);
         for (int p = 0; p < DP / 64; ++p)
-          tma_load_4d(sm + s * C::kTile + p * kPanelB, m, 64 * p, chunk(g / C::kPer) * kC, h, b, bars + kFull + s);
+          tma_load_4d(sm + off + s * C::kTile + p * kPanelB, m, 64 * p, chunk(k) * kC, h, b, bars + full + s);
+        return true;
+      };
+      int ny = 0, nx = 0, nz = 0;   // loads issued
+      for (int k = 0; k < n; ++k) {
+        if (!load(&jb.y, 0, C::kNY, kFullY, kEmptyY, k)) break;
+        ++ny;
+        if (!load(&jb.z, C::kOffZ, C::kNZ, kFullZ, kEmptyZ, k)) break;
+        ++nz;
+        if constexpr (!STATE) {
+          if (!load(&jb.x, C::kOffX, C::kNX, kFullX, kEmptyX, k)) break;
+          ++nx;
+        }
       }
-      for (int i = max(0, g - C::kSlots); i < g; ++i) wait.drain(kFull + i % C::kSlots, i / C::kSlots);
+      for (int i = max(0, ny - C::kNY); i < ny; ++i) wait.drain(kFullY + i % C::kNY, i / C::kNY);
+      for (int i = max(0, nz - C::kNZ); i < nz; ++i) wait.drain(kFullZ + i % C::kNZ, i / C::kNZ);
+      if constexpr (!STATE)
+        for (int i = max(0, nx - C::kNX); i < nx; ++i) wait.drain(kFullX + i % C::kNX, i / C::kNX);
     }
   } else if (!STATE && warp == C::kMmaO) {
-    if (lane == 0) {
-      // S, Ox, Oz of every chunk in turn. Descriptors of the ring's first slot and R; b bytes further is + b / 16
-      const uint32_t base = smem_u32(sm);
-      const uint64_t d_k = desc_sw128(base, 16, 1024), d_mn = desc_sw128(base, kPanelB, 1024),
-                     d_rb = desc_sw128(base + C::kOffR, DP * 128, 1024);
-      constexpr uint32_t id_s = idesc(1, kC, kC, 0, 0), id_o = idesc(1, kC, DP, 0, 1);
-      for (int k = 0; k < n; ++k) {
-        const int gy = k * C::kPer, gx = gy + 1, gz = gy + C::kPer - 1;
-        const int sy = gy % C::kSlots, sx = gx % C::kSlots, sz = gz % C::kSlots;
-        const uint64_t y = d_k + sy * (C::kTile / 16), x = d_k + sx * (C::kTile / 16), z = d_mn + sz * (C::kTile / 16);
-        wait(kFull + sy, gy / C::kSlots);
-        wait(kFull + sx, gx / C::kSlots);
-        if (k > 0) wait(kOFull, k - 1);   // P of the chunk before has been used
-        tc_fence_after();
+    if constexpr (!STATE) {
+      if (lane == 0) {
+        // S, Ox, Oz of every chunk in turn. Descriptors of a ring's first tile; b bytes further is + b / 16
+        const uint32_t base = smem_u32(sm);
+        const uint64_t d_y = desc_sw128(base, 16, 1024), d_x = desc_sw128(base + C::kOffX, 16, 1024),
+                       d_z = desc_sw128(base + C::kOffZ, kPanelB, 1024), d_rb = desc_sw128(base + C::kOffR, DP * 128, 1024);
+        constexpr uint32_t id_s = idesc(1, kC, kC, 0, 0), id_o = idesc(1, kC, DP, 0, 1);
+        auto scores = [&](int k) {
+          const int sy = k % C::kNY, sx = k % C::kNX;
+          const uint64_t y = d_y + sy * (C::kTile / 16), x = d_x + sx * (C::kTile / 16);
+          wait(kFullY + sy, k / C::kNY);
+          wait(kFullX + sx, k / C::kNX);
+          if (k > 0) wait(C::kOwnP ? kSRead : kOFull, k - 1);   // S has been read; without its own columns, P used (kNO 1)
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) {
-          const int off = ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16;
-          mma_bf16(tmem + C::kTs, x + off, y + off, id_s, kk > 0);
+          for (int kk = 0; kk < DP / 16; ++kk) {
+            const int off = ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16;
+            mma_bf16(tmem + C::kTs, x + off, y + off, id_s, kk > 0);
+          }
+          mma_commit(bars + kSFull);
+          mma_commit(bars + kEmptyY + sy);
+        };
+        scores(0);
+        for (int k = 0; k < n; ++k) {
+          const int sx = k % C::kNX, sz = k % C::kNZ;
+          const uint64_t x = d_x + sx * (C::kTile / 16), z = d_z + sz * (C::kTile / 16);
+          const uint32_t oz = tmem + C::kToz + (k % C::kNO) * 2 * DP, ox = oz + DP;
+          wait(kRbReady, k);
+          if (k >= C::kNO) wait(kOFree + k % C::kNO, k / C::kNO - 1);
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < DP / 16; ++kk)
+            mma_bf16(ox, x + ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16, d_rb + kk * 128, id_o, kk > 0);
+          mma_commit(bars + kXDone);
+          mma_commit(bars + kEmptyX + sx);
+          if (C::kOwnP && k + 1 < n) scores(k + 1);
+          wait(kFullZ + sz, k / C::kNZ);
+          if (valid(chunk(k)) < kC) wait(kZClean, 0);
+          wait(kPReady, k);
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kC / 16; ++kk) mma_bf16_ta(oz, tmem + C::kTp + 8 * kk, z + kk * 128, id_o, kk > 0);
+          mma_commit(bars + kOFull + k % C::kNO);
+          mma_commit(bars + kEmptyZ + sz);
+          if (!C::kOwnP && k + 1 < n) scores(k + 1);
         }
-        mma_commit(bars + kSFull);
-        mma_commit(bars + kEmpty + sy);
-        wait(kRbReady, k);
-        if (k > 0) wait(kOFree, k - 1);
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_bf16(tmem + C::kTox, x + ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16, d_rb + kk * 128, id_o, kk > 0);
-        mma_commit(bars + kXDone);
-        mma_commit(bars + kEmpty + sx);
-        mma_commit(bars + kEmpty + sx);
-        wait(kFull + sz, gz / C::kSlots);
-        if (valid(chunk(k)) < kC) wait(kZClean, 0);
-        wait(kPReady, k);
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kC / 16; ++kk)
-          mma_bf16_ta(tmem + C::kToz, tmem + C::kTs + 8 * kk, z + kk * 128, id_o, kk > 0);
-        mma_commit(bars + kOFull);
-        mma_commit(bars + kEmpty + sz);
+        mma_commit(bars + kFin);
+        wait.drain(kFin, 0);
       }
-      mma_commit(bars + kFin);
-      wait.drain(kFin, 0);
     }
   } else if (warp == C::kMma) {
     if (lane == 0) {
       // D of every chunk: its own thread, so that the state runs ahead of the outputs
       const uint32_t base = smem_u32(sm);
-      const uint64_t d_mn = desc_sw128(base, kPanelB, 1024), d_part = desc_sw128(base + C::kOffPart, C::kStep * 128, 1024);
+      const uint64_t d_z = desc_sw128(base + C::kOffZ, kPanelB, 1024),
+                     d_part = desc_sw128(base + C::kOffPart, C::kStep * 128, 1024);
       constexpr uint32_t id_d = idesc(1, DP, DP, 1, 1);
-      const bool third = jb.parts == 3;
       for (int k = 0; k < n; ++k) {
-        const int gy = k * C::kPer, gz = gy + C::kPer - 1, sy = gy % C::kSlots, sz = gz % C::kSlots;
-        const uint64_t z = d_mn + sz * (C::kTile / 16);
+        const int sz = k % C::kNZ;
+        const uint64_t z = d_z + sz * (C::kTile / 16);
         const bool carry = STATE || ends || k < n - 1;
-        wait(kFull + sz, gz / C::kSlots);
+        wait(kFullZ + sz, k / C::kNZ);
         if (k > 0) wait(kDRead, k - 1);
 #pragma unroll 1
         for (int s = 0; s < C::kSteps; ++s) {
-          const int g = k * C::kSteps + s, buf = g & 1;
-          wait(kYdReady + buf, g >> 1);
+          const int g = k * C::kSteps + s, buf = g % C::kBufs;
+          wait(kYdReady + buf, g / C::kBufs);
           tc_fence_after();
           if (carry) {
 #pragma unroll
-            for (int p = 0; p < 3; ++p)
-              if (p < 2 || third) {
+            for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-                for (int kk = 0; kk < C::kStep / 16; ++kk)
-                  mma_bf16(tmem + C::kTd, d_part + (3 * buf + p) * (C::kPart / 16) + kk * 128,
-                           z + (s * C::kStep + 16 * kk) * 8, id_d, s + p + kk > 0);
-              }
+              for (int kk = 0; kk < C::kStep / 16; ++kk)
+                mma_bf16(tmem + C::kTd, d_part + (PARTS * buf + p) * (C::kPart / 16) + kk * 128,
+                         z + (s * C::kStep + 16 * kk) * 8, id_d, s + p + kk > 0);
           }
           mma_commit(bars + kPartFree + buf);
         }
         if (carry) mma_commit(bars + kDFull);
-        mma_commit(bars + kEmpty + sy);
-        mma_commit(bars + kEmpty + sz);
+        mma_commit(bars + kEmptyZ + sz);
       }
       mma_commit(bars + kFin + 1);
       wait.drain(kFin + 1, 0);
     }
   } else if (!STATE && warp < C::kY0) {
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (rev)
-      weights<true>(n, wait, bars, tmem + C::kTs, pi, pb, L - (c_hi - 1) * kC);
+      weights<C, true>(n, wait, bars, tmem, pi, pb, L - (c_hi - 1) * kC);
     else
-      weights<false>(n, wait, bars, tmem + C::kTs, pi, pb, kC);
+      weights<C, false>(n, wait, bars, tmem, pi, pb, kC);
   } else if (warp < C::kR0) {
     // y's decayed rows, in steps of kStep tokens into one of two buffers
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     const int ty = t - 32 * C::kY0;
-    constexpr int CH = DP / 8, RS = 128 / CH;   // 16-byte vectors of a row, rows per pass
+    constexpr int CH = DP / 8, RS = 128 / CH;   // 16-byte vectors of a row, rows per pass (a multiple of 8)
     const int ch = ty % CH, rr = ty / CH;
-    const bool third = jb.parts == 3;
+    const uint32_t at = (ch >> 3) * kPanelB + sw128(rr, ch & 7);   // rows RS apart have the same place in the swizzle
+    unsigned char* d0 = sm + C::kOffPart + (ch >> 3) * (C::kStep * 128) + sw128(rr, ch & 7);
     for (int k = 0; k < n; ++k) {
       const int c = chunk(k), nv = valid(c), sub = (!STATE && c == nch - 1) ? jb.fin_sub : 0;
-      const int gy = k * C::kPer, gz = gy + C::kPer - 1;
-      const unsigned char* y = sm + (gy % C::kSlots) * C::kTile + (ch >> 3) * kPanelB;
-      unsigned char* z = sm + (gz % C::kSlots) * C::kTile + (ch >> 3) * kPanelB;
-      const uint4* w0 = wt + (rev ? 1 : nv) - sub;   // row r has weight w0[r] (rev) or w0[-r]
-      wait(kFull + gy % C::kSlots, gy / C::kSlots);
-      if (nv < kC) wait(kFull + gz % C::kSlots, gz / C::kSlots);
+      const unsigned char* y = sm + (k % C::kNY) * C::kTile + at;
+      unsigned char* z = sm + C::kOffZ + (k % C::kNZ) * C::kTile + at;
+      const unsigned char* w0 = wt + ((rev ? 1 : nv) - sub) * C::kWt;   // row r: r weights on (rev) or back
+      const int ws = rev ? C::kWt : -C::kWt;
+      wait(kFullY + k % C::kNY, k / C::kNY);
+      if (nv < kC) wait(kFullZ + k % C::kNZ, k / C::kNZ);
 #pragma unroll 1
       for (int st = 0; st < C::kSteps; ++st) {
-        const int g = k * C::kSteps + st, buf = g & 1;
-        uint4 v[4], w[4];
+        const int g = k * C::kSteps + st, buf = g % C::kBufs;
+        uint4 v[C::kVec];
+        uint2 w[C::kVec];
+        uint32_t w3[C::kVec];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < C::kVec; ++e) {
           const int r = st * C::kStep + rr + e * RS;
-          v[e] = *reinterpret_cast<const uint4*>(y + sw128(r, ch & 7));
-          w[e] = w0[r < nv ? (rev ? r : -r) : 0];
+          const unsigned char* wp = w0 + (r < nv ? r : 0) * ws;
+          v[e] = *reinterpret_cast<const uint4*>(y + (st * C::kStep + e * RS) * 128);
+          w[e] = *reinterpret_cast<const uint2*>(wp);
+          w3[e] = PARTS == 3 ? *reinterpret_cast<const uint32_t*>(wp + 8) : 0u;
         }
         if (nv < kC) {   // rows behind the sequence's end may hold anything
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = st * C::kStep + rr + e * RS;
-            if (r >= nv) {
+          for (int e = 0; e < C::kVec; ++e)
+            if (st * C::kStep + rr + e * RS >= nv) {
               v[e] = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(z + sw128(r, ch & 7)) = v[e];
+              *reinterpret_cast<uint4*>(z + (st * C::kStep + e * RS) * 128) = v[e];
             }
-          }
         }
-        if (g >= 2) wait(kPartFree + buf, (g >> 1) - 1);
-        unsigned char* d = sm + C::kOffPart + 3 * buf * C::kPart + (ch >> 3) * (C::kStep * 128) + sw128(rr, ch & 7);
-        if (third)
-          split_rows<true, RS, C::kPart>(v, w, d);
-        else
-          split_rows<false, RS, C::kPart>(v, w, d);
+        if (g >= C::kBufs) wait(kPartFree + buf, g / C::kBufs - 1);
+        unsigned char* d = d0 + PARTS * buf * C::kPart;
+#pragma unroll
+        for (int e = 0; e < C::kVec; ++e) {
+          uint4 o[3];
+          split<PARTS>(v[e].x, w[e], w3[e], o[0].x, o[1].x, o[2].x);
+          split<PARTS>(v[e].y, w[e], w3[e], o[0].y, o[1].y, o[2].y);
+          split<PARTS>(v[e].z, w[e], w3[e], o[0].z, o[1].z, o[2].z);
+          split<PARTS>(v[e].w, w[e], w3[e], o[0].w, o[1].w, o[2].w);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) *reinterpret_cast<uint4*>(d + e * RS * 128 + p * C::kPart) = o[p];
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + kYdReady + buf);
       }
-      if (!STATE && nv < kC && lane == 0) mbar_arrive(bars + kZClean);
+      if (lane == 0) {
+        mbar_arrive(bars + kEmptyY + k % C::kNY);
+        if (!STATE && nv < kC) mbar_arrive(bars + kZClean);
+      }
     }
   } else if (warp < C::kLoad) {
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     // state and epilogue: R row and half of its columns per thread (DP 64: M = 64 puts row 16 q + lane in
     // lane < 16); in the epilogue thread = token row, the same half of O's columns
-    constexpr int NR = DP / 2;
+    constexpr int NR = DP / 2, NT = DP == 64 ? 32 : 16;   // columns of R, columns read at once
     const int q = warp & 3, half = (warp - C::kR0) >> 2, i = 32 * q + lane;
     const bool live = DP == 128 || lane < 16, trans = jb.trans;
     const int row = DP == 128 ? i : 16 * q + lane, col = half * NR;
@@ -446,75 +507,80 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       const float f0 = (a.segs > 1 || !jb.init_decays) ? 1.f : expf(ld);
       const size_t at = (a.segs > 1 ? (size_t)u * a.segs + seg : (size_t)u) * dd;
 #pragma unroll
-      for (int c = 0; c < NR; c += 2) {   // da and db are even
-        float r0 = 0.f, r1 = 0.f;
+      for (int c = 0; c < NR; c += 4) {   // da and db are multiples of 8
+        float4 r = make_float4(0, 0, 0, 0);
         if (src && live && row < da && col + c < db) {
-          r0 = f0 * src[at + (trans ? (size_t)(col + c) * da + row : (size_t)row * db + col + c)];
-          r1 = f0 * src[at + (trans ? (size_t)(col + c + 1) * da + row : (size_t)row * db + col + c + 1)];
+          const float* p = src + at + (trans ? (size_t)(col + c) * da + row : (size_t)row * db + col + c);
+          r = trans ? make_float4(p[0], p[da], p[2 * da], p[3 * da]) : *reinterpret_cast<const float4*>(p);
         }
-        R[c / 2] = f2(r0, r1);
+        R[c / 2] = f2(f0 * r.x, f0 * r.y);
+        R[c / 2 + 1] = f2(f0 * r.z, f0 * r.w);
       }
     }
+    Decay dec(ld * kC);
     auto update = [&](int k) {   // R after the chunk of step k
-      const int c = chunk(k);
-      const Decay dec(ld * (valid(c) - (!STATE && c == nch - 1 ? jb.fin_sub : 0)));
+      const int c = chunk(k), tokens = valid(c) - (!STATE && c == nch - 1 ? jb.fin_sub : 0);
+      if (tokens < kC || k == 1) dec = Decay(ld * tokens);   // step 0 may have been the ragged one
       const uint64_t em = f2(dec.em, dec.em), mu = f2(dec.mul, dec.mul);
       wait(kDFull, k);
       tc_fence_after();
 #pragma unroll
-      for (int c0 = 0; c0 < NR; c0 += 16) {
-        uint32_t d[16];
-        tmem_ld16_async(quad + C::kTd + c0, d);
-        tmem_wait_ld16(d);
-        if (c0 + 16 == NR) {
+      for (int c0 = 0; c0 < NR; c0 += NT) {
+        uint32_t d[NT];
+        tmem_ld<NT>(quad + C::kTd + c0, d);
+        if (c0 + NT == NR) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bars + kDRead);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < NT / 2; ++e) {
           const uint64_t r = R[c0 / 2 + e];
           R[c0 / 2 + e] = add2(fma2(em, r, mul2(mu, r)), f2(d[2 * e], d[2 * e + 1]));
         }
       }
     };
     const long long ts = jb.os[2];
-    __nv_bfloat16* O = STATE ? nullptr : jb.O + b * jb.os[0] + h * jb.os[1] + col;
     const bool wide = jb.wide;
     const float c_inter = jb.c_inter;
+    const int left = db - col;
+    __nv_bfloat16* o = STATE ? nullptr : jb.O + b * jb.os[0] + h * jb.os[1] + col + (long long)(chunk(0) * kC + i) * ts;
+    const long long o_step = (rev ? -kC : kC) * ts;
+    float f = STATE ? 0.f : c_inter * expf(ld * (rev ? kC - 1 - i : i));
     auto epilogue = [&](int k) {
-      const int c = chunk(k), nv = valid(c), e = rev ? nv - 1 - i : i;
-      const float f = e >= 0 ? c_inter * pw[e] : 0.f;
-      const uint64_t ff = f2(f, f);
-      wait(kOFull, k);
+      const int nv = valid(chunk(k));
+      float fk = f;
+      if (rev && nv < kC) fk = i < nv ? c_inter * expf(ld * (nv - 1 - i)) : 0.f;
+      const uint64_t ff = f2(fk, fk);
+      const uint32_t oz = quad + C::kToz + (k % C::kNO) * 2 * DP, ox = oz + DP;
+      wait(kOFull + k % C::kNO, k / C::kNO);
       tc_fence_after();
-      __nv_bfloat16* o = O + (long long)(c * kC + i) * ts;
-#pragma unroll 1
-      for (int c0 = 0; c0 < NR; c0 += 16) {
-        uint32_t z[16], x[16];
-        tmem_ld16_async(quad + C::kToz + c0, z);
-        tmem_ld16_async(quad + C::kTox + c0, x);
-        tmem_wait_ld16(z);
-        tmem_wait_ld16(x);
-        if (c0 + 16 == NR) {
+#pragma unroll
+      for (int c0 = 0; c0 < NR; c0 += NT) {
+        uint32_t z[NT], x[NT];
+        tmem_ld2<NT>(oz + c0, z, ox + c0, x);
+        if (c0 + NT == NR) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bars + kOFree);
+          if (lane == 0) mbar_arrive(bars + kOFree + k % C::kNO);
         }
-        uint32_t w[8];
 #pragma unroll
-        for (int g = 0; g < 8; ++g)
-          w[g] = packf2(fma2(ff, f2(x[2 * g], x[2 * g + 1]), f2(z[2 * g], z[2 * g + 1])));
-        if (i < nv) {
-          const int left = db - col - c0;
-          if (wide && left > 0) {
-            st_global_32(o + c0, w);
-          } else {
-            if (left > 0) *reinterpret_cast<uint4*>(o + c0) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (left > 8) *reinterpret_cast<uint4*>(o + c0 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int g = 0; g < NT; g += 16) {
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            w[e] = packf2(fma2(ff, f2(x[g + 2 * e], x[g + 2 * e + 1]), f2(z[g + 2 * e], z[g + 2 * e + 1])));
+          if (i < nv && c0 + g < left) {
+            if (wide) {
+              st_global_32(o + c0 + g, w);
+            } else {
+              *reinterpret_cast<uint4*>(o + c0 + g) = make_uint4(w[0], w[1], w[2], w[3]);
+              if (c0 + g + 8 < left) *reinterpret_cast<uint4*>(o + c0 + g + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         }
       }
+      o += o_step;
     };
     for (int k = 0; k < n; ++k) {
       if (k > 0) update(k - 1);
@@ -540,11 +606,10 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       float* dst = STATE ? jb.local + ((size_t)u * a.segs + seg) * dd : jb.fin + u * dd;
       if (live && row < da) {
 #pragma unroll
-        for (int c = 0; c < NR; c += 2)
-          if (col + c < db) {
-            dst[!STATE && trans ? (size_t)(col + c) * da + row : (size_t)row * db + col + c] = f2_lo(R[c / 2]);
-            dst[!STATE && trans ? (size_t)(col + c + 1) * da + row : (size_t)row * db + col + c + 1] = f2_hi(R[c / 2]);
-          }
+        for (int c = 0; c < NR; c += 4)
+          if (col + c < db)   // a returned state is never a transposed one
+            *reinterpret_cast<float4*>(dst + (size_t)row * db + col + c) =
+                make_float4(f2_lo(R[c / 2]), f2_hi(R[c / 2]), f2_lo(R[c / 2 + 1]), f2_hi(R[c / 2 + 1]));
       }
     }
   }
@@ -603,13 +668,18 @@ bool maps(TcJob* t, const DecayArgs& a, const DecayJob& j, bool with_x) {
          make_tmap_tokens_bf16(&t->z, j.Z, j.db, a.N, a.heads, a.B, j.zs, kC);
 }
 
-template <int DP, bool STATE>
+template <int DP, bool STATE, int PARTS>
 cudaError_t run(const TcArgs& a, int units, int njobs, cudaStream_t st) {
-  using C = Cfg<DP, STATE>;
-  cudaError_t e = cudaFuncSetAttribute(k_decay_tc<DP, STATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  using C = Cfg<DP, STATE, PARTS>;
+  cudaError_t e = cudaFuncSetAttribute(k_decay_tc<DP, STATE, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  k_decay_tc<DP, STATE><<<dim3(units, a.segs, njobs), C::kThreads, C::kSmem, st>>>(a);
+  k_decay_tc<DP, STATE, PARTS><<<dim3(units, a.segs, njobs), C::kThreads, C::kSmem, st>>>(a);
   return cudaGetLastError();
+}
+template <bool STATE>
+cudaError_t run(const TcArgs& a, int dp, int parts, int units, int njobs, cudaStream_t st) {
+  if (dp == 64) return parts == 2 ? run<64, STATE, 2>(a, units, njobs, st) : run<64, STATE, 3>(a, units, njobs, st);
+  return parts == 2 ? run<128, STATE, 2>(a, units, njobs, st) : run<128, STATE, 3>(a, units, njobs, st);
 }
 
 }  // namespace
@@ -656,10 +726,11 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
   t.N = a.N;
   t.segs = sp.segs;
   t.seg_chunks = sp.seg_chunks;
-  int dp = 64;
+  int dp = 64, parts = 2;   // three parts of y's decayed rows where a state is returned
   for (int i = 0; i < a.njobs; ++i) {
     const DecayJob& j = a.job[i];
     if (j.da > 64 || j.db > 64) dp = 128;
+    if (j.fin) parts = 3;
   }
   const int dd = a.job[0].da * a.job[0].db;
   // states before the segments: run 0 forwards, and for the backward its last run (y = q, z = dO)
@@ -687,12 +758,11 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
       o.rev = j.rev;
       o.c_state = j.c_state;
       o.local = a.ws + i * states;
-      o.parts = j.fin ? 3 : 2;
       p.init[i] = j.init;
       p.rev[i] = j.rev;
       p.init_decays[i] = j.init_decays;
     }
-    const cudaError_t e = dp == 64 ? run<64, true>(t, units, ns, st) : run<128, true>(t, units, ns, st);
+    const cudaError_t e = run<true>(t, dp, parts, units, ns, st);
     if (e != cudaSuccess) return e;
     p.log_decay = a.log_decay;
     p.lengths = a.lengths;
@@ -721,12 +791,11 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
     o.trans = j.trans;
     o.init_decays = j.init_decays;
     o.fin_sub = j.fin_sub;
-    o.parts = j.fin ? 3 : 2;
     o.c_inter = j.c_inter;
     o.c_intra = j.c_intra;
     o.c_state = j.c_state;
   }
-  return dp == 64 ? run<64, false>(t, units, a.njobs, st) : run<128, false>(t, units, a.njobs, st);
+  return run<false>(t, dp, parts, units, a.njobs, st);
 }
 
 }  // namespace lfa
