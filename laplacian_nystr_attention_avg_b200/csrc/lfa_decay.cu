@@ -255,7 +255,8 @@ __global__ void __launch_bounds__(kStepT) k_decay_step(const __grid_constant__ D
 
 template <typename T>
 cudaError_t run_core(const DecayArgs& a, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(k_decay_core<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(CoreSmem));
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = raise_smem(k_decay_core<T>, (int)sizeof(CoreSmem), done);
   if (e != cudaSuccess) return e;
   int db = 0;
   for (int j = 0; j < a.njobs; ++j) db = a.job[j].db > db ? a.job[j].db : db;

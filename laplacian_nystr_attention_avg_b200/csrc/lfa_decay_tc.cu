@@ -671,7 +671,8 @@ bool maps(TcJob* t, const DecayArgs& a, const DecayJob& j, bool with_x) {
 template <int DP, bool STATE, int PARTS>
 cudaError_t run(const TcArgs& a, int units, int njobs, cudaStream_t st) {
   using C = Cfg<DP, STATE, PARTS>;
-  cudaError_t e = cudaFuncSetAttribute(k_decay_tc<DP, STATE, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = raise_smem(k_decay_tc<DP, STATE, PARTS>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   k_decay_tc<DP, STATE, PARTS><<<dim3(units, a.segs, njobs), C::kThreads, C::kSmem, st>>>(a);
   return cudaGetLastError();

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "lfa.h"
 
 namespace lfa {
@@ -94,9 +96,22 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st);
 cudaError_t decay_take_status(int* out, cudaStream_t st);
 cudaError_t launch_decay_step(const DecayStepArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t st);
-size_t norm_workspace_floats(int B, int N, int C, int G, int backward);
+size_t norm_workspace_floats(int B, int N, int C, int G, int dtype, int backward);
 cudaError_t launch_norm(const NormArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_norm_backward(const NormArgs& a, int dtype, cudaStream_t st);
+
+// the dynamic shared memory limit of a kernel, raised once per device; `done` is that kernel's own
+template <typename K>
+inline cudaError_t raise_smem(K kernel, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // ---- small device helpers shared by the two files -------------------------------------------------
 // decays below exp(-1e4) are zero to every power but 0; the bound keeps 0 * inf out of exp(n ld)

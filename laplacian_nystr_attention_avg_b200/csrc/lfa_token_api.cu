@@ -250,16 +250,17 @@ static lfa_status check_norm(const lfa_norm_config* c) {
   if (!(c->eps > 0.f) || !isfinite(c->eps)) return LFA_ERR_INVALID_ARG;
   if (c->act < LFA_ACT_NONE || c->act > LFA_ACT_GELU) return LFA_ERR_INVALID_ARG;
   if (c->dtype != LFA_F32 && c->dtype != LFA_BF16) return LFA_ERR_UNSUPPORTED;
-  // row and (sample, group) counts, and one sample's elements, fit 31 bits
-  if ((long long)c->B * c->N >= (1ll << 31) || (long long)c->B * c->groups >= (1ll << 31) ||
-      (long long)c->N * c->C >= (1ll << 31))
+  // row and (sample, group) counts, and one sample's elements, fit 30 bits
+  if (c->C > (1 << 20)) return LFA_ERR_UNSUPPORTED;
+  if ((long long)c->B * c->N > (1ll << 30) || (long long)c->B * c->groups > (1ll << 30) ||
+      (long long)c->N * c->C > (1ll << 30))
     return LFA_ERR_UNSUPPORTED;
   return LFA_OK;
 }
 
 size_t lfa_group_norm_workspace_size(const lfa_norm_config* cfg, int backward) {
   if (check_norm(cfg) != LFA_OK) return 0;
-  const size_t n = lfa::norm_workspace_floats(cfg->B, cfg->N, cfg->C, cfg->groups, backward) * sizeof(float);
+  const size_t n = lfa::norm_workspace_floats(cfg->B, cfg->N, cfg->C, cfg->groups, cfg->dtype, backward) * sizeof(float);
   return n < 256 ? 256 : (n + 255) / 256 * 256;
 }
 

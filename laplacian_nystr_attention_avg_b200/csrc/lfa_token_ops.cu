@@ -1,4 +1,8 @@
 // Rotary positions (lfa_rotary) and group norm with an activation (lfa_group_norm and its backward).
+#include <string.h>
+
+#include <type_traits>
+
 #include "lfa_internal.h"
 #include "lfa_token.h"
 
@@ -112,121 +116,758 @@ void run_rotary(const RotaryArgs& a, cudaStream_t st) {
 }
 
 // ---- group norm ---------------------------------------------------------------------------------------
-constexpr int kNT = 256;
+// Two ways through the data. Small groups (N C/G elements that one warp or one block holds in registers) are read
+// once: a team of threads per (sample, group) forms the mean, the variance about it and the output. Larger ones
+// take three launches: per-channel sums of row chunks, their combination per group, and the output; the second
+// reading comes from the 126 MB L2 as far as the tensor fits there. All sums are joined in a fixed order.
+constexpr int kNT = 256;         // threads per block
+constexpr int kNRows = 8;        // rows a thread has in flight
+constexpr int kMaxChunks = 64;   // row chunks per sample (large groups)
 
-__device__ __forceinline__ float act_f(float z, int act) {
-  if (act == LFA_ACT_SILU) return z / (1.f + expf(-z));
-  if (act == LFA_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+template <int ACT>
+__device__ __forceinline__ float act_f(float z) {
+  if (ACT == LFA_ACT_SILU) return z * sigmoid_f(z);
+  if (ACT == LFA_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
   return z;
 }
-__device__ __forceinline__ float act_slope(float z, int act) {
-  if (act == LFA_ACT_SILU) {
-    const float p = 1.f / (1.f + expf(-z));
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if (ACT == LFA_ACT_SILU) {
+    const float p = sigmoid_f(z);
     return p * fmaf(z, 1.f - p, 1.f);
   }
-  if (act == LFA_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * expf(-0.5f * z * z);
+  if (ACT == LFA_ACT_GELU)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
   return 1.f;
 }
 
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float s[kNT / 32];
+// VB bytes of a row, and its elements in fp32
+template <int VB>
+struct Raw {
+  uint32_t w[(VB + 3) / 4];
+};
+template <int VB>
+__device__ __forceinline__ Raw<VB> raw_load(const void* p) {
+  Raw<VB> r;
+  if constexpr (VB == 16) *reinterpret_cast<uint4*>(r.w) = *reinterpret_cast<const uint4*>(p);
+  if constexpr (VB == 8) *reinterpret_cast<uint2*>(r.w) = *reinterpret_cast<const uint2*>(p);
+  if constexpr (VB == 4) r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  if constexpr (VB == 2) r.w[0] = *reinterpret_cast<const uint16_t*>(p);
+  return r;
+}
+template <int VB>
+__device__ __forceinline__ void raw_store(void* p, const Raw<VB>& r) {
+  if constexpr (VB == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.w);
+  if constexpr (VB == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(r.w);
+  if constexpr (VB == 4) *reinterpret_cast<uint32_t*>(p) = r.w[0];
+  if constexpr (VB == 2) *reinterpret_cast<uint16_t*>(p) = (uint16_t)r.w[0];
+}
+template <typename T, int VB>
+__device__ __forceinline__ float raw_get(const Raw<VB>& r, int i) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(r.w[i]);
+  return __uint_as_float((i & 1) ? (r.w[i >> 1] & 0xffff0000u) : (r.w[i >> 1] << 16));
+}
+template <typename T, int VB>
+__device__ __forceinline__ Raw<VB> raw_make(const float* v) {
+  Raw<VB> r;
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float r = 0.f;
-  for (int i = 0; i < kNT / 32; ++i) r += s[i];
+    for (int i = 0; i < VB / 4; ++i) r.w[i] = __float_as_uint(v[i]);
+  } else if constexpr (VB == 2) {
+    const __nv_bfloat16 b = __float2bfloat16_rn(v[0]);
+    r.w[0] = *reinterpret_cast<const uint16_t*>(&b);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VB / 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      r.w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
   return r;
 }
 
-// one CTA per (sample, group): mean, then the variance about it, then the output
-template <typename T>
-__global__ void __launch_bounds__(kNT) k_norm(const __grid_constant__ NormArgs a) {
-  const int b = blockIdx.x / a.G, g = blockIdx.x % a.G, dg = a.C / a.G;
-  const long long n = (long long)a.N * dg;
-  const T* x = static_cast<const T*>(a.x) + (size_t)b * a.N * a.C + g * dg;
-  T* y = static_cast<T*>(a.y) + (size_t)b * a.N * a.C + g * dg;
-  float s = 0.f;
-  for (long long e = threadIdx.x; e < n; e += kNT) s += to_f<T>(x[e / dg * a.C + e % dg]);
-  const float mean = block_sum(s) / (float)n;
-  s = 0.f;
-  for (long long e = threadIdx.x; e < n; e += kNT) {
-    const float d = to_f<T>(x[e / dg * a.C + e % dg]) - mean;
-    s = fmaf(d, d, s);
-  }
-  const float rstd = rsqrtf(block_sum(s) / (float)n + a.eps);
-  for (long long e = threadIdx.x; e < n; e += kNT) {
-    const int c = (int)(e % dg);
-    const size_t at = (size_t)(e / dg) * a.C + c;
-    float z = (to_f<T>(x[at]) - mean) * rstd;
-    z = z * (a.gamma ? a.gamma[g * dg + c] : 1.f) + (a.beta ? a.beta[g * dg + c] : 0.f);
-    y[at] = from_f<T>(act_f(z, a.act));
-  }
-  if (threadIdx.x == 0 && a.mean) {
-    a.mean[blockIdx.x] = mean;
-    a.rstd[blockIdx.x] = rstd;
+// sum over a team of T lanes (a power of two up to 32), or with T = 0 over the block
+template <bool BLOCK>
+__device__ __forceinline__ float team_sum(float v, int T, float* s) {
+  if constexpr (!BLOCK) {
+    for (int o = T >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  } else {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float r = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNT / 32; ++i) r += s[i];
+    return r;
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kNT) k_norm_dx(const __grid_constant__ NormArgs a) {
-  const int b = blockIdx.x / a.G, g = blockIdx.x % a.G, dg = a.C / a.G;
-  const long long n = (long long)a.N * dg;
+struct SmallArgs {
+  NormArgs a;
+  int T, dv, nvec;     // threads of a team (0: the block), vectors of a group in a row and in all
+  uint32_t magic;      // j / dv = umulhi(j, magic) for dv > 1
+};
+
+// Where a team's vector j lies: element offset from the group's first element, and its first channel in the group
+template <typename T, int VB>
+__device__ __forceinline__ void place(const SmallArgs& s, int j, long long& off, int& c) {
+  constexpr int V = VB / sizeof(T);
+  const int n = s.dv > 1 ? (int)__umulhi((uint32_t)j, s.magic) : j;
+  c = (j - n * s.dv) * V;
+  off = (long long)n * s.a.C + c;
+}
+
+template <typename T, int VB, int E, bool BLOCK, int ACT>
+__global__ void __launch_bounds__(kNT) k_norm_small(const __grid_constant__ SmallArgs s) {
+  __shared__ float red[kNT / 32];
+  constexpr int V = VB / sizeof(T);
+  const NormArgs& a = s.a;
+  const int team = BLOCK ? kNT : s.T, tl = threadIdx.x & (team - 1);
+  const long long id = BLOCK ? blockIdx.x : (long long)blockIdx.x * (kNT / s.T) + threadIdx.x / s.T;
+  const bool on = id < (long long)a.B * a.G;
+  const int b = on ? (int)(id / a.G) : 0, g = on ? (int)(id % a.G) : 0, dg = a.C / a.G;
+  const size_t base = (size_t)b * a.N * a.C + g * dg;
+  const T* x = static_cast<const T*>(a.x) + base;
+  Raw<VB> v[E];
+  float sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int j = tl + e * team;
+    if (on && j < s.nvec) {
+      long long off;
+      int c;
+      place<T, VB>(s, j, off, c);
+      v[e] = raw_load<VB>(x + off);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (on && tl + e * team < s.nvec)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += raw_get<T>(v[e], i);
+  const float n = (float)(s.nvec * V), mean = team_sum<BLOCK>(sum, s.T, red) / n;
+  sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (on && tl + e * team < s.nvec)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float d = raw_get<T>(v[e], i) - mean;
+        sum = fmaf(d, d, sum);
+      }
+  const float rstd = rsqrtf(team_sum<BLOCK>(sum, s.T, red) / n + a.eps);
+  if (!on) return;
+  if (tl == 0 && a.mean) {
+    a.mean[id] = mean;
+    a.rstd[id] = rstd;
+  }
+  T* y = static_cast<T*>(a.y) + base;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int j = tl + e * team;
+    if (j >= s.nvec) break;
+    long long off;
+    int c;
+    place<T, VB>(s, j, off, c);
+    float o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float z = (raw_get<T>(v[e], i) - mean) * rstd;
+      if (a.gamma) z = fmaf(z, a.gamma[g * dg + c + i], a.beta[g * dg + c + i]);
+      o[i] = act_f<ACT>(z);
+    }
+    raw_store<VB>(y + off, raw_make<T, VB>(o));
+  }
+}
+
+template <typename T, int VB, int E, bool BLOCK, int ACT>
+__global__ void __launch_bounds__(kNT) k_norm_small_dx(const __grid_constant__ SmallArgs s) {
+  __shared__ float red[kNT / 32];
+  constexpr int V = VB / sizeof(T);
+  const NormArgs& a = s.a;
+  const int team = BLOCK ? kNT : s.T, tl = threadIdx.x & (team - 1);
+  const long long id = BLOCK ? blockIdx.x : (long long)blockIdx.x * (kNT / s.T) + threadIdx.x / s.T;
+  const bool on = id < (long long)a.B * a.G;
+  const int b = on ? (int)(id / a.G) : 0, g = on ? (int)(id % a.G) : 0, dg = a.C / a.G;
   const size_t base = (size_t)b * a.N * a.C + g * dg;
   const T* x = static_cast<const T*>(a.x) + base;
   const T* dy = static_cast<const T*>(a.dy) + base;
-  T* dx = static_cast<T*>(a.y) + base;
-  const float mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
+  const float mean = on ? a.mean[id] : 0.f, rstd = on ? a.rstd[id] : 0.f;
+  Raw<VB> v[E], w[E];
   float s1 = 0.f, s2 = 0.f;
-  for (int pass = 0; pass < 2; ++pass) {
-    const float m1 = pass ? block_sum(s1) / (float)n : 0.f, m2 = pass ? block_sum(s2) / (float)n : 0.f;
-    for (long long e = threadIdx.x; e < n; e += kNT) {
-      const int c = (int)(e % dg);
-      const size_t at = (size_t)(e / dg) * a.C + c;
-      const float ga = a.gamma ? a.gamma[g * dg + c] : 1.f, be = a.beta ? a.beta[g * dg + c] : 0.f;
-      const float xh = (to_f<T>(x[at]) - mean) * rstd;
-      const float gz = ga * to_f<T>(dy[at]) * act_slope(fmaf(xh, ga, be), a.act);
-      if (pass) {
-        dx[at] = from_f<T>(rstd * (gz - m1 - xh * m2));
-      } else {
-        s1 += gz;
-        s2 = fmaf(gz, xh, s2);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int j = tl + e * team;
+    if (on && j < s.nvec) {
+      long long off;
+      int c;
+      place<T, VB>(s, j, off, c);
+      v[e] = raw_load<VB>(x + off);
+      w[e] = raw_load<VB>(dy + off);
+    }
+  }
+  auto grad = [&](int e, int i, int c, float& xh) {
+    xh = (raw_get<T>(v[e], i) - mean) * rstd;
+    float z = xh, ga = 1.f;
+    if (a.gamma) {
+      ga = a.gamma[g * dg + c + i];
+      z = fmaf(xh, ga, a.beta[g * dg + c + i]);
+    }
+    return ga * raw_get<T>(w[e], i) * act_slope<ACT>(z);
+  };
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int j = tl + e * team;
+    if (on && j < s.nvec) {
+      long long off;
+      int c;
+      place<T, VB>(s, j, off, c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float xh;
+        const float d = grad(e, i, c, xh);
+        s1 += d;
+        s2 = fmaf(d, xh, s2);
       }
+    }
+  }
+  const float n = (float)(s.nvec * V);
+  const float m1 = team_sum<BLOCK>(s1, s.T, red) / n, m2 = team_sum<BLOCK>(s2, s.T, red) / n;
+  if (!on) return;
+  T* dx = static_cast<T*>(a.y) + base;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int j = tl + e * team;
+    if (j >= s.nvec) break;
+    long long off;
+    int c;
+    place<T, VB>(s, j, off, c);
+    float o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float xh;
+      const float d = grad(e, i, c, xh);
+      o[i] = rstd * (d - m1 - xh * m2);
+    }
+    raw_store<VB>(dx + off, raw_make<T, VB>(o));
+  }
+}
+
+// ---- large groups: rows in chunks, a thread takes the same V channels of every rl-th row -------------------
+struct RowArgs {
+  NormArgs a;
+  int cw, rl, colblocks;     // vector columns and row lanes of a block, blocks side by side
+  int chunks, chunk_rows;    // per sample, or over all rows (flat)
+  float* part;               // [B or 1][chunks][2][C]
+};
+struct Lane {   // this thread's place
+  int c, ty, b, r0, r1;
+  bool on;
+};
+template <int V>
+__device__ __forceinline__ Lane lane_of(const RowArgs& p, int rows) {
+  Lane l;
+  const int tx = threadIdx.x % p.cw, col = blockIdx.y * p.cw + tx;
+  l.ty = threadIdx.x / p.cw;
+  l.c = col * V;
+  l.on = l.ty < p.rl && l.c < p.a.C;
+  l.b = blockIdx.x / p.chunks;
+  l.r0 = (blockIdx.x - l.b * p.chunks) * p.chunk_rows;
+  l.r1 = min(l.r0 + p.chunk_rows, rows);
+  return l;
+}
+
+// per-channel mean and sum of squares about it of a chunk's rows
+template <typename T, int VB>
+__global__ void __launch_bounds__(kNT) k_norm_stats(const __grid_constant__ RowArgs p) {
+  constexpr int V = VB / sizeof(T);
+  extern __shared__ float sm[];   // [rl][cw V] means, the same of squares
+  const NormArgs& a = p.a;
+  const Lane l = lane_of<V>(p, a.N);
+  float m[V] = {}, q[V] = {};
+  int cnt = 0;
+  if (l.on) {
+    const T* x = static_cast<const T*>(a.x) + (size_t)l.b * a.N * a.C + l.c;
+    for (int r = l.r0 + l.ty; r < l.r1; r += p.rl * kNRows) {
+      Raw<VB> v[kNRows];
+      int k = 0;
+#pragma unroll
+      for (int e = 0; e < kNRows; ++e)
+        if (r + e * p.rl < l.r1) {
+          v[e] = raw_load<VB>(x + (size_t)(r + e * p.rl) * a.C);
+          ++k;
+        }
+      // the block's mean and squares, joined to those so far (parallel form of the running variance)
+      const float inv = 1.f / (float)k, fr = (float)k / (float)(cnt + k), wt = (float)cnt * fr;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < kNRows; ++e)
+          if (e < k) s += raw_get<T>(v[e], i);
+        s *= inv;
+        float d2 = 0.f;
+#pragma unroll
+        for (int e = 0; e < kNRows; ++e)
+          if (e < k) {
+            const float d = raw_get<T>(v[e], i) - s;
+            d2 = fmaf(d, d, d2);
+          }
+        const float d = s - m[i];
+        q[i] += fmaf(d * d, wt, d2);
+        m[i] = fmaf(d, fr, m[i]);
+      }
+      cnt += k;
+    }
+  }
+  const int width = p.cw * V, at = l.ty * width + (threadIdx.x % p.cw) * V;
+  float* sq = sm + p.rl * width;
+  if (l.ty < p.rl)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      sm[at + i] = m[i];
+      sq[at + i] = q[i];
+    }
+  __syncthreads();
+  const int rows = l.r1 - l.r0;
+  float* out = p.part + (size_t)blockIdx.x * 2 * a.C;
+  for (int c = threadIdx.x; c < width; c += kNT) {
+    const int ch = blockIdx.y * width + c;
+    if (ch >= a.C) continue;
+    float mean = 0.f, sqs = 0.f;
+    int n = 0;
+    for (int y = 0; y < p.rl && y < rows; ++y) {
+      const int k = (rows - y + p.rl - 1) / p.rl;   // rows of lane y
+      const float d = sm[y * width + c] - mean, fr = (float)k / (float)(n + k);
+      sqs += sq[y * width + c] + d * d * (float)n * fr;
+      mean = fmaf(d, fr, mean);
+      n += k;
+    }
+    out[ch] = mean;
+    out[a.C + ch] = sqs;
+  }
+}
+
+// one block per (sample, group): mean and 1 / deviation from the chunks' channels
+__global__ void __launch_bounds__(kNT) k_norm_group(const __grid_constant__ RowArgs p) {
+  __shared__ float red[kNT / 32];
+  const NormArgs& a = p.a;
+  const int b = blockIdx.x / a.G, g = blockIdx.x % a.G, dg = a.C / a.G, cells = p.chunks * dg;
+  const float* part = p.part + (size_t)b * p.chunks * 2 * a.C + g * dg;
+  const float total = (float)a.N * (float)dg;
+  float s = 0.f;
+  for (int e = threadIdx.x; e < cells; e += kNT) {
+    const int k = e / dg;
+    s = fmaf(part[(size_t)k * 2 * a.C + e % dg], (float)(min(a.N, (k + 1) * p.chunk_rows) - k * p.chunk_rows), s);
+  }
+  const float mean = team_sum<true>(s, 0, red) / total;
+  s = 0.f;
+  for (int e = threadIdx.x; e < cells; e += kNT) {
+    const int k = e / dg;
+    const float* at = part + (size_t)k * 2 * a.C + e % dg;
+    const float d = at[0] - mean;
+    s += fmaf(d * d, (float)(min(a.N, (k + 1) * p.chunk_rows) - k * p.chunk_rows), at[a.C]);
+  }
+  s = team_sum<true>(s, 0, red);
+  if (threadIdx.x == 0) {
+    a.mean[blockIdx.x] = mean;
+    a.rstd[blockIdx.x] = rsqrtf(s / total + a.eps);
+  }
+}
+
+// the channels' constants of a thread
+template <int V>
+struct Chan {
+  float mean[V], rstd[V], ga[V], be[V];
+};
+template <int V>
+__device__ __forceinline__ void chan_affine(const NormArgs& a, int c, Chan<V>& k) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    k.ga[i] = a.gamma ? a.gamma[c + i] : 1.f;
+    k.be[i] = a.beta ? a.beta[c + i] : 0.f;
+  }
+}
+template <int V>
+__device__ __forceinline__ void chan_stats(const NormArgs& a, int b, int c, int dg, Chan<V>& k) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const size_t at = (size_t)b * a.G + (c + i) / dg;
+    k.mean[i] = a.mean[at];
+    k.rstd[i] = a.rstd[at];
+  }
+}
+
+template <typename T, int VB, int ACT>
+__global__ void __launch_bounds__(kNT) k_norm_apply(const __grid_constant__ RowArgs p) {
+  constexpr int V = VB / sizeof(T);
+  const NormArgs& a = p.a;
+  const Lane l = lane_of<V>(p, a.N);
+  if (!l.on) return;
+  Chan<V> k;
+  chan_affine(a, l.c, k);
+  chan_stats(a, l.b, l.c, a.C / a.G, k);
+#pragma unroll
+  for (int i = 0; i < V; ++i) k.ga[i] *= k.rstd[i];
+  const size_t base = (size_t)l.b * a.N * a.C + l.c;
+  const T* x = static_cast<const T*>(a.x) + base;
+  T* y = static_cast<T*>(a.y) + base;
+  for (int r = l.r0 + l.ty; r < l.r1; r += p.rl * kNRows) {
+    Raw<VB> v[kNRows];
+#pragma unroll
+    for (int e = 0; e < kNRows; ++e)
+      if (r + e * p.rl < l.r1) v[e] = raw_load<VB>(x + (size_t)(r + e * p.rl) * a.C);
+#pragma unroll
+    for (int e = 0; e < kNRows; ++e)
+      if (r + e * p.rl < l.r1) {
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = act_f<ACT>(fmaf(raw_get<T>(v[e], i) - k.mean[i], k.ga[i], k.be[i]));
+        raw_store<VB>(y + (size_t)(r + e * p.rl) * a.C, raw_make<T, VB>(o));
+      }
+  }
+}
+
+// per-channel sums of dz and dz xhat over a chunk's rows: of one sample, or (FLAT) of all samples' rows in turn
+template <typename T, int VB, int ACT, bool FLAT>
+__global__ void __launch_bounds__(kNT) k_norm_bsum(const __grid_constant__ RowArgs p) {
+  constexpr int V = VB / sizeof(T);
+  constexpr int R = 4;   // rows in flight, of two tensors
+  extern __shared__ float sm[];
+  const NormArgs& a = p.a;
+  const int dg = a.C / a.G;
+  const Lane l = lane_of<V>(p, FLAT ? a.B * a.N : a.N);
+  float s1[V] = {}, s2[V] = {};
+  if (l.on) {
+    Chan<V> k;
+    chan_affine(a, l.c, k);
+    if (!FLAT) chan_stats(a, l.b, l.c, dg, k);
+    const size_t base = (size_t)l.b * a.N * a.C + l.c;
+    const T* x = static_cast<const T*>(a.x) + base;
+    const T* dy = static_cast<const T*>(a.dy) + base;
+    for (int r = l.r0 + l.ty; r < l.r1; r += p.rl * R) {
+      Raw<VB> v[R], w[R];
+#pragma unroll
+      for (int e = 0; e < R; ++e)
+        if (r + e * p.rl < l.r1) {
+          v[e] = raw_load<VB>(x + (size_t)(r + e * p.rl) * a.C);
+          w[e] = raw_load<VB>(dy + (size_t)(r + e * p.rl) * a.C);
+        }
+#pragma unroll
+      for (int e = 0; e < R; ++e)
+        if (r + e * p.rl < l.r1) {
+          if (FLAT) chan_stats(a, (r + e * p.rl) / a.N, l.c, dg, k);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float xh = (raw_get<T>(v[e], i) - k.mean[i]) * k.rstd[i];
+            const float dz = raw_get<T>(w[e], i) * act_slope<ACT>(fmaf(xh, k.ga[i], k.be[i]));
+            s1[i] += dz;
+            s2[i] = fmaf(dz, xh, s2[i]);
+          }
+        }
+    }
+  }
+  const int width = p.cw * V, at = l.ty * width + (threadIdx.x % p.cw) * V;
+  float* sq = sm + p.rl * width;
+  if (l.ty < p.rl)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      sm[at + i] = s1[i];
+      sq[at + i] = s2[i];
+    }
+  __syncthreads();
+  float* out = p.part + (size_t)blockIdx.x * 2 * a.C;
+  for (int c = threadIdx.x; c < width; c += kNT) {
+    const int ch = blockIdx.y * width + c;
+    if (ch >= a.C) continue;
+    float t1 = 0.f, t2 = 0.f;
+    for (int y = 0; y < p.rl; ++y) {
+      t1 += sm[y * width + c];
+      t2 += sq[y * width + c];
+    }
+    out[ch] = t1;
+    out[a.C + ch] = t2;
+  }
+}
+
+// Blocks below groups: m1, m2 of one (sample, group) from its channels' sums. The rest: dbeta, dgamma of 32
+// channels, 8 lanes over the records.
+__global__ void __launch_bounds__(kNT) k_norm_bjoin(const __grid_constant__ RowArgs p, int groups, int records,
+                                                     float* m12) {
+  __shared__ float red[2][kNT];
+  const NormArgs& a = p.a;
+  if ((int)blockIdx.x < groups) {
+    const int b = blockIdx.x / a.G, g = blockIdx.x % a.G, dg = a.C / a.G, cells = p.chunks * dg;
+    const float* part = p.part + (size_t)b * p.chunks * 2 * a.C + g * dg;
+    float s1 = 0.f, s2 = 0.f;
+    for (int e = threadIdx.x; e < cells; e += kNT) {
+      const int k = e / dg, c = e % dg;
+      const float ga = a.gamma ? a.gamma[g * dg + c] : 1.f;
+      s1 = fmaf(ga, part[(size_t)k * 2 * a.C + c], s1);
+      s2 = fmaf(ga, part[(size_t)k * 2 * a.C + a.C + c], s2);
+    }
+    const float n = (float)a.N * (float)dg;
+    s1 = team_sum<true>(s1, 0, red[0]);
+    s2 = team_sum<true>(s2, 0, red[1]);
+    if (threadIdx.x == 0) {
+      m12[2 * blockIdx.x] = s1 / n;
+      m12[2 * blockIdx.x + 1] = s2 / n;
+    }
+  } else {
+    const int c = ((int)blockIdx.x - groups) * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+    float s1 = 0.f, s2 = 0.f;
+    if (c < a.C)
+      for (int r = y; r < records; r += kNT / 32) {
+        s1 += p.part[(size_t)r * 2 * a.C + c];
+        s2 += p.part[(size_t)r * 2 * a.C + a.C + c];
+      }
+    red[0][threadIdx.x] = s1;
+    red[1][threadIdx.x] = s2;
+    __syncthreads();
+    if (y == 0 && c < a.C) {
+      for (int i = 1; i < kNT / 32; ++i) {
+        s1 += red[0][32 * i + threadIdx.x];
+        s2 += red[1][32 * i + threadIdx.x];
+      }
+      a.dbeta[c] = s1;
+      a.dgamma[c] = s2;
     }
   }
 }
 
-// one CTA per channel
-template <typename T>
-__global__ void __launch_bounds__(kNT) k_norm_dparam(const __grid_constant__ NormArgs a) {
-  const int c = blockIdx.x, g = c / (a.C / a.G);
-  const float ga = a.gamma ? a.gamma[c] : 1.f, be = a.beta ? a.beta[c] : 0.f;
-  float s1 = 0.f, s2 = 0.f;
-  for (long long r = threadIdx.x; r < (long long)a.B * a.N; r += kNT) {
-    const int b = (int)(r / a.N);
-    const float xh = (to_f<T>(static_cast<const T*>(a.x)[r * a.C + c]) - a.mean[b * a.G + g]) * a.rstd[b * a.G + g];
-    const float dz = to_f<T>(static_cast<const T*>(a.dy)[r * a.C + c]) * act_slope(fmaf(xh, ga, be), a.act);
-    s1 += dz;
-    s2 = fmaf(dz, xh, s2);
+template <typename T, int VB, int ACT>
+__global__ void __launch_bounds__(kNT) k_norm_dx(const __grid_constant__ RowArgs p, const float* m12) {
+  constexpr int V = VB / sizeof(T);
+  constexpr int R = 4;
+  const NormArgs& a = p.a;
+  const int dg = a.C / a.G;
+  const Lane l = lane_of<V>(p, a.N);
+  if (!l.on) return;
+  Chan<V> k;
+  chan_affine(a, l.c, k);
+  chan_stats(a, l.b, l.c, dg, k);
+  float m1[V], m2[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const size_t at = 2 * ((size_t)l.b * a.G + (l.c + i) / dg);
+    m1[i] = m12[at];
+    m2[i] = m12[at + 1];
   }
-  s1 = block_sum(s1);
-  s2 = block_sum(s2);
-  if (threadIdx.x == 0) {
-    a.dbeta[c] = s1;
-    a.dgamma[c] = s2;
+  const size_t base = (size_t)l.b * a.N * a.C + l.c;
+  const T* x = static_cast<const T*>(a.x) + base;
+  const T* dy = static_cast<const T*>(a.dy) + base;
+  T* dx = static_cast<T*>(a.y) + base;
+  for (int r = l.r0 + l.ty; r < l.r1; r += p.rl * R) {
+    Raw<VB> v[R], w[R];
+#pragma unroll
+    for (int e = 0; e < R; ++e)
+      if (r + e * p.rl < l.r1) {
+        v[e] = raw_load<VB>(x + (size_t)(r + e * p.rl) * a.C);
+        w[e] = raw_load<VB>(dy + (size_t)(r + e * p.rl) * a.C);
+      }
+#pragma unroll
+    for (int e = 0; e < R; ++e)
+      if (r + e * p.rl < l.r1) {
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float xh = (raw_get<T>(v[e], i) - k.mean[i]) * k.rstd[i];
+          const float d = k.ga[i] * raw_get<T>(w[e], i) * act_slope<ACT>(fmaf(xh, k.ga[i], k.be[i]));
+          o[i] = k.rstd[i] * (d - m1[i] - xh * m2[i]);
+        }
+        raw_store<VB>(dx + (size_t)(r + e * p.rl) * a.C, raw_make<T, VB>(o));
+      }
   }
 }
 
+// ---- choice of the way, by sizes alone -----------------------------------------------------------------
+// bytes of a vector: the widest power of two up to 16 that divides n elements
+int vec_bytes(int n, int es) {
+  int v = es;
+  while (v < 16 && n % (2 * v / es) == 0) v *= 2;
+  return v;
+}
+
+struct Plan {
+  bool small;
+  int VB, E;
+  SmallArgs s;
+  RowArgs r;           // large groups; small ones: the flat sums of the backward
+  size_t floats;       // workspace
+  size_t m12, stats;   // offsets in it
+};
+
+Plan plan_norm(int B, int N, int C, int G, int es, bool backward) {
+  Plan p;
+  memset(&p, 0, sizeof(p));
+  const int dg = C / G;
+  p.VB = vec_bytes(dg, es);
+  const long long nvec = (long long)N * dg * es / p.VB;
+  // a warp's team holds up to 8 vectors a thread (2 tensors: 4), a block's as well
+  const int cap = backward ? 4 : 8;
+  p.small = nvec <= (long long)kNT * cap;
+  if (p.small) {
+    p.s.dv = dg * es / p.VB;
+    p.s.nvec = (int)nvec;
+    p.s.magic = p.s.dv > 1 ? (uint32_t)(((1ull << 32) + p.s.dv - 1) / p.s.dv) : 0;
+    if (nvec <= 32 * cap) {
+      p.s.T = 1;
+      while (p.s.T < 32 && p.s.T < nvec) p.s.T *= 2;
+      p.E = nvec <= p.s.T ? 1 : cap;
+    } else {
+      p.s.T = 0;
+      p.E = cap;
+    }
+  }
+  // rows in chunks
+  RowArgs& r = p.r;
+  const int VB = p.small ? vec_bytes(C, es) : (p.VB = vec_bytes(C, es)), cv = C * es / VB;
+  r.cw = cv <= 256 ? cv : 128;
+  r.rl = kNT / r.cw;
+  r.colblocks = ceil_div(cv, r.cw);
+  const long long rows = p.small ? (long long)B * N : N;
+  const int samples = p.small ? 1 : B;
+  long long want = ceil_div(148 * 6, samples * r.colblocks < 1000 ? samples * r.colblocks : 1000);
+  const long long most = (rows + r.rl * kNRows - 1) / (r.rl * kNRows);
+  if (want > most) want = most;
+  if (want < 1) want = 1;
+  if (!p.small && want > kMaxChunks) want = kMaxChunks;
+  r.chunk_rows = (int)((rows + want - 1) / want);
+  r.chunks = (int)((rows + r.chunk_rows - 1) / r.chunk_rows);
+  if (!p.small || backward) p.floats = (size_t)samples * r.chunks * 2 * C;
+  p.m12 = p.floats;
+  if (!p.small && backward) p.floats += 2 * (size_t)B * G;
+  p.stats = p.floats;
+  if (!p.small && !backward) p.floats += 2 * (size_t)B * G;
+  return p;
+}
+
+template <typename T, int VB, int ACT>
+void small_forward(const Plan& p, cudaStream_t st) {
+  const long long teams = (long long)p.s.a.B * p.s.a.G;
+  if (p.s.T == 0) {
+    k_norm_small<T, VB, 8, true, ACT><<<(unsigned)teams, kNT, 0, st>>>(p.s);
+  } else {
+    const unsigned grid = (unsigned)((teams + kNT / p.s.T - 1) / (kNT / p.s.T));
+    if (p.E == 1)
+      k_norm_small<T, VB, 1, false, ACT><<<grid, kNT, 0, st>>>(p.s);
+    else
+      k_norm_small<T, VB, 8, false, ACT><<<grid, kNT, 0, st>>>(p.s);
+  }
+}
+template <typename T, int VB, int ACT>
+void small_backward(const Plan& p, cudaStream_t st) {
+  const long long teams = (long long)p.s.a.B * p.s.a.G;
+  if (p.s.T == 0) {
+    k_norm_small_dx<T, VB, 4, true, ACT><<<(unsigned)teams, kNT, 0, st>>>(p.s);
+  } else {
+    const unsigned grid = (unsigned)((teams + kNT / p.s.T - 1) / (kNT / p.s.T));
+    if (p.E == 1)
+      k_norm_small_dx<T, VB, 1, false, ACT><<<grid, kNT, 0, st>>>(p.s);
+    else
+      k_norm_small_dx<T, VB, 4, false, ACT><<<grid, kNT, 0, st>>>(p.s);
+  }
+}
+template <typename T, int VB>
+size_t row_smem(const RowArgs& r) { return 2 * sizeof(float) * r.rl * r.cw * (VB / sizeof(T)); }
+
+template <typename T, int VB, int ACT>
+void large_forward(const Plan& p, cudaStream_t st) {
+  const RowArgs& r = p.r;
+  const dim3 grid(r.chunks * r.a.B, r.colblocks);
+  k_norm_stats<T, VB><<<grid, kNT, row_smem<T, VB>(r), st>>>(r);
+  k_norm_group<<<r.a.B * r.a.G, kNT, 0, st>>>(r);
+  k_norm_apply<T, VB, ACT><<<grid, kNT, 0, st>>>(r);
+}
+template <typename T, int VB, int ACT, bool FLAT>
+void channel_sums(const Plan& p, cudaStream_t st) {
+  const RowArgs& r = p.r;
+  const dim3 grid(r.chunks * (FLAT ? 1 : r.a.B), r.colblocks);
+  k_norm_bsum<T, VB, ACT, FLAT><<<grid, kNT, row_smem<T, VB>(r), st>>>(r);
+  const int groups = FLAT ? 0 : r.a.B * r.a.G, chan = r.a.dgamma ? ceil_div(r.a.C, 32) : 0;
+  k_norm_bjoin<<<groups + chan, kNT, 0, st>>>(r, groups, (FLAT ? 1 : r.a.B) * r.chunks, r.a.ws + p.m12);
+}
+template <typename T, int VB, int ACT>
+void large_backward(const Plan& p, cudaStream_t st) {
+  channel_sums<T, VB, ACT, false>(p, st);
+  k_norm_dx<T, VB, ACT><<<dim3(p.r.chunks * p.r.a.B, p.r.colblocks), kNT, 0, st>>>(p.r, p.r.a.ws + p.m12);
+}
+
+// f.template operator()<T, VB, ACT>() for the vector's bytes and the activation
+template <typename T, typename F>
+void by_vec(int VB, int act, F f) {
+  auto go = [&](auto vb) {
+    constexpr int N = decltype(vb)::value;
+    if constexpr (N >= (int)sizeof(T)) {
+      if (act == LFA_ACT_SILU) f.template operator()<N, LFA_ACT_SILU>();
+      else if (act == LFA_ACT_GELU) f.template operator()<N, LFA_ACT_GELU>();
+      else f.template operator()<N, LFA_ACT_NONE>();
+    }
+  };
+  if (VB == 16) go(std::integral_constant<int, 16>{});
+  else if (VB == 8) go(std::integral_constant<int, 8>{});
+  else if (VB == 4) go(std::integral_constant<int, 4>{});
+  else go(std::integral_constant<int, 2>{});
+}
+
+template <typename T>
+struct Forward {
+  const Plan& p;
+  cudaStream_t st;
+  template <int VB, int ACT>
+  void operator()() const {
+    if (p.small) small_forward<T, VB, ACT>(p, st);
+    else large_forward<T, VB, ACT>(p, st);
+  }
+};
+template <typename T>
+struct SmallDx {
+  const Plan& p;
+  cudaStream_t st;
+  template <int VB, int ACT>
+  void operator()() const { small_backward<T, VB, ACT>(p, st); }
+};
+template <typename T>
+struct FlatSums {
+  const Plan& p;
+  cudaStream_t st;
+  template <int VB, int ACT>
+  void operator()() const { channel_sums<T, VB, ACT, true>(p, st); }
+};
+template <typename T>
+struct LargeBackward {
+  const Plan& p;
+  cudaStream_t st;
+  template <int VB, int ACT>
+  void operator()() const { large_backward<T, VB, ACT>(p, st); }
+};
+
 template <typename T>
 void run_norm(const NormArgs& a, cudaStream_t st) {
-  k_norm<T><<<a.B * a.G, kNT, 0, st>>>(a);
+  Plan p = plan_norm(a.B, a.N, a.C, a.G, sizeof(T), false);
+  p.s.a = p.r.a = a;
+  p.r.part = a.ws;
+  if (!p.small && !a.mean) {
+    p.r.a.mean = a.ws + p.stats;
+    p.r.a.rstd = p.r.a.mean + (size_t)a.B * a.G;
+  }
+  by_vec<T>(p.VB, a.act, Forward<T>{p, st});
 }
 template <typename T>
 void run_norm_backward(const NormArgs& a, cudaStream_t st) {
-  if (a.dgamma) k_norm_dparam<T><<<a.C, kNT, 0, st>>>(a);   // first: dx may overwrite dy
-  k_norm_dx<T><<<a.B * a.G, kNT, 0, st>>>(a);
+  Plan p = plan_norm(a.B, a.N, a.C, a.G, sizeof(T), true);
+  p.s.a = p.r.a = a;
+  p.r.part = a.ws;
+  if (!p.small) {
+    by_vec<T>(p.VB, a.act, LargeBackward<T>{p, st});
+    return;
+  }
+  if (a.dgamma) by_vec<T>(vec_bytes(a.C, sizeof(T)), a.act, FlatSums<T>{p, st});   // before dx, which may overwrite dy
+  by_vec<T>(p.VB, a.act, SmallDx<T>{p, st});
 }
 
 }  // namespace
@@ -239,7 +880,9 @@ cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-size_t norm_workspace_floats(int, int, int, int, int) { return 64; }
+size_t norm_workspace_floats(int B, int N, int C, int G, int dtype, int backward) {
+  return plan_norm(B, N, C, G, dtype == LFA_BF16 ? 2 : 4, backward != 0).floats;
+}
 
 cudaError_t launch_norm(const NormArgs& a, int dtype, cudaStream_t st) {
   if (dtype == LFA_BF16)

@@ -106,7 +106,7 @@ def _state(t: Optional[torch.Tensor], name: str, shape, device) -> None:
 
 
 @contextlib.contextmanager
-def _switched(device: torch.device, stream):
+def _switched(device: int, stream):
     with torch.cuda.device(device):
         if stream is None:
             yield
@@ -116,15 +116,46 @@ def _switched(device: torch.device, stream):
                 yield
 
 
-def _on(device: torch.device, stream):
-    """Context in which allocations and launches go to `stream` of `device`."""
-    if stream is None and device.index == torch.cuda.current_device():
+def _in(device: int, stream):
+    """Context in which a run of calls and allocations goes to `stream` of the device."""
+    if stream is None and device == torch.cuda.current_device():
         return contextlib.nullcontext()
     return _switched(device, stream)
 
 
-def _cur(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _elsewhere(t, stream) -> bool:
+    """Whether a call on tensor t has to leave the current device or stream (see _switched)."""
+    return (isinstance(t, torch.Tensor) and t.is_cuda
+            and (stream is not None or t.get_device() != torch.cuda.current_device()))
+
+
+def _cur(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+# Checked configurations by the shapes, strides, dtypes and devices of a call's arguments: a repeated shape is
+# checked once.
+_plans = {}
+
+
+def _sig(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _plan(kind, extra, tensors, check):
+    """check()'s answer for arguments of these shapes (errors are raised anew each time)."""
+    try:
+        key = (kind, extra, tuple([_sig(t) for t in tensors]))
+        plan = _plans.get(key)
+    except (AttributeError, TypeError, RuntimeError):
+        key = plan = None
+    if plan is None:
+        plan = check()
+        if key is not None:
+            if len(_plans) >= 4096:
+                _plans.clear()
+            _plans[key] = plan
+    return plan
 
 
 def _workspace(nbytes: int, device: torch.device, what: str) -> torch.Tensor:
@@ -155,6 +186,11 @@ def _new(like: torch.Tensor, lengths) -> torch.Tensor:
     return torch.empty_like(like) if lengths is None else torch.zeros_like(like)
 
 
+def _strided_like(like: torch.Tensor, lengths) -> torch.Tensor:
+    t = torch.empty_strided(like.shape, like.stride(), dtype=like.dtype, device=like.device)
+    return t if lengths is None else t.zero_()
+
+
 def decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *, scale=None,
                   S0: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
                   O: Optional[torch.Tensor] = None, S_out: Optional[torch.Tensor] = None,
@@ -166,21 +202,29 @@ def decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: 
     S0, S_out float32 [B, heads, dk, dv] (S_out may be S0; made if return_state, else None if not given);
     lengths int32 [B]: rows of O behind a sequence's end stay as they were (zeros in an O made here).
     """
-    cfg, device = _decay_config(q, k, v, log_decay, lengths, scale)
-    state = (cfg.B, cfg.heads, cfg.dk, cfg.dv)
-    _state(S0, "S0", state, device)
-    _state(S_out, "S_out", state, device)
+    if _elsewhere(q, stream):
+        with _switched(q.get_device(), stream):
+            return decay_forward(q, k, v, log_decay, scale=scale, S0=S0, lengths=lengths, O=O, S_out=S_out,
+                                 return_state=return_state)
     lib = load()
-    with _on(device, stream):
-        if O is None:
-            O = _new(v, lengths)
-        cfg.o_stride[:] = _tokens(O, "O", v.shape, q.dtype, device)[:3]
-        if S_out is None and return_state:
-            S_out = torch.empty(state, dtype=torch.float32, device=device)
-        ws = _workspace(lib.lfa_decay_workspace_size(cfg, 0), device, "lfa_decay_workspace_size")
-        _check(lib.lfa_decay_forward(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(S0),
-                                     _ptr(lengths), O.data_ptr(), _ptr(S_out), ws.data_ptr(), ws.numel(),
-                                     _cur(device)), "lfa_decay_forward")
+
+    def check():
+        cfg, device = _decay_config(q, k, v, log_decay, lengths, scale)
+        state = (cfg.B, cfg.heads, cfg.dk, cfg.dv)
+        _state(S0, "S0", state, device)
+        _state(S_out, "S_out", state, device)
+        cfg.o_stride[:] = _tokens(_new(v, lengths) if O is None else O, "O", v.shape, q.dtype, device)[:3]
+        return cfg, device, state, lib.lfa_decay_workspace_size(cfg, 0)
+
+    cfg, device, state, nbytes = _plan("forward", scale, (q, k, v, log_decay, S0, lengths, O, S_out), check)
+    if O is None:
+        O = _new(v, lengths)
+    if S_out is None and return_state:
+        S_out = torch.empty(state, dtype=torch.float32, device=device)
+    ws = _workspace(nbytes, device, "lfa_decay_workspace_size")
+    _check(lib.lfa_decay_forward(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(S0),
+                                 _ptr(lengths), O.data_ptr(), _ptr(S_out), ws.data_ptr(), nbytes,
+                                 _cur(device.index)), "lfa_decay_forward")
     return O, S_out
 
 
@@ -189,33 +233,38 @@ def decay_backward(q, k, v, log_decay, dO, *, scale=None, S0=None, lengths=None,
     """Gradients of <dO, O> + <dS_out, S_out> (lfa_decay_backward). Returns (dQ, dK, dV, dS0).
 
     dO [B, heads, N, dv]; dQ, dK, dV need the strides of q, k, v (made so if not given); dS0 is made if
-    return_state. Rows behind a sequence's end stay as they were. log_decay gets no gradient.
+    return_state. Rows behind a sequence's end stay as they were (zeros in tensors made here). log_decay gets no
+    gradient.
     """
-    cfg, device = _decay_config(q, k, v, log_decay, lengths, scale)
-    state = (cfg.B, cfg.heads, cfg.dk, cfg.dv)
-    for name, t in (("S0", S0), ("dS_out", dS_out), ("dS0", dS0)):
-        _state(t, name, state, device)
-    cfg.o_stride[:] = _tokens(dO, "dO", v.shape, q.dtype, device)[:3]
+    if _elsewhere(q, stream):
+        with _switched(q.get_device(), stream):
+            return decay_backward(q, k, v, log_decay, dO, scale=scale, S0=S0, lengths=lengths, dS_out=dS_out, dQ=dQ,
+                                  dK=dK, dV=dV, dS0=dS0, return_state=return_state)
     lib = load()
-    with _on(device, stream):
-        outs = []
+
+    def check():
+        cfg, device = _decay_config(q, k, v, log_decay, lengths, scale)
+        state = (cfg.B, cfg.heads, cfg.dk, cfg.dv)
+        for name, t in (("S0", S0), ("dS_out", dS_out), ("dS0", dS0)):
+            _state(t, name, state, device)
+        cfg.o_stride[:] = _tokens(dO, "dO", v.shape, q.dtype, device)[:3]
         for name, t, like in (("dQ", dQ, q), ("dK", dK, k), ("dV", dV, v)):
-            if t is None:
-                t = torch.empty_strided(like.shape, like.stride(), dtype=like.dtype, device=device)
-                if lengths is not None:
-                    t.zero_()
-            st = _tokens(t, name, like.shape, q.dtype, device)
-            if any(n > 1 and a != b for n, a, b in zip(like.shape, st, like.stride())):
-                raise ValueError(f"{name}: strides {st}, expected {like.stride()}")
-            outs.append(t)
-        dQ, dK, dV = outs
-        if dS0 is None and return_state:
-            dS0 = torch.empty(state, dtype=torch.float32, device=device)
-        ws = _workspace(lib.lfa_decay_workspace_size(cfg, 1), device, "lfa_decay_workspace_size")
-        _check(lib.lfa_decay_backward(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(S0),
-                                      _ptr(lengths), dO.data_ptr(), _ptr(dS_out), dQ.data_ptr(), dK.data_ptr(),
-                                      dV.data_ptr(), _ptr(dS0), ws.data_ptr(), ws.numel(), _cur(device)),
-               "lfa_decay_backward")
+            if t is not None:
+                st = _tokens(t, name, like.shape, q.dtype, device)
+                if any(n > 1 and a != b for n, a, b in zip(like.shape, st, like.stride())):
+                    raise ValueError(f"{name}: strides {st}, expected {like.stride()}")
+        return cfg, device, state, lib.lfa_decay_workspace_size(cfg, 1)
+
+    cfg, device, state, nbytes = _plan("backward", scale, (q, k, v, log_decay, dO, S0, lengths, dS_out, dQ, dK, dV, dS0),
+                                       check)
+    dQ, dK, dV = (_strided_like(like, lengths) if t is None else t for t, like in ((dQ, q), (dK, k), (dV, v)))
+    if dS0 is None and return_state:
+        dS0 = torch.empty(state, dtype=torch.float32, device=device)
+    ws = _workspace(nbytes, device, "lfa_decay_workspace_size")
+    _check(lib.lfa_decay_backward(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(S0),
+                                  _ptr(lengths), dO.data_ptr(), _ptr(dS_out), dQ.data_ptr(), dK.data_ptr(),
+                                  dV.data_ptr(), _ptr(dS0), ws.data_ptr(), nbytes, _cur(device.index)),
+           "lfa_decay_backward")
     return dQ, dK, dV, dS0
 
 
@@ -226,35 +275,42 @@ def decay_step(q, k, v, log_decay, S, *, scale=None, slots=None, O=None, stream=
     (slots int32 [B]), or S[b]. Rows with a slot outside the pool, or one that an earlier row has too, change
     nothing and get zeros.
     """
-    device = _first(q, "q", 3)
-    B, heads, dk = q.shape
-    if not isinstance(v, torch.Tensor) or v.dim() != 3:
-        raise ValueError("v: expected a 3-dimensional tensor")
-    dv = v.shape[2]
-    if not isinstance(S, torch.Tensor) or S.dim() != 4 or S.shape[0] < 1:
-        raise ValueError("S: expected a [n_slots, heads, dk, dv] tensor")
-    cfg = DecayConfig(B, heads, 1, dk, dv, _DTYPES[q.dtype], dk ** -0.5 if scale is None else float(scale))
-    cfg.q_stride[:2] = _tokens(q, "q", (B, heads, dk), q.dtype, device)[:2]
-    cfg.k_stride[:2] = _tokens(k, "k", (B, heads, dk), q.dtype, device)[:2]
-    cfg.v_stride[:2] = _tokens(v, "v", (B, heads, dv), q.dtype, device)[:2]
-    _require(log_decay, "log_decay", (heads,), torch.float32, device)
-    _require(S, "S", (S.shape[0], heads, dk, dv), torch.float32, device)
-    if slots is not None:
-        _require(slots, "slots", (B,), torch.int32, device)
-    with _on(device, stream):
-        if O is None:
-            O = torch.empty_like(v)
-        cfg.o_stride[:2] = _tokens(O, "O", v.shape, q.dtype, device)[:2]
-        _check(load().lfa_decay_step(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), S.data_ptr(),
-                                     _ptr(slots), S.shape[0], O.data_ptr(), _cur(device)), "lfa_decay_step")
+    if _elsewhere(q, stream):
+        with _switched(q.get_device(), stream):
+            return decay_step(q, k, v, log_decay, S, scale=scale, slots=slots, O=O)
+
+    def check():
+        device = _first(q, "q", 3)
+        B, heads, dk = q.shape
+        if not isinstance(v, torch.Tensor) or v.dim() != 3:
+            raise ValueError("v: expected a 3-dimensional tensor")
+        dv = v.shape[2]
+        if not isinstance(S, torch.Tensor) or S.dim() != 4 or S.shape[0] < 1:
+            raise ValueError("S: expected a [n_slots, heads, dk, dv] tensor")
+        cfg = DecayConfig(B, heads, 1, dk, dv, _DTYPES[q.dtype], dk ** -0.5 if scale is None else float(scale))
+        cfg.q_stride[:2] = _tokens(q, "q", (B, heads, dk), q.dtype, device)[:2]
+        cfg.k_stride[:2] = _tokens(k, "k", (B, heads, dk), q.dtype, device)[:2]
+        cfg.v_stride[:2] = _tokens(v, "v", (B, heads, dv), q.dtype, device)[:2]
+        cfg.o_stride[:2] = _tokens(torch.empty_like(v) if O is None else O, "O", v.shape, q.dtype, device)[:2]
+        _require(log_decay, "log_decay", (heads,), torch.float32, device)
+        _require(S, "S", (S.shape[0], heads, dk, dv), torch.float32, device)
+        if slots is not None:
+            _require(slots, "slots", (B,), torch.int32, device)
+        return cfg, device.index, S.shape[0]
+
+    cfg, device, n_slots = _plan("step", scale, (q, k, v, log_decay, S, slots, O), check)
+    if O is None:
+        O = torch.empty_like(v)
+    _check(load().lfa_decay_step(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), S.data_ptr(),
+                                 _ptr(slots), n_slots, O.data_ptr(), _cur(device)), "lfa_decay_step")
     return O
 
 
 def decay_status(stream=None, device=None) -> int:
     """LFA_OK, or LFA_ERR_TIMEOUT once after a decay call on the device gave up a wait (lfa_decay_status)."""
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with _on(device, stream):
-        return int(load().lfa_decay_status(_cur(device)))
+    device = torch.device("cuda" if device is None else device)
+    with _switched(torch.cuda.current_device() if device.index is None else device.index, stream):
+        return int(load().lfa_decay_status(_cur(torch.cuda.current_device())))
 
 
 # ---- rotary positions --------------------------------------------------------------------------------
@@ -305,34 +361,41 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, x2:
     layout "half" pairs channels (i, i + rot/2), "interleaved" (2i, 2i+1). inverse: the transpose, which
     takes gradients of the outputs to gradients of the inputs. out may be x (and out2 x2).
     """
-    device = _first(x, "x", 4)
-    B, heads, N, d = x.shape
-    if layout not in ("half", "interleaved"):
-        raise ValueError(f"layout: {layout!r}")
-    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
-        raise ValueError("freqs: expected a 1-dimensional tensor")
-    _require(positions, "positions", (B, N), torch.int32, device)
-    _require(freqs, "freqs", (freqs.shape[0],), torch.float64, device)
-    if x2 is not None and (not isinstance(x2, torch.Tensor) or x2.dim() != 4 or x2.shape[1] < 1):
-        raise ValueError("x2: expected a [B, heads2, N, d] tensor")
-    if x2 is None and out2 is not None:
-        raise ValueError("out2 without x2")
-    heads2 = 0 if x2 is None else x2.shape[1]
-    cfg = RotaryConfig(B, N, d, 2 * freqs.shape[0], heads, heads2, _DTYPES[x.dtype], layout == "interleaved", bool(inverse),
-                       float(mscale))
-    cfg.x_stride[:] = _tokens(x, "x", (B, heads, N, d), x.dtype, device)[:3]
-    if x2 is not None:
-        cfg.x2_stride[:] = _tokens(x2, "x2", (B, heads2, N, d), x.dtype, device)[:3]
-    with _on(device, stream):
-        if out is None:
-            out = torch.empty_like(x)
-        cfg.y_stride[:] = _tokens(out, "out", x.shape, x.dtype, device)[:3]
+    if _elsewhere(x, stream):
+        with _switched(x.get_device(), stream):
+            return rotary(x, positions, freqs, x2=x2, layout=layout, mscale=mscale, inverse=inverse, out=out, out2=out2)
+
+    def check():
+        device = _first(x, "x", 4)
+        B, heads, N, d = x.shape
+        if layout not in ("half", "interleaved"):
+            raise ValueError(f"layout: {layout!r}")
+        if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+            raise ValueError("freqs: expected a 1-dimensional tensor")
+        _require(positions, "positions", (B, N), torch.int32, device)
+        _require(freqs, "freqs", (freqs.shape[0],), torch.float64, device)
+        if x2 is not None and (not isinstance(x2, torch.Tensor) or x2.dim() != 4 or x2.shape[1] < 1):
+            raise ValueError("x2: expected a [B, heads2, N, d] tensor")
+        if x2 is None and out2 is not None:
+            raise ValueError("out2 without x2")
+        heads2 = 0 if x2 is None else x2.shape[1]
+        cfg = RotaryConfig(B, N, d, 2 * freqs.shape[0], heads, heads2, _DTYPES[x.dtype], layout == "interleaved",
+                           bool(inverse), float(mscale))
+        cfg.x_stride[:] = _tokens(x, "x", (B, heads, N, d), x.dtype, device)[:3]
+        cfg.y_stride[:] = _tokens(torch.empty_like(x) if out is None else out, "out", x.shape, x.dtype, device)[:3]
         if x2 is not None:
-            if out2 is None:
-                out2 = torch.empty_like(x2)
-            cfg.y2_stride[:] = _tokens(out2, "out2", x2.shape, x.dtype, device)[:3]
-        _check(load().lfa_rotary(cfg, x.data_ptr(), _ptr(x2), positions.data_ptr(), freqs.data_ptr(), out.data_ptr(),
-                                 _ptr(out2), _cur(device)), "lfa_rotary")
+            cfg.x2_stride[:] = _tokens(x2, "x2", (B, heads2, N, d), x.dtype, device)[:3]
+            y2 = torch.empty_like(x2) if out2 is None else out2
+            cfg.y2_stride[:] = _tokens(y2, "out2", x2.shape, x.dtype, device)[:3]
+        return cfg, device.index
+
+    cfg, device = _plan("rotary", (layout, mscale, inverse), (x, positions, freqs, x2, out, out2), check)
+    if out is None:
+        out = torch.empty_like(x)
+    if out2 is None and x2 is not None:
+        out2 = torch.empty_like(x2)
+    _check(load().lfa_rotary(cfg, x.data_ptr(), _ptr(x2), positions.data_ptr(), freqs.data_ptr(), out.data_ptr(),
+                             _ptr(out2), _cur(device)), "lfa_rotary")
     return out, out2
 
 
@@ -359,16 +422,25 @@ def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = Non
 
     gamma, beta float32 [C] or None; act "none", "silu" or "gelu" (exact); out may be x.
     """
-    cfg, device = _norm_config(x, groups, gamma, beta, eps, act)
+    if _elsewhere(x, stream):
+        with _switched(x.get_device(), stream):
+            return group_norm(x, groups, gamma, beta, eps=eps, act=act, out=out)
     lib = load()
-    with _on(device, stream):
-        if out is None:
-            out = torch.empty_like(x)
-        _require(out, "out", x.shape, x.dtype, device)
-        ws = _workspace(lib.lfa_group_norm_workspace_size(cfg, 0), device, "lfa_group_norm_workspace_size")
-        mean, rstd = torch.empty((2, cfg.B, cfg.groups), dtype=torch.float32, device=device)
-        _check(lib.lfa_group_norm(cfg, x.data_ptr(), _ptr(gamma), _ptr(beta), out.data_ptr(), mean.data_ptr(),
-                                  rstd.data_ptr(), ws.data_ptr(), ws.numel(), _cur(device)), "lfa_group_norm")
+
+    def check():
+        cfg, device = _norm_config(x, groups, gamma, beta, eps, act)
+        if out is not None:
+            _require(out, "out", x.shape, x.dtype, device)
+        return cfg, device, lib.lfa_group_norm_workspace_size(cfg, 0)
+
+    cfg, device, nbytes = _plan("norm", (groups, eps, act), (x, gamma, beta, out), check)
+    if out is None:
+        out = torch.empty_like(x)
+    ws = _workspace(nbytes, device, "lfa_group_norm_workspace_size")
+    mean = torch.empty((cfg.B, cfg.groups), dtype=torch.float32, device=device)
+    rstd = torch.empty((cfg.B, cfg.groups), dtype=torch.float32, device=device)
+    _check(lib.lfa_group_norm(cfg, x.data_ptr(), _ptr(gamma), _ptr(beta), out.data_ptr(), mean.data_ptr(),
+                              rstd.data_ptr(), ws.data_ptr(), nbytes, _cur(device.index)), "lfa_group_norm")
     return out, mean, rstd
 
 
@@ -376,22 +448,31 @@ def group_norm_backward(x, dy, mean, rstd, groups: int, gamma=None, beta=None, *
                         dx=None, stream=None):
     """Gradients of group_norm from its inputs and saved statistics (lfa_group_norm_backward). Returns
     (dx, dgamma, dbeta), the last two float32 [C], or None without gamma. dx may be dy."""
-    cfg, device = _norm_config(x, groups, gamma, beta, eps, act)
-    _require(dy, "dy", x.shape, x.dtype, device)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _require(t, name, (cfg.B, cfg.groups), torch.float32, device)
+    if _elsewhere(x, stream):
+        with _switched(x.get_device(), stream):
+            return group_norm_backward(x, dy, mean, rstd, groups, gamma, beta, eps=eps, act=act, dx=dx)
     lib = load()
-    with _on(device, stream):
-        if dx is None:
-            dx = torch.empty_like(x)
-        _require(dx, "dx", x.shape, x.dtype, device)
-        ws = _workspace(lib.lfa_group_norm_workspace_size(cfg, 1), device, "lfa_group_norm_workspace_size")
-        dgamma = dbeta = None
-        if gamma is not None:
-            dgamma, dbeta = torch.empty((2, cfg.C), dtype=torch.float32, device=device)
-        _check(lib.lfa_group_norm_backward(cfg, x.data_ptr(), dy.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                                           _ptr(gamma), _ptr(beta), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta),
-                                           ws.data_ptr(), ws.numel(), _cur(device)), "lfa_group_norm_backward")
+
+    def check():
+        cfg, device = _norm_config(x, groups, gamma, beta, eps, act)
+        _require(dy, "dy", x.shape, x.dtype, device)
+        for name, t in (("mean", mean), ("rstd", rstd)):
+            _require(t, name, (cfg.B, cfg.groups), torch.float32, device)
+        if dx is not None:
+            _require(dx, "dx", x.shape, x.dtype, device)
+        return cfg, device, lib.lfa_group_norm_workspace_size(cfg, 1)
+
+    cfg, device, nbytes = _plan("norm_backward", (groups, eps, act), (x, dy, mean, rstd, gamma, beta, dx), check)
+    if dx is None:
+        dx = torch.empty_like(x)
+    ws = _workspace(nbytes, device, "lfa_group_norm_workspace_size")
+    dgamma = dbeta = None
+    if gamma is not None:
+        dgamma = torch.empty(cfg.C, dtype=torch.float32, device=device)
+        dbeta = torch.empty(cfg.C, dtype=torch.float32, device=device)
+    _check(lib.lfa_group_norm_backward(cfg, x.data_ptr(), dy.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                       _ptr(gamma), _ptr(beta), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta),
+                                       ws.data_ptr(), nbytes, _cur(device.index)), "lfa_group_norm_backward")
     return dx, dgamma, dbeta
 
 
@@ -421,7 +502,7 @@ class DecayAttention:
     def forward(self, q, k, v, positions=None, *, S0=None, lengths=None, stream=None):
         """Returns (y, S_out, saved): saved is what backward needs. With lengths, rows of y behind a
         sequence's end are the norm of zeros."""
-        with _on(_first(v, "v", 4), stream):
+        with _in(_first(v, "v", 4).index, stream):
             qr, kr = self._rotate(q.transpose(1, 2), k.transpose(1, 2), positions, False)
             o = (torch.empty if lengths is None else torch.zeros)(v.shape, dtype=v.dtype, device=v.device)
             _, S = decay_forward(qr, kr, v.transpose(1, 2), self.log_decay, scale=self.scale, S0=S0, lengths=lengths,
@@ -437,7 +518,7 @@ class DecayAttention:
         qr, kr, v, o, mean, rstd, positions, S0, lengths = saved
         B, N, heads, dv = v.shape
         flat = (B * N, 1, heads * dv)
-        with _on(v.device, stream):
+        with _in(v.get_device(), stream):
             do, dgamma, dbeta = group_norm_backward(o.view(flat), dy.reshape(flat), mean, rstd, heads, self.gamma,
                                                     self.beta, eps=self.eps, act=self.act)
             dq, dk, dvt, dS0 = decay_backward(qr, kr, v.transpose(1, 2), self.log_decay,
@@ -450,7 +531,7 @@ class DecayAttention:
         """One token of every row: q, k [B, heads, dk], v [B, heads, dv], positions [B]; S is updated in place.
         Returns y [B, heads * dv]."""
         B, heads, dv = v.shape
-        with _on(_first(v, "v", 3), stream):
+        with _in(_first(v, "v", 3).index, stream):
             if self.freqs is not None:
                 qr, kr = self._rotate(q.unsqueeze(2), k.unsqueeze(2), positions.view(-1, 1), False)
                 q, k = qr.squeeze(2), kr.squeeze(2)
