@@ -226,17 +226,27 @@ __global__ void __launch_bounds__(kStepT) k_decay_step(const __grid_constant__ D
     const float l = expf(decay_log(a.log_decay[h]));
     const float4 v = load4(vp + c);
     float* S = a.S + ((size_t)slot * a.heads + h) * a.dk * a.dv + c;
-    for (int r = w; r < a.dk; r += kStepT / 32) {
-      float4 s = *reinterpret_cast<float4*>(S + (size_t)r * a.dv);
-      s.x = fmaf(l, s.x, k[r] * v.x);
-      s.y = fmaf(l, s.y, k[r] * v.y);
-      s.z = fmaf(l, s.z, k[r] * v.z);
-      s.w = fmaf(l, s.w, k[r] * v.w);
-      *reinterpret_cast<float4*>(S + (size_t)r * a.dv) = s;
-      o.x = fmaf(q[r], s.x, o.x);
-      o.y = fmaf(q[r], s.y, o.y);
-      o.z = fmaf(q[r], s.z, o.z);
-      o.w = fmaf(q[r], s.w, o.w);
+    constexpr int W = kStepT / 32, U = 8;   // warps; rows a thread has in flight
+    for (int r0 = w; r0 < a.dk; r0 += W * U) {
+      float4 s[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (r0 + i * W < a.dk) s[i] = *reinterpret_cast<const float4*>(S + (size_t)(r0 + i * W) * a.dv);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int r = r0 + i * W;
+        if (r < a.dk) {
+          s[i].x = fmaf(l, s[i].x, k[r] * v.x);
+          s[i].y = fmaf(l, s[i].y, k[r] * v.y);
+          s[i].z = fmaf(l, s[i].z, k[r] * v.z);
+          s[i].w = fmaf(l, s[i].w, k[r] * v.w);
+          *reinterpret_cast<float4*>(S + (size_t)r * a.dv) = s[i];
+          o.x = fmaf(q[r], s[i].x, o.x);
+          o.y = fmaf(q[r], s[i].y, o.y);
+          o.z = fmaf(q[r], s[i].z, o.z);
+          o.w = fmaf(q[r], s[i].w, o.w);
+        }
+      }
     }
   }
   part[w][lane] = o;

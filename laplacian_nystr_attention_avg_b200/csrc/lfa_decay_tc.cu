@@ -632,8 +632,8 @@ struct PrefixArgs {
   const int* lengths;
   int heads, N, segs, seg_chunks, dd;
 };
-__global__ void __launch_bounds__(256) k_decay_prefix(const __grid_constant__ PrefixArgs a) {
-  const int u = blockIdx.x, j = blockIdx.z, e = (blockIdx.y * 256 + threadIdx.x) * 4;
+__global__ void __launch_bounds__(64) k_decay_prefix(const __grid_constant__ PrefixArgs a) {
+  const int u = blockIdx.x, j = blockIdx.z, e = (blockIdx.y * 64 + threadIdx.x) * 4;
   if (e >= a.dd) return;
   const int L = unit_length(a.lengths, u / a.heads, a.N), nch = (L + kC - 1) / kC;
   const int segs = (nch + a.seg_chunks - 1) / a.seg_chunks, span = a.seg_chunks * kC;
@@ -646,19 +646,26 @@ __global__ void __launch_bounds__(256) k_decay_prefix(const __grid_constant__ Pr
     r = *reinterpret_cast<const float4*>(a.init[j] + (size_t)u * a.dd + e);
     r.x *= f; r.y *= f; r.z *= f; r.w *= f;
   }
-  for (int i = 0; i < segs; ++i) {
-    const int p = a.rev[j] ? segs - 1 - i : i;
-    float4* at = reinterpret_cast<float4*>(st + (size_t)p * a.dd);
-    const bool more = i + 1 < segs;
-    const float4 own = more ? *at : r;
-    *at = r;
-    if (more) {
-      const Decay dec(ld * min(span, L - p * span));
-      r.x = dec(r.x) + own.x;
-      r.y = dec(r.y) + own.y;
-      r.z = dec(r.z) + own.z;
-      r.w = dec(r.w) + own.w;
-    }
+  constexpr int kAhead = 8;   // segments read at once: the chain over them is arithmetic only
+  for (int i0 = 0; i0 < segs; i0 += kAhead) {
+    float4 own[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i0 + i + 1 < segs)   // the run's last segment has no sum: nothing follows it
+        own[i] = *reinterpret_cast<const float4*>(st + (size_t)(a.rev[j] ? segs - 1 - i0 - i : i0 + i) * a.dd);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i0 + i < segs) {
+        const int p = a.rev[j] ? segs - 1 - i0 - i : i0 + i;
+        *reinterpret_cast<float4*>(st + (size_t)p * a.dd) = r;
+        if (i0 + i + 1 < segs) {
+          const Decay dec(ld * min(span, L - p * span));
+          r.x = dec(r.x) + own[i].x;
+          r.y = dec(r.y) + own[i].y;
+          r.z = dec(r.z) + own[i].z;
+          r.w = dec(r.w) + own[i].w;
+        }
+      }
   }
 }
 
@@ -772,7 +779,7 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
     p.segs = sp.segs;
     p.seg_chunks = sp.seg_chunks;
     p.dd = dd;
-    k_decay_prefix<<<dim3(units, ceil_div(dd, 1024), ns), 256, 0, st>>>(p);
+    k_decay_prefix<<<dim3(units, ceil_div(dd, 256), ns), 64, 0, st>>>(p);
     const cudaError_t e2 = cudaGetLastError();
     if (e2 != cudaSuccess) return e2;
   }

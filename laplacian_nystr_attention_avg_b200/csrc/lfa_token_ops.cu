@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "lfa_internal.h"
+#include "lfa_sm100.cuh"
 #include "lfa_token.h"
 
 namespace lfa {
@@ -11,12 +12,11 @@ namespace {
 
 // ---- rotary positions -------------------------------------------------------------------------------
 // Pair i of a token at position p turns by th = p f_i: (a, b) -> mscale (a cos th - b sin th, a sin th + b cos th).
-// th is reduced in turns in 64 bits (p f / 2 pi minus its nearest whole number), so that far positions keep
-// their angle; the rest is fp32. A CTA takes kRT tokens: their cosines and sines are formed once in shared
-// memory and serve every head.
-constexpr int kRT = 16;        // tokens per CTA
+// th is reduced in turns in 64 bits (p f / 2 pi minus its nearest whole number), so that far positions keep their
+// angle; the rest is fp32. A thread has one token and one unit of a head's channels (V pairs in two 16-byte
+// vectors, V / 2 pairs in one, or a single pair), forms their cosines and sines once, and goes over the heads.
 constexpr int kRThreads = 256;
-constexpr int kRMaxPairs = 64;
+constexpr int kRHeads = 4;   // heads in flight
 
 template <typename T>
 struct Vec {
@@ -33,86 +33,118 @@ template <typename T>
 __device__ __forceinline__ void vstore(T* p, const Vec<T>& r) {
   *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.v);
 }
+__device__ __forceinline__ float2 turn(const RotaryArgs& a, double pos, int i) {
+  const double turns = pos * (a.freqs[i] * 0.15915494309189533577);
+  float sn, c;
+  sincospif(2.f * (float)(turns - rint(turns)), &sn, &c);
+  return make_float2(a.mscale * c, a.inverse ? -a.mscale * sn : a.mscale * sn);
+}
 
-// MODE 0: half layout, rot / 2 a whole number of 16-byte vectors; 1: interleaved; 2: half layout, any even rot
+// units of a head's row: MODE 0: half layout, rot / 2 a whole number of vectors; 1: interleaved; 2: half layout,
+// any even rot
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kRThreads) k_rotary(const __grid_constant__ RotaryArgs a) {
-  __shared__ float2 cs[kRT][kRMaxPairs];
-  constexpr int V = Vec<T>::n;
-  const int tiles = (a.N + kRT - 1) / kRT;
-  const int b = blockIdx.x / tiles, n0 = (blockIdx.x % tiles) * kRT, nt = min(kRT, a.N - n0);
+__host__ __device__ __forceinline__ int rotary_units(int d, int rot) {
+  constexpr int V = 16 / sizeof(T);
+  return MODE == 0 ? rot / 2 / V + (d - rot) / V : MODE == 1 ? d / V : rot / 2 + d - rot;
+}
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kRThreads) k_rotary(const __grid_constant__ RotaryArgs a, int units, int tokens,
+                                                      int heads_each) {
+  constexpr int V = Vec<T>::n, NP = MODE == 0 ? V : MODE == 1 ? V / 2 : 1;   // pairs of a unit
+  const int tl = threadIdx.x / units, unit = threadIdx.x - tl * units, tok = blockIdx.x * tokens + tl;
+  if (tl >= tokens || tok >= a.B * a.N) return;
   const int half = a.rot >> 1;
-  for (int e = threadIdx.x; e < nt * half; e += kRThreads) {
-    const int n = e / half, i = e % half;
-    const double turns = (double)a.positions[(size_t)b * a.N + n0 + n] * (a.freqs[i] * 0.15915494309189533577);
-    float sn, c;
-    sincospif(2.f * (float)(turns - rint(turns)), &sn, &c);
-    cs[n][i] = make_float2(a.mscale * c, a.inverse ? -a.mscale * sn : a.mscale * sn);
+  const int b = tok / a.N, n = tok - b * a.N;
+  // first pair of the unit, and its channels
+  const int pair = unit * NP, c0 = MODE == 2 ? unit : unit * V;
+  const bool turns = MODE == 1 ? c0 < a.rot : pair < half;
+  const int copy = MODE == 0 ? a.rot + (unit - half / V) * V : MODE == 1 ? c0 : half + unit;
+  float2 w[NP];
+  if (turns) {
+    const double pos = (double)a.positions[tok];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) w[i] = pair + i < half ? turn(a, pos, pair + i) : make_float2(1.f, 0.f);
   }
-  __syncthreads();
-  const int rest = a.d - a.rot;
-  const int units = MODE == 0 ? half / V + rest / V : (MODE == 1 ? a.d / V : half + rest);
   const int all = a.heads + a.heads2;
-  for (int e = threadIdx.x; e < units * nt * all; e += kRThreads) {
-    const int unit = e % units, n = (e / units) % nt, h = e / (units * nt);
-    const bool second = h >= a.heads;
-    const long long* si = second ? a.x2s : a.xs;
-    const long long* so = second ? a.y2s : a.ys;
-    const int hh = second ? h - a.heads : h;
-    const T* x = static_cast<const T*>(second ? a.x2 : a.x) + b * si[0] + hh * si[1] + (n0 + n) * si[2];
-    T* y = static_cast<T*>(second ? a.y2 : a.y) + b * so[0] + hh * so[1] + (n0 + n) * so[2];
-    if (MODE == 0) {
-      if (unit < half / V) {
-        const Vec<T> p = vload(x + unit * V), q = vload(x + half + unit * V);
-        Vec<T> po, qo;
+  const int h0 = blockIdx.y * heads_each, h1 = min(h0 + heads_each, all);
+  for (int h = h0; h < h1; h += kRHeads) {
+    const T* x[kRHeads];
+    T* y[kRHeads];
+    Vec<T> p[kRHeads], q[kRHeads];
+    T sp[kRHeads], sq[kRHeads];
+#pragma unroll
+    for (int e = 0; e < kRHeads; ++e) {
+      if (h + e >= h1) break;
+      const bool second = h + e >= a.heads;
+      const int hh = second ? h + e - a.heads : h + e;
+      const long long* si = second ? a.x2s : a.xs;
+      const long long* so = second ? a.y2s : a.ys;
+      x[e] = static_cast<const T*>(second ? a.x2 : a.x) + b * si[0] + hh * si[1] + n * si[2];
+      y[e] = static_cast<T*>(second ? a.y2 : a.y) + b * so[0] + hh * so[1] + n * so[2];
+      if constexpr (MODE == 2) {
+        sp[e] = x[e][turns ? c0 : copy];
+        if (turns) sq[e] = x[e][c0 + half];
+      } else {
+        p[e] = vload(x[e] + (turns ? c0 : copy));
+        if (MODE == 0 && turns) q[e] = vload(x[e] + c0 + half);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kRHeads; ++e) {
+      if (h + e >= h1) break;
+      if (!turns) {
+        if constexpr (MODE == 2)
+          y[e][copy] = sp[e];
+        else
+          vstore(y[e] + copy, p[e]);
+      } else if constexpr (MODE == 0) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float2 w = cs[n][unit * V + i];
-          const float u = to_f<T>(p.v[i]), v = to_f<T>(q.v[i]);
-          po.v[i] = from_f<T>(u * w.x - v * w.y);
-          qo.v[i] = from_f<T>(u * w.y + v * w.x);
+          const float u = to_f<T>(p[e].v[i]), v = to_f<T>(q[e].v[i]);
+          p[e].v[i] = from_f<T>(u * w[i].x - v * w[i].y);
+          q[e].v[i] = from_f<T>(u * w[i].y + v * w[i].x);
         }
-        vstore(y + unit * V, po);
-        vstore(y + half + unit * V, qo);
-      } else {
-        const int c = a.rot + (unit - half / V) * V;
-        vstore(y + c, vload(x + c));
-      }
-    } else if (MODE == 1) {
-      Vec<T> p = vload(x + unit * V);
+        vstore(y[e] + c0, p[e]);
+        vstore(y[e] + c0 + half, q[e]);
+      } else if constexpr (MODE == 1) {
 #pragma unroll
-      for (int i = 0; i < V; i += 2) {
-        const int c = unit * V + i;
-        if (c < a.rot) {
-          const float2 w = cs[n][c >> 1];
-          const float u = to_f<T>(p.v[i]), v = to_f<T>(p.v[i + 1]);
-          p.v[i] = from_f<T>(u * w.x - v * w.y);
-          p.v[i + 1] = from_f<T>(u * w.y + v * w.x);
+        for (int i = 0; i < V; i += 2) {
+          if (c0 + i < a.rot) {   // channels behind rot stay as they are, bit by bit
+            const float u = to_f<T>(p[e].v[i]), v = to_f<T>(p[e].v[i + 1]);
+            const float2 z = w[i / 2];
+            p[e].v[i] = from_f<T>(u * z.x - v * z.y);
+            p[e].v[i + 1] = from_f<T>(u * z.y + v * z.x);
+          }
         }
-      }
-      vstore(y + unit * V, p);
-    } else {
-      if (unit < half) {
-        const float2 w = cs[n][unit];
-        const float u = to_f<T>(x[unit]), v = to_f<T>(x[unit + half]);
-        y[unit] = from_f<T>(u * w.x - v * w.y);
-        y[unit + half] = from_f<T>(u * w.y + v * w.x);
+        vstore(y[e] + c0, p[e]);
       } else {
-        y[half + unit] = x[half + unit];
+        const float u = to_f<T>(sp[e]), v = to_f<T>(sq[e]);
+        y[e][c0] = from_f<T>(u * w[0].x - v * w[0].y);
+        y[e][c0 + half] = from_f<T>(u * w[0].y + v * w[0].x);
       }
     }
   }
 }
 
+template <typename T, int MODE>
+void rotary_launch(const RotaryArgs& a, cudaStream_t st) {
+  const int units = rotary_units<T, MODE>(a.d, a.rot), tokens = kRThreads / units;   // units <= 256
+  const int tiles = ceil_div(a.B * a.N, tokens), all = a.heads + a.heads2;
+  // heads are split over blocks until about four blocks an SM run; the angles are then formed once more each
+  int parts = tiles < 592 ? ceil_div(592, tiles) : 1;
+  if (parts > all) parts = all;
+  const int each = ceil_div(all, parts);
+  k_rotary<T, MODE><<<dim3(tiles, ceil_div(all, each)), kRThreads, 0, st>>>(a, units, tokens, each);
+}
 template <typename T>
 void run_rotary(const RotaryArgs& a, cudaStream_t st) {
-  const int grid = a.B * ceil_div(a.N, kRT);
   if (a.interleaved)
-    k_rotary<T, 1><<<grid, kRThreads, 0, st>>>(a);
+    rotary_launch<T, 1>(a, st);
   else if ((a.rot / 2) % Vec<T>::n == 0)
-    k_rotary<T, 0><<<grid, kRThreads, 0, st>>>(a);
+    rotary_launch<T, 0>(a, st);
   else
-    k_rotary<T, 2><<<grid, kRThreads, 0, st>>>(a);
+    rotary_launch<T, 2>(a, st);
 }
 
 // ---- group norm ---------------------------------------------------------------------------------------
@@ -124,7 +156,12 @@ constexpr int kNT = 256;         // threads per block
 constexpr int kNRows = 8;        // rows a thread has in flight
 constexpr int kMaxChunks = 64;   // row chunks per sample (large groups)
 
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 1 / (1 + exp(-z)): exponent and reciprocal within 2 units each (2^-22 relative)
+__device__ __forceinline__ float sigmoid_f(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + sm100::ex2_approx(z * -1.4426950408889634f)));
+  return r;
+}
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
   if (ACT == LFA_ACT_SILU) return z * sigmoid_f(z);
@@ -138,7 +175,7 @@ __device__ __forceinline__ float act_slope(float z) {
     return p * fmaf(z, 1.f - p, 1.f);
   }
   if (ACT == LFA_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * sm100::ex2_approx(z * z * -0.72134752044448170f);
   return 1.f;
 }
 
@@ -281,6 +318,127 @@ __global__ void __launch_bounds__(kNT) k_norm_small(const __grid_constant__ Smal
       o[i] = act_f<ACT>(z);
     }
     raw_store<VB>(y + off, raw_make<T, VB>(o));
+  }
+}
+
+// The same for groups of one vector per thread (T a power of two): a thread keeps its channels over all the samples it
+// takes (every teams-th (sample, group); teams is a multiple of G), U of them in flight.
+template <typename T, int VB, int ACT, bool BACKWARD>
+__global__ void __launch_bounds__(kNT) k_norm_rows(const __grid_constant__ SmallArgs s, int teams) {
+  constexpr int V = VB / sizeof(T), U = 4;
+  const NormArgs& a = s.a;
+  const int tl = threadIdx.x & (s.T - 1), team = blockIdx.x * (kNT / s.T) + threadIdx.x / s.T;
+  const long long total = (long long)a.B * a.G;
+  const int g = team % a.G, dg = a.C / a.G;
+  const bool has = tl < s.nvec;
+  long long off;
+  int c;
+  place<T, VB>(s, has ? tl : 0, off, c);
+  float ga[V], be[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    ga[i] = a.gamma ? a.gamma[g * dg + c + i] : 1.f;
+    be[i] = a.beta ? a.beta[g * dg + c + i] : 0.f;
+  }
+  const float n = (float)(s.nvec * V), inv = 1.f / n;
+  const long long step = (long long)(teams / a.G) * a.N * a.C;   // elements from one sample of this thread to its next
+  long long at = (long long)(team / a.G) * a.N * a.C + g * dg + off;
+  const T* x = static_cast<const T*>(a.x);
+  const T* dy = static_cast<const T*>(a.dy);
+  T* y = static_cast<T*>(a.y);
+  // the block's threads stay together (they shuffle), whatever teams still have a sample
+  for (long long id0 = (long long)blockIdx.x * (kNT / s.T); id0 < total; id0 += (long long)U * teams, at += U * step) {
+    const long long id = id0 + threadIdx.x / s.T;
+    Raw<VB> v[U], w[U];
+    float m[U], rs[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long iu = id + (long long)u * teams;
+      const bool on = iu < total;
+#pragma unroll
+      for (int i = 0; i < (VB + 3) / 4; ++i) v[u].w[i] = w[u].w[i] = 0u;
+      if (on && has) {
+        v[u] = raw_load<VB>(x + at + u * step);
+        if (BACKWARD) w[u] = raw_load<VB>(dy + at + u * step);
+      }
+      if (BACKWARD) {
+        m[u] = on ? a.mean[iu] : 0.f;
+        rs[u] = on ? a.rstd[iu] : 0.f;
+      }
+    }
+    if constexpr (!BACKWARD) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) t += raw_get<T>(v[u], i);
+        m[u] = t;   // threads without a vector hold zeros
+      }
+      for (int o = s.T >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) m[u] += __shfl_xor_sync(0xffffffffu, m[u], o);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        m[u] = __fdiv_rn(m[u], n);   // exact for constant groups
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float d = raw_get<T>(v[u], i) - m[u];
+          t = fmaf(d, d, t);
+        }
+        rs[u] = has ? t : 0.f;
+      }
+      for (int o = s.T >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) rs[u] += __shfl_xor_sync(0xffffffffu, rs[u], o);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        rs[u] = rsqrtf(fmaf(rs[u], inv, a.eps));
+        const long long iu = id + (long long)u * teams;
+        if (iu < total) {
+          if (tl == 0 && a.mean) {
+            a.mean[iu] = m[u];
+            a.rstd[iu] = rs[u];
+          }
+          if (has) {
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = act_f<ACT>(fmaf((raw_get<T>(v[u], i) - m[u]) * rs[u], ga[i], be[i]));
+            raw_store<VB>(y + at + u * step, raw_make<T, VB>(o));
+          }
+        }
+      }
+    } else {
+      float d[U][V], s1[U], s2[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        s1[u] = s2[u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float xh = (raw_get<T>(v[u], i) - m[u]) * rs[u];
+          d[u][i] = ga[i] * raw_get<T>(w[u], i) * act_slope<ACT>(fmaf(xh, ga[i], be[i]));
+          s1[u] += d[u][i];   // dy is zero in threads without a vector
+          s2[u] = fmaf(d[u][i], xh, s2[u]);
+        }
+      }
+      for (int o = s.T >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          s1[u] += __shfl_xor_sync(0xffffffffu, s1[u], o);
+          s2[u] += __shfl_xor_sync(0xffffffffu, s2[u], o);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (has && id + (long long)u * teams < total) {
+          float o[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float xh = (raw_get<T>(v[u], i) - m[u]) * rs[u];
+            o[i] = rs[u] * (d[u][i] - s1[u] * inv - xh * (s2[u] * inv));
+          }
+          raw_store<VB>(y + at + u * step, raw_make<T, VB>(o));
+        }
+    }
   }
 }
 
@@ -494,6 +652,16 @@ __device__ __forceinline__ void chan_affine(const NormArgs& a, int c, Chan<V>& k
 }
 template <int V>
 __device__ __forceinline__ void chan_stats(const NormArgs& a, int b, int c, int dg, Chan<V>& k) {
+  if (dg % V == 0) {   // one group
+    const size_t at = (size_t)b * a.G + c / dg;
+    const float m = a.mean[at], r = a.rstd[at];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      k.mean[i] = m;
+      k.rstd[i] = r;
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const size_t at = (size_t)b * a.G + (c + i) / dg;
@@ -594,8 +762,8 @@ __global__ void __launch_bounds__(kNT) k_norm_bsum(const __grid_constant__ RowAr
   }
 }
 
-// Blocks below groups: m1, m2 of one (sample, group) from its channels' sums. The rest: dbeta, dgamma of 32
-// channels, 8 lanes over the records.
+// Blocks below groups: m1, m2 of one (sample, group) from its channels' sums. The rest: dbeta, dgamma of 8
+// channels, 32 lanes over the records.
 __global__ void __launch_bounds__(kNT) k_norm_bjoin(const __grid_constant__ RowArgs p, int groups, int records,
                                                      float* m12) {
   __shared__ float red[2][kNT];
@@ -618,20 +786,22 @@ __global__ void __launch_bounds__(kNT) k_norm_bjoin(const __grid_constant__ RowA
       m12[2 * blockIdx.x + 1] = s2 / n;
     }
   } else {
-    const int c = ((int)blockIdx.x - groups) * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+    const int cl = threadIdx.x & 7, c = ((int)blockIdx.x - groups) * 8 + cl, y = threadIdx.x >> 3;
     float s1 = 0.f, s2 = 0.f;
-    if (c < a.C)
-      for (int r = y; r < records; r += kNT / 32) {
+    if (c < a.C) {
+#pragma unroll 8
+      for (int r = y; r < records; r += kNT / 8) {
         s1 += p.part[(size_t)r * 2 * a.C + c];
         s2 += p.part[(size_t)r * 2 * a.C + a.C + c];
       }
+    }
     red[0][threadIdx.x] = s1;
     red[1][threadIdx.x] = s2;
     __syncthreads();
     if (y == 0 && c < a.C) {
-      for (int i = 1; i < kNT / 32; ++i) {
-        s1 += red[0][32 * i + threadIdx.x];
-        s2 += red[1][32 * i + threadIdx.x];
+      for (int i = 1; i < kNT / 8; ++i) {
+        s1 += red[0][8 * i + cl];
+        s2 += red[1][8 * i + cl];
       }
       a.dbeta[c] = s1;
       a.dgamma[c] = s2;
@@ -746,6 +916,18 @@ Plan plan_norm(int B, int N, int C, int G, int es, bool backward) {
   return p;
 }
 
+// blocks of k_norm_rows: at most about eight an SM, with a number of teams that G divides
+template <typename T, int VB, int ACT, bool BACKWARD>
+void rows_launch(const Plan& p, cudaStream_t st) {
+  const int per = kNT / p.s.T, G = p.s.a.G;
+  int unit = G;   // blocks whose teams are a multiple of G: G / gcd(G, per)
+  for (int d = per; d > 1; d /= 2)
+    if (unit % 2 == 0) unit /= 2;
+  const long long teams = (long long)p.s.a.B * G, need = (teams + per - 1) / per;
+  long long blocks = need < 8 * 148 ? need : 8 * 148;
+  blocks = (blocks + unit - 1) / unit * unit;
+  k_norm_rows<T, VB, ACT, BACKWARD><<<(unsigned)blocks, kNT, 0, st>>>(p.s, (int)(blocks * per));
+}
 template <typename T, int VB, int ACT>
 void small_forward(const Plan& p, cudaStream_t st) {
   const long long teams = (long long)p.s.a.B * p.s.a.G;
@@ -754,7 +936,7 @@ void small_forward(const Plan& p, cudaStream_t st) {
   } else {
     const unsigned grid = (unsigned)((teams + kNT / p.s.T - 1) / (kNT / p.s.T));
     if (p.E == 1)
-      k_norm_small<T, VB, 1, false, ACT><<<grid, kNT, 0, st>>>(p.s);
+      rows_launch<T, VB, ACT, false>(p, st);
     else
       k_norm_small<T, VB, 8, false, ACT><<<grid, kNT, 0, st>>>(p.s);
   }
@@ -767,7 +949,7 @@ void small_backward(const Plan& p, cudaStream_t st) {
   } else {
     const unsigned grid = (unsigned)((teams + kNT / p.s.T - 1) / (kNT / p.s.T));
     if (p.E == 1)
-      k_norm_small_dx<T, VB, 1, false, ACT><<<grid, kNT, 0, st>>>(p.s);
+      rows_launch<T, VB, ACT, true>(p, st);
     else
       k_norm_small_dx<T, VB, 4, false, ACT><<<grid, kNT, 0, st>>>(p.s);
   }
@@ -788,7 +970,7 @@ void channel_sums(const Plan& p, cudaStream_t st) {
   const RowArgs& r = p.r;
   const dim3 grid(r.chunks * (FLAT ? 1 : r.a.B), r.colblocks);
   k_norm_bsum<T, VB, ACT, FLAT><<<grid, kNT, row_smem<T, VB>(r), st>>>(r);
-  const int groups = FLAT ? 0 : r.a.B * r.a.G, chan = r.a.dgamma ? ceil_div(r.a.C, 32) : 0;
+  const int groups = FLAT ? 0 : r.a.B * r.a.G, chan = r.a.dgamma ? ceil_div(r.a.C, 8) : 0;
   k_norm_bjoin<<<groups + chan, kNT, 0, st>>>(r, groups, (FLAT ? 1 : r.a.B) * r.chunks, r.a.ws + p.m12);
 }
 template <typename T, int VB, int ACT>
