@@ -16,7 +16,7 @@ namespace {
 // angle; the rest is fp32. A thread has one token and one unit of a head's channels (V pairs in two 16-byte
 // vectors, V / 2 pairs in one, or a single pair), forms their cosines and sines once, and goes over the heads.
 constexpr int kRThreads = 256;
-constexpr int kRHeads = 4;   // heads in flight
+constexpr int kRHeads = 2;   // heads read at once, one such group ahead
 
 template <typename T>
 struct Vec {
@@ -60,70 +60,77 @@ __global__ void __launch_bounds__(kRThreads) k_rotary(const __grid_constant__ Ro
   const int pair = unit * NP, c0 = MODE == 2 ? unit : unit * V;
   const bool turns = MODE == 1 ? c0 < a.rot : pair < half;
   const int copy = MODE == 0 ? a.rot + (unit - half / V) * V : MODE == 1 ? c0 : half + unit;
+  const int all = a.heads + a.heads2;
+  const int h0 = blockIdx.y * heads_each, h1 = min(h0 + heads_each, all);
+  auto element = [&](int h, bool out) {   // of this token's row of head h, from x (y) or x2 (y2)
+    const bool second = h >= a.heads;
+    const long long* s = out ? (second ? a.y2s : a.ys) : (second ? a.x2s : a.xs);
+    return b * s[0] + (second ? h - a.heads : h) * s[1] + n * s[2];
+  };
+  struct Group {
+    Vec<T> p[kRHeads], q[kRHeads];
+    T sp[kRHeads], sq[kRHeads];
+  };
+  auto load = [&](Group& g, int h) {
+#pragma unroll
+    for (int e = 0; e < kRHeads; ++e)
+      if (h + e < h1) {
+        const T* x = static_cast<const T*>(h + e >= a.heads ? a.x2 : a.x) + element(h + e, false);
+        if constexpr (MODE == 2) {
+          g.sp[e] = x[turns ? c0 : copy];
+          if (turns) g.sq[e] = x[c0 + half];
+        } else {
+          g.p[e] = vload(x + (turns ? c0 : copy));
+          if (MODE == 0 && turns) g.q[e] = vload(x + c0 + half);
+        }
+      }
+  };
+  Group cur, next;
+  load(cur, h0);   // under way while the angles are formed
   float2 w[NP];
   if (turns) {
     const double pos = (double)a.positions[tok];
 #pragma unroll
     for (int i = 0; i < NP; ++i) w[i] = pair + i < half ? turn(a, pos, pair + i) : make_float2(1.f, 0.f);
   }
-  const int all = a.heads + a.heads2;
-  const int h0 = blockIdx.y * heads_each, h1 = min(h0 + heads_each, all);
   for (int h = h0; h < h1; h += kRHeads) {
-    const T* x[kRHeads];
-    T* y[kRHeads];
-    Vec<T> p[kRHeads], q[kRHeads];
-    T sp[kRHeads], sq[kRHeads];
+    if (h + kRHeads < h1) load(next, h + kRHeads);
 #pragma unroll
     for (int e = 0; e < kRHeads; ++e) {
       if (h + e >= h1) break;
-      const bool second = h + e >= a.heads;
-      const int hh = second ? h + e - a.heads : h + e;
-      const long long* si = second ? a.x2s : a.xs;
-      const long long* so = second ? a.y2s : a.ys;
-      x[e] = static_cast<const T*>(second ? a.x2 : a.x) + b * si[0] + hh * si[1] + n * si[2];
-      y[e] = static_cast<T*>(second ? a.y2 : a.y) + b * so[0] + hh * so[1] + n * so[2];
-      if constexpr (MODE == 2) {
-        sp[e] = x[e][turns ? c0 : copy];
-        if (turns) sq[e] = x[e][c0 + half];
-      } else {
-        p[e] = vload(x[e] + (turns ? c0 : copy));
-        if (MODE == 0 && turns) q[e] = vload(x[e] + c0 + half);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < kRHeads; ++e) {
-      if (h + e >= h1) break;
+      T* y = static_cast<T*>(h + e >= a.heads ? a.y2 : a.y) + element(h + e, true);
       if (!turns) {
         if constexpr (MODE == 2)
-          y[e][copy] = sp[e];
+          y[copy] = cur.sp[e];
         else
-          vstore(y[e] + copy, p[e]);
+          vstore(y + copy, cur.p[e]);
       } else if constexpr (MODE == 0) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float u = to_f<T>(p[e].v[i]), v = to_f<T>(q[e].v[i]);
-          p[e].v[i] = from_f<T>(u * w[i].x - v * w[i].y);
-          q[e].v[i] = from_f<T>(u * w[i].y + v * w[i].x);
+          const float u = to_f<T>(cur.p[e].v[i]), v = to_f<T>(cur.q[e].v[i]);
+          cur.p[e].v[i] = from_f<T>(u * w[i].x - v * w[i].y);
+          cur.q[e].v[i] = from_f<T>(u * w[i].y + v * w[i].x);
         }
-        vstore(y[e] + c0, p[e]);
-        vstore(y[e] + c0 + half, q[e]);
+        vstore(y + c0, cur.p[e]);
+        vstore(y + c0 + half, cur.q[e]);
       } else if constexpr (MODE == 1) {
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
           if (c0 + i < a.rot) {   // channels behind rot stay as they are, bit by bit
-            const float u = to_f<T>(p[e].v[i]), v = to_f<T>(p[e].v[i + 1]);
+            const float u = to_f<T>(cur.p[e].v[i]), v = to_f<T>(cur.p[e].v[i + 1]);
             const float2 z = w[i / 2];
-            p[e].v[i] = from_f<T>(u * z.x - v * z.y);
-            p[e].v[i + 1] = from_f<T>(u * z.y + v * z.x);
+            cur.p[e].v[i] = from_f<T>(u * z.x - v * z.y);
+            cur.p[e].v[i + 1] = from_f<T>(u * z.y + v * z.x);
           }
         }
-        vstore(y[e] + c0, p[e]);
+        vstore(y + c0, cur.p[e]);
       } else {
-        const float u = to_f<T>(sp[e]), v = to_f<T>(sq[e]);
-        y[e][c0] = from_f<T>(u * w[0].x - v * w[0].y);
-        y[e][c0 + half] = from_f<T>(u * w[0].y + v * w[0].x);
+        const float u = to_f<T>(cur.sp[e]), v = to_f<T>(cur.sq[e]);
+        y[c0] = from_f<T>(u * w[0].x - v * w[0].y);
+        y[c0 + half] = from_f<T>(u * w[0].y + v * w[0].x);
       }
     }
+    cur = next;
   }
 }
 
@@ -156,27 +163,47 @@ constexpr int kNT = 256;         // threads per block
 constexpr int kNRows = 8;        // rows a thread has in flight
 constexpr int kMaxChunks = 64;   // row chunks per sample (large groups)
 
+using sm100::add2;
+using sm100::f2;
+using sm100::f2_hi;
+using sm100::f2_lo;
+using sm100::fma2;
+using sm100::mul2;
+
+// Channels go in pairs: the packed fp32 instructions take two at a time.
+__device__ __forceinline__ uint64_t both(float v) { return f2(v, v); }
 // 1 / (1 + exp(-z)): exponent and reciprocal within 2 units each (2^-22 relative)
-__device__ __forceinline__ float sigmoid_f(float z) {
+__device__ __forceinline__ float rcp_approx(float v) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + sm100::ex2_approx(z * -1.4426950408889634f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
+  const uint64_t t = mul2(z, both(-1.4426950408889634f));
+  const uint64_t d = add2(f2(sm100::ex2_approx(f2_lo(t)), sm100::ex2_approx(f2_hi(t))), both(1.f));
+  return f2(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d)));
+}
+__device__ __forceinline__ uint64_t normal_cdf2(uint64_t z) {   // 0.5 (1 + erf(z / sqrt 2))
+  return f2(fmaf(0.5f, erff(f2_lo(z) * 0.70710678118654752f), 0.5f), fmaf(0.5f, erff(f2_hi(z) * 0.70710678118654752f), 0.5f));
+}
 template <int ACT>
-__device__ __forceinline__ float act_f(float z) {
-  if (ACT == LFA_ACT_SILU) return z * sigmoid_f(z);
-  if (ACT == LFA_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+__device__ __forceinline__ uint64_t act2(uint64_t z) {
+  if (ACT == LFA_ACT_SILU) return mul2(z, sigmoid2(z));
+  if (ACT == LFA_ACT_GELU) return mul2(z, normal_cdf2(z));
   return z;
 }
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-  if (ACT == LFA_ACT_SILU) {
-    const float p = sigmoid_f(z);
-    return p * fmaf(z, 1.f - p, 1.f);
+__device__ __forceinline__ uint64_t slope2(uint64_t z) {
+  if (ACT == LFA_ACT_SILU) {   // p + z p (1 - p)
+    const uint64_t p = sigmoid2(z);
+    return fma2(mul2(z, p), fma2(p, both(-1.f), both(1.f)), p);
   }
-  if (ACT == LFA_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * sm100::ex2_approx(z * z * -0.72134752044448170f);
-  return 1.f;
+  if (ACT == LFA_ACT_GELU) {
+    const uint64_t t = mul2(mul2(z, z), both(-0.72134752044448170f));
+    const uint64_t e = f2(sm100::ex2_approx(f2_lo(t)), sm100::ex2_approx(f2_hi(t)));
+    return fma2(mul2(z, both(0.3989422804014327f)), e, normal_cdf2(z));
+  }
+  return both(1.f);
 }
 
 // VB bytes of a row, and its elements in fp32
@@ -205,23 +232,52 @@ __device__ __forceinline__ float raw_get(const Raw<VB>& r, int i) {
   if constexpr (sizeof(T) == 4) return __uint_as_float(r.w[i]);
   return __uint_as_float((i & 1) ? (r.w[i >> 1] & 0xffff0000u) : (r.w[i >> 1] << 16));
 }
+// elements 2 i, 2 i + 1 (a single element has a zero beside it), and back
 template <typename T, int VB>
-__device__ __forceinline__ Raw<VB> raw_make(const float* v) {
+__device__ __forceinline__ uint64_t raw_pair(const Raw<VB>& r, int i) {
+  if constexpr (sizeof(T) == 4) return f2(r.w[2 * i], VB == 4 ? 0u : r.w[(2 * i + 1) % ((VB + 3) / 4)]);
+  return f2(r.w[i] << 16, VB == 2 ? 0u : r.w[i] & 0xffff0000u);
+}
+template <typename T, int VB>
+__device__ __forceinline__ Raw<VB> raw_make(const uint64_t* v) {
   Raw<VB> r;
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < VB / 4; ++i) r.w[i] = __float_as_uint(v[i]);
+    for (int i = 0; i < VB / 4; ++i) r.w[i] = (uint32_t)(v[i / 2] >> (32 * (i & 1)));
   } else if constexpr (VB == 2) {
-    const __nv_bfloat16 b = __float2bfloat16_rn(v[0]);
+    const __nv_bfloat16 b = __float2bfloat16_rn(f2_lo(v[0]));
     r.w[0] = *reinterpret_cast<const uint16_t*>(&b);
   } else {
 #pragma unroll
     for (int i = 0; i < VB / 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f2_lo(v[i]), f2_hi(v[i]));
       r.w[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
   }
   return r;
+}
+// V values from channel c on of an fp32 array (`none` without one), in pairs; a single one has a zero beside it
+template <int V>
+__device__ __forceinline__ void load_pairs(const float* p, int c, float none, uint64_t* o) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; ++i) o[i] = both(none);
+    return;
+  }
+  p += c;
+  if constexpr (V % 4 == 0) {
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const float4 t = reinterpret_cast<const float4*>(p)[i];
+        o[2 * i] = f2(t.x, t.y);
+        o[2 * i + 1] = f2(t.z, t.w);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < (V + 1) / 2; ++i) o[i] = f2(p[2 * i], 2 * i + 1 < V ? p[2 * i + 1] : 0.f);
 }
 
 // sum over a team of T lanes (a power of two up to 32), or with T = 0 over the block
@@ -310,13 +366,13 @@ __global__ void __launch_bounds__(kNT) k_norm_small(const __grid_constant__ Smal
     long long off;
     int c;
     place<T, VB>(s, j, off, c);
-    float o[V];
+    constexpr int NP = (V + 1) / 2;
+    uint64_t o[NP], ga[NP], be[NP];
+    load_pairs<V>(a.gamma, g * dg + c, 1.f, ga);
+    load_pairs<V>(a.beta, g * dg + c, 0.f, be);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float z = (raw_get<T>(v[e], i) - mean) * rstd;
-      if (a.gamma) z = fmaf(z, a.gamma[g * dg + c + i], a.beta[g * dg + c + i]);
-      o[i] = act_f<ACT>(z);
-    }
+    for (int i = 0; i < NP; ++i)
+      o[i] = act2<ACT>(fma2(mul2(add2(raw_pair<T>(v[e], i), both(-mean)), both(rstd)), ga[i], be[i]));
     raw_store<VB>(y + off, raw_make<T, VB>(o));
   }
 }
@@ -325,7 +381,7 @@ __global__ void __launch_bounds__(kNT) k_norm_small(const __grid_constant__ Smal
 // takes (every teams-th (sample, group); teams is a multiple of G), U of them in flight.
 template <typename T, int VB, int ACT, bool BACKWARD>
 __global__ void __launch_bounds__(kNT) k_norm_rows(const __grid_constant__ SmallArgs s, int teams) {
-  constexpr int V = VB / sizeof(T), U = 4;
+  constexpr int V = VB / sizeof(T), U = BACKWARD ? 2 : 4;
   const NormArgs& a = s.a;
   const int tl = threadIdx.x & (s.T - 1), team = blockIdx.x * (kNT / s.T) + threadIdx.x / s.T;
   const long long total = (long long)a.B * a.G;
@@ -334,12 +390,10 @@ __global__ void __launch_bounds__(kNT) k_norm_rows(const __grid_constant__ Small
   long long off;
   int c;
   place<T, VB>(s, has ? tl : 0, off, c);
-  float ga[V], be[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    ga[i] = a.gamma ? a.gamma[g * dg + c + i] : 1.f;
-    be[i] = a.beta ? a.beta[g * dg + c + i] : 0.f;
-  }
+  constexpr int NP = (V + 1) / 2;
+  uint64_t ga[NP], be[NP];
+  load_pairs<V>(a.gamma, g * dg + c, 1.f, ga);
+  load_pairs<V>(a.beta, g * dg + c, 0.f, be);
   const float n = (float)(s.nvec * V), inv = 1.f / n;
   const long long step = (long long)(teams / a.G) * a.N * a.C;   // elements from one sample of this thread to its next
   long long at = (long long)(team / a.G) * a.N * a.C + g * dg + off;
@@ -401,25 +455,29 @@ __global__ void __launch_bounds__(kNT) k_norm_rows(const __grid_constant__ Small
             a.rstd[iu] = rs[u];
           }
           if (has) {
-            float o[V];
+            uint64_t o[NP];
 #pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = act_f<ACT>(fmaf((raw_get<T>(v[u], i) - m[u]) * rs[u], ga[i], be[i]));
+            for (int i = 0; i < NP; ++i)
+              o[i] = act2<ACT>(fma2(mul2(add2(raw_pair<T>(v[u], i), both(-m[u])), both(rs[u])), ga[i], be[i]));
             raw_store<VB>(y + at + u * step, raw_make<T, VB>(o));
           }
         }
       }
     } else {
-      float d[U][V], s1[U], s2[U];
+      uint64_t d[U][NP], xh[U][NP];
+      float s1[U], s2[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        s1[u] = s2[u] = 0.f;
+        uint64_t t1 = 0, t2 = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float xh = (raw_get<T>(v[u], i) - m[u]) * rs[u];
-          d[u][i] = ga[i] * raw_get<T>(w[u], i) * act_slope<ACT>(fmaf(xh, ga[i], be[i]));
-          s1[u] += d[u][i];   // dy is zero in threads without a vector
-          s2[u] = fmaf(d[u][i], xh, s2[u]);
+        for (int i = 0; i < NP; ++i) {
+          xh[u][i] = mul2(add2(raw_pair<T>(v[u], i), both(-m[u])), both(rs[u]));
+          d[u][i] = mul2(mul2(ga[i], raw_pair<T>(w[u], i)), slope2<ACT>(fma2(xh[u][i], ga[i], be[i])));
+          t1 = add2(t1, d[u][i]);   // dy is zero in threads without a vector and beside a lone channel
+          t2 = fma2(d[u][i], xh[u][i], t2);
         }
+        s1[u] = f2_lo(t1) + f2_hi(t1);
+        s2[u] = f2_lo(t2) + f2_hi(t2);
       }
       for (int o = s.T >> 1; o > 0; o >>= 1)
 #pragma unroll
@@ -430,13 +488,10 @@ __global__ void __launch_bounds__(kNT) k_norm_rows(const __grid_constant__ Small
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (has && id + (long long)u * teams < total) {
-          float o[V];
+          const uint64_t m1 = both(-s1[u] * inv), m2 = both(-s2[u] * inv);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float xh = (raw_get<T>(v[u], i) - m[u]) * rs[u];
-            o[i] = rs[u] * (d[u][i] - s1[u] * inv - xh * (s2[u] * inv));
-          }
-          raw_store<VB>(y + at + u * step, raw_make<T, VB>(o));
+          for (int i = 0; i < NP; ++i) d[u][i] = mul2(both(rs[u]), fma2(xh[u][i], m2, add2(d[u][i], m1)));
+          raw_store<VB>(y + at + u * step, raw_make<T, VB>(d[u]));
         }
     }
   }
@@ -445,7 +500,7 @@ __global__ void __launch_bounds__(kNT) k_norm_rows(const __grid_constant__ Small
 template <typename T, int VB, int E, bool BLOCK, int ACT>
 __global__ void __launch_bounds__(kNT) k_norm_small_dx(const __grid_constant__ SmallArgs s) {
   __shared__ float red[kNT / 32];
-  constexpr int V = VB / sizeof(T);
+  constexpr int V = VB / sizeof(T), NP = (V + 1) / 2;
   const NormArgs& a = s.a;
   const int team = BLOCK ? kNT : s.T, tl = threadIdx.x & (team - 1);
   const long long id = BLOCK ? blockIdx.x : (long long)blockIdx.x * (kNT / s.T) + threadIdx.x / s.T;
@@ -456,7 +511,6 @@ __global__ void __launch_bounds__(kNT) k_norm_small_dx(const __grid_constant__ S
   const T* dy = static_cast<const T*>(a.dy) + base;
   const float mean = on ? a.mean[id] : 0.f, rstd = on ? a.rstd[id] : 0.f;
   Raw<VB> v[E], w[E];
-  float s1 = 0.f, s2 = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int j = tl + e * team;
@@ -468,14 +522,16 @@ __global__ void __launch_bounds__(kNT) k_norm_small_dx(const __grid_constant__ S
       w[e] = raw_load<VB>(dy + off);
     }
   }
-  auto grad = [&](int e, int i, int c, float& xh) {
-    xh = (raw_get<T>(v[e], i) - mean) * rstd;
-    float z = xh, ga = 1.f;
-    if (a.gamma) {
-      ga = a.gamma[g * dg + c + i];
-      z = fmaf(xh, ga, a.beta[g * dg + c + i]);
+  uint64_t t1 = 0, t2 = 0;
+  auto grads = [&](int e, int c, uint64_t* d, uint64_t* xh) {
+    uint64_t ga[NP], be[NP];
+    load_pairs<V>(a.gamma, g * dg + c, 1.f, ga);
+    load_pairs<V>(a.beta, g * dg + c, 0.f, be);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      xh[i] = mul2(add2(raw_pair<T>(v[e], i), both(-mean)), both(rstd));
+      d[i] = mul2(mul2(ga[i], raw_pair<T>(w[e], i)), slope2<ACT>(fma2(xh[i], ga[i], be[i])));
     }
-    return ga * raw_get<T>(w[e], i) * act_slope<ACT>(z);
   };
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -484,17 +540,18 @@ __global__ void __launch_bounds__(kNT) k_norm_small_dx(const __grid_constant__ S
       long long off;
       int c;
       place<T, VB>(s, j, off, c);
+      uint64_t d[NP], xh[NP];
+      grads(e, c, d, xh);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float xh;
-        const float d = grad(e, i, c, xh);
-        s1 += d;
-        s2 = fmaf(d, xh, s2);
+      for (int i = 0; i < NP; ++i) {   // a lone channel's neighbour has dy = 0
+        t1 = add2(t1, d[i]);
+        t2 = fma2(d[i], xh[i], t2);
       }
     }
   }
   const float n = (float)(s.nvec * V);
-  const float m1 = team_sum<BLOCK>(s1, s.T, red) / n, m2 = team_sum<BLOCK>(s2, s.T, red) / n;
+  const float m1 = team_sum<BLOCK>(f2_lo(t1) + f2_hi(t1), s.T, red) / n;
+  const float m2 = team_sum<BLOCK>(f2_lo(t2) + f2_hi(t2), s.T, red) / n;
   if (!on) return;
   T* dx = static_cast<T*>(a.y) + base;
 #pragma unroll
@@ -504,14 +561,11 @@ __global__ void __launch_bounds__(kNT) k_norm_small_dx(const __grid_constant__ S
     long long off;
     int c;
     place<T, VB>(s, j, off, c);
-    float o[V];
+    uint64_t d[NP], xh[NP];
+    grads(e, c, d, xh);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float xh;
-      const float d = grad(e, i, c, xh);
-      o[i] = rstd * (d - m1 - xh * m2);
-    }
-    raw_store<VB>(dx + off, raw_make<T, VB>(o));
+    for (int i = 0; i < NP; ++i) d[i] = mul2(both(rstd), fma2(xh[i], both(-m2), add2(d[i], both(-m1))));
+    raw_store<VB>(dx + off, raw_make<T, VB>(d));
   }
 }
 
@@ -637,50 +691,49 @@ __global__ void __launch_bounds__(kNT) k_norm_group(const __grid_constant__ RowA
   }
 }
 
-// the channels' constants of a thread
+// the channels' constants of a thread, in pairs: minus the mean, 1 / deviation, gamma, beta
 template <int V>
 struct Chan {
-  float mean[V], rstd[V], ga[V], be[V];
+  static constexpr int NP = (V + 1) / 2;
+  uint64_t nm[NP], rs[NP], ga[NP], be[NP];
 };
 template <int V>
 __device__ __forceinline__ void chan_affine(const NormArgs& a, int c, Chan<V>& k) {
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    k.ga[i] = a.gamma ? a.gamma[c + i] : 1.f;
-    k.be[i] = a.beta ? a.beta[c + i] : 0.f;
-  }
+  load_pairs<V>(a.gamma, c, 1.f, k.ga);
+  load_pairs<V>(a.beta, c, 0.f, k.be);
 }
-template <int V>
+// ONE: the V channels are of one group
+template <int V, bool ONE>
 __device__ __forceinline__ void chan_stats(const NormArgs& a, int b, int c, int dg, Chan<V>& k) {
-  if (dg % V == 0) {   // one group
-    const size_t at = (size_t)b * a.G + c / dg;
-    const float m = a.mean[at], r = a.rstd[at];
+  const size_t at = (size_t)b * a.G;
+  if (ONE) {
+    const uint64_t m = both(-a.mean[at + c / dg]), r = both(a.rstd[at + c / dg]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      k.mean[i] = m;
-      k.rstd[i] = r;
+    for (int i = 0; i < Chan<V>::NP; ++i) {
+      k.nm[i] = m;
+      k.rs[i] = r;
     }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const size_t at = (size_t)b * a.G + (c + i) / dg;
-    k.mean[i] = a.mean[at];
-    k.rstd[i] = a.rstd[at];
+  for (int i = 0; i < Chan<V>::NP; ++i) {
+    const size_t g0 = at + (c + 2 * i) / dg, g1 = 2 * i + 1 < V ? at + (c + 2 * i + 1) / dg : g0;
+    k.nm[i] = f2(-a.mean[g0], -a.mean[g1]);
+    k.rs[i] = f2(a.rstd[g0], a.rstd[g1]);
   }
 }
 
-template <typename T, int VB, int ACT>
+template <typename T, int VB, int ACT, bool ONE>
 __global__ void __launch_bounds__(kNT) k_norm_apply(const __grid_constant__ RowArgs p) {
-  constexpr int V = VB / sizeof(T);
+  constexpr int V = VB / sizeof(T), NP = (V + 1) / 2;
   const NormArgs& a = p.a;
   const Lane l = lane_of<V>(p, a.N);
   if (!l.on) return;
   Chan<V> k;
   chan_affine(a, l.c, k);
-  chan_stats(a, l.b, l.c, a.C / a.G, k);
+  chan_stats<V, ONE>(a, l.b, l.c, a.C / a.G, k);
 #pragma unroll
-  for (int i = 0; i < V; ++i) k.ga[i] *= k.rstd[i];
+  for (int i = 0; i < NP; ++i) k.ga[i] = mul2(k.ga[i], k.rs[i]);
   const size_t base = (size_t)l.b * a.N * a.C + l.c;
   const T* x = static_cast<const T*>(a.x) + base;
   T* y = static_cast<T*>(a.y) + base;
@@ -692,16 +745,16 @@ __global__ void __launch_bounds__(kNT) k_norm_apply(const __grid_constant__ RowA
 #pragma unroll
     for (int e = 0; e < kNRows; ++e)
       if (r + e * p.rl < l.r1) {
-        float o[V];
+        uint64_t o[NP];
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = act_f<ACT>(fmaf(raw_get<T>(v[e], i) - k.mean[i], k.ga[i], k.be[i]));
+        for (int i = 0; i < NP; ++i) o[i] = act2<ACT>(fma2(add2(raw_pair<T>(v[e], i), k.nm[i]), k.ga[i], k.be[i]));
         raw_store<VB>(y + (size_t)(r + e * p.rl) * a.C, raw_make<T, VB>(o));
       }
   }
 }
 
 // per-channel sums of dz and dz xhat over a chunk's rows: of one sample, or (FLAT) of all samples' rows in turn
-template <typename T, int VB, int ACT, bool FLAT>
+template <typename T, int VB, int ACT, bool ONE, bool FLAT>
 __global__ void __launch_bounds__(kNT) k_norm_bsum(const __grid_constant__ RowArgs p) {
   constexpr int V = VB / sizeof(T);
   constexpr int R = 4;   // rows in flight, of two tensors
@@ -709,11 +762,16 @@ __global__ void __launch_bounds__(kNT) k_norm_bsum(const __grid_constant__ RowAr
   const NormArgs& a = p.a;
   const int dg = a.C / a.G;
   const Lane l = lane_of<V>(p, FLAT ? a.B * a.N : a.N);
-  float s1[V] = {}, s2[V] = {};
+  constexpr int NP = (V + 1) / 2;
+  uint64_t s1[NP] = {}, s2[NP] = {};   // of dz, and of dz (x - mean) (FLAT: dz xhat)
   if (l.on) {
     Chan<V> k;
     chan_affine(a, l.c, k);
-    if (!FLAT) chan_stats(a, l.b, l.c, dg, k);
+    if (!FLAT) {
+      chan_stats<V, ONE>(a, l.b, l.c, dg, k);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) k.ga[i] = mul2(k.ga[i], k.rs[i]);
+    }
     const size_t base = (size_t)l.b * a.N * a.C + l.c;
     const T* x = static_cast<const T*>(a.x) + base;
     const T* dy = static_cast<const T*>(a.dy) + base;
@@ -728,24 +786,28 @@ __global__ void __launch_bounds__(kNT) k_norm_bsum(const __grid_constant__ RowAr
 #pragma unroll
       for (int e = 0; e < R; ++e)
         if (r + e * p.rl < l.r1) {
-          if (FLAT) chan_stats(a, (r + e * p.rl) / a.N, l.c, dg, k);
+          if (FLAT) chan_stats<V, ONE>(a, (r + e * p.rl) / a.N, l.c, dg, k);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float xh = (raw_get<T>(v[e], i) - k.mean[i]) * k.rstd[i];
-            const float dz = raw_get<T>(w[e], i) * act_slope<ACT>(fmaf(xh, k.ga[i], k.be[i]));
-            s1[i] += dz;
-            s2[i] = fmaf(dz, xh, s2[i]);
+          for (int i = 0; i < NP; ++i) {
+            uint64_t d = add2(raw_pair<T>(v[e], i), k.nm[i]);
+            if (FLAT) d = mul2(d, k.rs[i]);
+            const uint64_t dz = mul2(raw_pair<T>(w[e], i), slope2<ACT>(fma2(d, k.ga[i], k.be[i])));
+            s1[i] = add2(s1[i], dz);
+            s2[i] = fma2(dz, d, s2[i]);
           }
         }
     }
+    if (!FLAT)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) s2[i] = mul2(s2[i], k.rs[i]);
   }
   const int width = p.cw * V, at = l.ty * width + (threadIdx.x % p.cw) * V;
   float* sq = sm + p.rl * width;
   if (l.ty < p.rl)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      sm[at + i] = s1[i];
-      sq[at + i] = s2[i];
+      sm[at + i] = (i & 1) ? f2_hi(s1[i / 2]) : f2_lo(s1[i / 2]);
+      sq[at + i] = (i & 1) ? f2_hi(s2[i / 2]) : f2_lo(s2[i / 2]);
     }
   __syncthreads();
   float* out = p.part + (size_t)blockIdx.x * 2 * a.C;
@@ -809,9 +871,9 @@ __global__ void __launch_bounds__(kNT) k_norm_bjoin(const __grid_constant__ RowA
   }
 }
 
-template <typename T, int VB, int ACT>
+template <typename T, int VB, int ACT, bool ONE>
 __global__ void __launch_bounds__(kNT) k_norm_dx(const __grid_constant__ RowArgs p, const float* m12) {
-  constexpr int V = VB / sizeof(T);
+  constexpr int V = VB / sizeof(T), NP = (V + 1) / 2;
   constexpr int R = 4;
   const NormArgs& a = p.a;
   const int dg = a.C / a.G;
@@ -819,13 +881,14 @@ __global__ void __launch_bounds__(kNT) k_norm_dx(const __grid_constant__ RowArgs
   if (!l.on) return;
   Chan<V> k;
   chan_affine(a, l.c, k);
-  chan_stats(a, l.b, l.c, dg, k);
-  float m1[V], m2[V];
+  chan_stats<V, ONE>(a, l.b, l.c, dg, k);
+  uint64_t m1[NP], m2[NP];   // minus the group's means of gamma dz and of gamma dz xhat
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const size_t at = 2 * ((size_t)l.b * a.G + (l.c + i) / dg);
-    m1[i] = m12[at];
-    m2[i] = m12[at + 1];
+  for (int i = 0; i < NP; ++i) {
+    const size_t at = (size_t)l.b * a.G, g0 = 2 * (at + (l.c + (ONE ? 0 : 2 * i)) / dg),
+                 g1 = ONE || 2 * i + 1 >= V ? g0 : 2 * (at + (l.c + 2 * i + 1) / dg);
+    m1[i] = f2(-m12[g0], -m12[g1]);
+    m2[i] = f2(-m12[g0 + 1], -m12[g1 + 1]);
   }
   const size_t base = (size_t)l.b * a.N * a.C + l.c;
   const T* x = static_cast<const T*>(a.x) + base;
@@ -842,12 +905,12 @@ __global__ void __launch_bounds__(kNT) k_norm_dx(const __grid_constant__ RowArgs
 #pragma unroll
     for (int e = 0; e < R; ++e)
       if (r + e * p.rl < l.r1) {
-        float o[V];
+        uint64_t o[NP];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float xh = (raw_get<T>(v[e], i) - k.mean[i]) * k.rstd[i];
-          const float d = k.ga[i] * raw_get<T>(w[e], i) * act_slope<ACT>(fmaf(xh, k.ga[i], k.be[i]));
-          o[i] = k.rstd[i] * (d - m1[i] - xh * m2[i]);
+        for (int i = 0; i < NP; ++i) {
+          const uint64_t xh = mul2(add2(raw_pair<T>(v[e], i), k.nm[i]), k.rs[i]);
+          const uint64_t d = mul2(mul2(k.ga[i], raw_pair<T>(w[e], i)), slope2<ACT>(fma2(xh, k.ga[i], k.be[i])));
+          o[i] = mul2(k.rs[i], fma2(xh, m2[i], add2(d, m1[i])));
         }
         raw_store<VB>(dx + (size_t)(r + e * p.rl) * a.C, raw_make<T, VB>(o));
       }
@@ -963,20 +1026,30 @@ void large_forward(const Plan& p, cudaStream_t st) {
   const dim3 grid(r.chunks * r.a.B, r.colblocks);
   k_norm_stats<T, VB><<<grid, kNT, row_smem<T, VB>(r), st>>>(r);
   k_norm_group<<<r.a.B * r.a.G, kNT, 0, st>>>(r);
-  k_norm_apply<T, VB, ACT><<<grid, kNT, 0, st>>>(r);
+  if (r.a.C / r.a.G % (VB / sizeof(T)) == 0)
+    k_norm_apply<T, VB, ACT, true><<<grid, kNT, 0, st>>>(r);
+  else
+    k_norm_apply<T, VB, ACT, false><<<grid, kNT, 0, st>>>(r);
 }
 template <typename T, int VB, int ACT, bool FLAT>
 void channel_sums(const Plan& p, cudaStream_t st) {
   const RowArgs& r = p.r;
   const dim3 grid(r.chunks * (FLAT ? 1 : r.a.B), r.colblocks);
-  k_norm_bsum<T, VB, ACT, FLAT><<<grid, kNT, row_smem<T, VB>(r), st>>>(r);
+  if (r.a.C / r.a.G % (VB / sizeof(T)) == 0)
+    k_norm_bsum<T, VB, ACT, true, FLAT><<<grid, kNT, row_smem<T, VB>(r), st>>>(r);
+  else
+    k_norm_bsum<T, VB, ACT, false, FLAT><<<grid, kNT, row_smem<T, VB>(r), st>>>(r);
   const int groups = FLAT ? 0 : r.a.B * r.a.G, chan = r.a.dgamma ? ceil_div(r.a.C, 8) : 0;
   k_norm_bjoin<<<groups + chan, kNT, 0, st>>>(r, groups, (FLAT ? 1 : r.a.B) * r.chunks, r.a.ws + p.m12);
 }
 template <typename T, int VB, int ACT>
 void large_backward(const Plan& p, cudaStream_t st) {
   channel_sums<T, VB, ACT, false>(p, st);
-  k_norm_dx<T, VB, ACT><<<dim3(p.r.chunks * p.r.a.B, p.r.colblocks), kNT, 0, st>>>(p.r, p.r.a.ws + p.m12);
+  const dim3 grid(p.r.chunks * p.r.a.B, p.r.colblocks);
+  if (p.r.a.C / p.r.a.G % (VB / sizeof(T)) == 0)
+    k_norm_dx<T, VB, ACT, true><<<grid, kNT, 0, st>>>(p.r, p.r.a.ws + p.m12);
+  else
+    k_norm_dx<T, VB, ACT, false><<<grid, kNT, 0, st>>>(p.r, p.r.a.ws + p.m12);
 }
 
 // f.template operator()<T, VB, ACT>() for the vector's bytes and the activation
