@@ -368,7 +368,8 @@ typedef struct {
 } lfa_decay_config;
 
 /* Bytes of device workspace (256-byte aligned, overwritten) of lfa_decay_forward (backward = 0) or
- * lfa_decay_backward (backward = 1); at least 256; 0 for a config that these calls refuse. */
+ * lfa_decay_backward (backward = 1); 0 for a config that these calls refuse. 256 says that the call uses
+ * none: its workspace may then be NULL. */
 size_t lfa_decay_workspace_size(const lfa_decay_config* cfg, int backward);
 
 /* Outputs O and, if S_out is not NULL, the state after each sequence's last token. lengths: device int32
@@ -434,7 +435,7 @@ typedef struct {
 } lfa_norm_config;
 
 /* Bytes of device workspace (256-byte aligned, overwritten) of lfa_group_norm (backward = 0) or its backward
- * (1); at least 256; 0 for a config that these calls refuse. */
+ * (1); 0 for a config that these calls refuse. 256 says that the call uses none: it may then be NULL. */
 size_t lfa_group_norm_workspace_size(const lfa_norm_config* cfg, int backward);
 /* y may be x. */
 lfa_status lfa_group_norm(const lfa_norm_config* cfg, const void* x, const float* gamma, const float* beta,

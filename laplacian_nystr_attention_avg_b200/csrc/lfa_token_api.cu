@@ -12,8 +12,10 @@ using lfa::DecayJob;
 
 bool ok16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool ok16_or_null(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// What the size calls answer: 256 says that none is used, so a used one is larger however little it holds
+size_t ws_bytes(size_t used) { return used == 0 ? 256 : 256 + (used + 255) / 256 * 256; }
 bool ok_ws(const void* p, size_t bytes, size_t need) {
-  return p && (reinterpret_cast<uintptr_t>(p) & 255u) == 0 && bytes >= need;
+  return need <= 256 || (p && (reinterpret_cast<uintptr_t>(p) & 255u) == 0 && bytes >= need);
 }
 int elem(int dtype) { return dtype == LFA_BF16 ? 2 : 4; }
 
@@ -66,7 +68,7 @@ extern "C" {
 size_t lfa_decay_workspace_size(const lfa_decay_config* cfg, int backward) {
   if (check(cfg) != LFA_OK) return 0;
   const size_t n = 4 * lfa::decay_workspace_floats(cfg->B, cfg->heads, cfg->N, cfg->dk, cfg->dv, backward ? 3 : 1, cfg->dtype);
-  return n < 256 ? 256 : (n + 255) / 256 * 256;
+  return ws_bytes(n);
 }
 
 lfa_status lfa_decay_forward(const lfa_decay_config* c, const void* Q, const void* K, const void* V,
@@ -261,7 +263,7 @@ static lfa_status check_norm(const lfa_norm_config* c) {
 size_t lfa_group_norm_workspace_size(const lfa_norm_config* cfg, int backward) {
   if (check_norm(cfg) != LFA_OK) return 0;
   const size_t n = lfa::norm_workspace_floats(cfg->B, cfg->N, cfg->C, cfg->groups, cfg->dtype, backward) * sizeof(float);
-  return n < 256 ? 256 : (n + 255) / 256 * 256;
+  return ws_bytes(n);
 }
 
 lfa_status lfa_group_norm(const lfa_norm_config* c, const void* x, const float* gamma, const float* beta, void* y,

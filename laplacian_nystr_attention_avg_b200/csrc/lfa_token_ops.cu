@@ -16,6 +16,7 @@ namespace {
 // angle; the rest is fp32. A thread has one token and one unit of a head's channels (V pairs in two 16-byte
 // vectors, V / 2 pairs in one, or a single pair), forms their cosines and sines once, and goes over the heads.
 constexpr int kRThreads = 256;
+constexpr int kWave = 3 * 148;   // blocks of 256 threads with 80 registers that run at once
 constexpr int kRHeads = 2;   // heads read at once, one such group ahead
 
 template <typename T>
@@ -138,10 +139,19 @@ template <typename T, int MODE>
 void rotary_launch(const RotaryArgs& a, cudaStream_t st) {
   const int units = rotary_units<T, MODE>(a.d, a.rot), tokens = kRThreads / units;   // units <= 256
   const int tiles = ceil_div(a.B * a.N, tokens), all = a.heads + a.heads2;
-  // heads are split over blocks until about four blocks an SM run; the angles are then formed once more each
-  int parts = tiles < 592 ? ceil_div(592, tiles) : 1;
-  if (parts > all) parts = all;
-  const int each = ceil_div(all, parts);
+  // Heads are split over blocks, which form the angles once each (worth about three heads): as many parts as give
+  // the shortest run of whole waves, three blocks an SM at a time (4 x 4096 tokens, 32 heads: one part 57 us in
+  // 1.5 waves, two 51 us in 3).
+  int each = all;
+  long long best = 0;
+  for (int parts = 1; parts <= all; ++parts) {
+    const int e = ceil_div(all, parts);
+    const long long waves = ((long long)tiles * ceil_div(all, e) + kWave - 1) / kWave, cost = waves * (e + 3);
+    if (best == 0 || cost < best) {
+      best = cost;
+      each = e;
+    }
+  }
   k_rotary<T, MODE><<<dim3(tiles, ceil_div(all, each)), kRThreads, 0, st>>>(a, units, tokens, each);
 }
 template <typename T>
@@ -706,15 +716,14 @@ __device__ __forceinline__ void chan_affine(const NormArgs& a, int c, Chan<V>& k
 template <int V, bool ONE>
 __device__ __forceinline__ void chan_stats(const NormArgs& a, int b, int c, int dg, Chan<V>& k) {
   const size_t at = (size_t)b * a.G;
-  if (ONE) {
+  if constexpr (ONE) {
     const uint64_t m = both(-a.mean[at + c / dg]), r = both(a.rstd[at + c / dg]);
 #pragma unroll
     for (int i = 0; i < Chan<V>::NP; ++i) {
       k.nm[i] = m;
       k.rs[i] = r;
     }
-    return;
-  }
+  } else
 #pragma unroll
   for (int i = 0; i < Chan<V>::NP; ++i) {
     const size_t g0 = at + (c + 2 * i) / dg, g1 = 2 * i + 1 < V ? at + (c + 2 * i + 1) / dg : g0;
@@ -964,7 +973,7 @@ Plan plan_norm(int B, int N, int C, int G, int es, bool backward) {
   r.colblocks = ceil_div(cv, r.cw);
   const long long rows = p.small ? (long long)B * N : N;
   const int samples = p.small ? 1 : B;
-  long long want = ceil_div(148 * 6, samples * r.colblocks < 1000 ? samples * r.colblocks : 1000);
+  long long want = kWave / ((long long)samples * r.colblocks < kWave ? samples * r.colblocks : kWave);   // one wave
   const long long most = (rows + r.rl * kNRows - 1) / (r.rl * kNRows);
   if (want > most) want = most;
   if (want < 1) want = 1;
@@ -979,7 +988,7 @@ Plan plan_norm(int B, int N, int C, int G, int es, bool backward) {
   return p;
 }
 
-// blocks of k_norm_rows: at most about eight an SM, with a number of teams that G divides
+// blocks of k_norm_rows: at most one wave, with a number of teams that G divides
 template <typename T, int VB, int ACT, bool BACKWARD>
 void rows_launch(const Plan& p, cudaStream_t st) {
   const int per = kNT / p.s.T, G = p.s.a.G;
@@ -987,7 +996,7 @@ void rows_launch(const Plan& p, cudaStream_t st) {
   for (int d = per; d > 1; d /= 2)
     if (unit % 2 == 0) unit /= 2;
   const long long teams = (long long)p.s.a.B * G, need = (teams + per - 1) / per;
-  long long blocks = need < 8 * 148 ? need : 8 * 148;
+  long long blocks = need < kWave ? need : kWave;
   blocks = (blocks + unit - 1) / unit * unit;
   k_norm_rows<T, VB, ACT, BACKWARD><<<(unsigned)blocks, kNT, 0, st>>>(p.s, (int)(blocks * per));
 }

@@ -16,7 +16,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import lfa
-from .lfa import LFA_BF16, LFA_ERR_INVALID_ARG, LFA_F32, LFA_OK, LfaError, _check, _ptr, _require
+from .lfa import LFA_BF16, LFA_F32, _check, _ptr, _require
 
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
 _DTYPES = {torch.bfloat16: LFA_BF16, torch.float32: LFA_F32}
@@ -158,10 +158,10 @@ def _plan(kind, extra, tensors, check):
     return plan
 
 
-def _workspace(nbytes: int, device: torch.device, what: str) -> torch.Tensor:
-    if nbytes == 0:
-        raise LfaError(LFA_ERR_INVALID_ARG, what)
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)   # torch allocations are 512-byte aligned
+def _workspace(nbytes: int, device: torch.device) -> Optional[torch.Tensor]:
+    """A call's workspace (torch allocations are 512-byte aligned). None where it uses none, or refuses its
+    configuration: the call itself then says why."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 256 else None
 
 
 # ---- decay attention -------------------------------------------------------------------------------
@@ -221,9 +221,9 @@ def decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: 
         O = _new(v, lengths)
     if S_out is None and return_state:
         S_out = torch.empty(state, dtype=torch.float32, device=device)
-    ws = _workspace(nbytes, device, "lfa_decay_workspace_size")
+    ws = _workspace(nbytes, device)
     _check(lib.lfa_decay_forward(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(S0),
-                                 _ptr(lengths), O.data_ptr(), _ptr(S_out), ws.data_ptr(), nbytes,
+                                 _ptr(lengths), O.data_ptr(), _ptr(S_out), _ptr(ws), nbytes,
                                  _cur(device.index)), "lfa_decay_forward")
     return O, S_out
 
@@ -260,10 +260,10 @@ def decay_backward(q, k, v, log_decay, dO, *, scale=None, S0=None, lengths=None,
     dQ, dK, dV = (_strided_like(like, lengths) if t is None else t for t, like in ((dQ, q), (dK, k), (dV, v)))
     if dS0 is None and return_state:
         dS0 = torch.empty(state, dtype=torch.float32, device=device)
-    ws = _workspace(nbytes, device, "lfa_decay_workspace_size")
+    ws = _workspace(nbytes, device)
     _check(lib.lfa_decay_backward(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(S0),
                                   _ptr(lengths), dO.data_ptr(), _ptr(dS_out), dQ.data_ptr(), dK.data_ptr(),
-                                  dV.data_ptr(), _ptr(dS0), ws.data_ptr(), nbytes, _cur(device.index)),
+                                  dV.data_ptr(), _ptr(dS0), _ptr(ws), nbytes, _cur(device.index)),
            "lfa_decay_backward")
     return dQ, dK, dV, dS0
 
@@ -436,11 +436,11 @@ def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = Non
     cfg, device, nbytes = _plan("norm", (groups, eps, act), (x, gamma, beta, out), check)
     if out is None:
         out = torch.empty_like(x)
-    ws = _workspace(nbytes, device, "lfa_group_norm_workspace_size")
+    ws = _workspace(nbytes, device)
     mean = torch.empty((cfg.B, cfg.groups), dtype=torch.float32, device=device)
     rstd = torch.empty((cfg.B, cfg.groups), dtype=torch.float32, device=device)
     _check(lib.lfa_group_norm(cfg, x.data_ptr(), _ptr(gamma), _ptr(beta), out.data_ptr(), mean.data_ptr(),
-                              rstd.data_ptr(), ws.data_ptr(), nbytes, _cur(device.index)), "lfa_group_norm")
+                              rstd.data_ptr(), _ptr(ws), nbytes, _cur(device.index)), "lfa_group_norm")
     return out, mean, rstd
 
 
@@ -465,14 +465,14 @@ def group_norm_backward(x, dy, mean, rstd, groups: int, gamma=None, beta=None, *
     cfg, device, nbytes = _plan("norm_backward", (groups, eps, act), (x, dy, mean, rstd, gamma, beta, dx), check)
     if dx is None:
         dx = torch.empty_like(x)
-    ws = _workspace(nbytes, device, "lfa_group_norm_workspace_size")
+    ws = _workspace(nbytes, device)
     dgamma = dbeta = None
     if gamma is not None:
         dgamma = torch.empty(cfg.C, dtype=torch.float32, device=device)
         dbeta = torch.empty(cfg.C, dtype=torch.float32, device=device)
     _check(lib.lfa_group_norm_backward(cfg, x.data_ptr(), dy.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
                                        _ptr(gamma), _ptr(beta), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta),
-                                       ws.data_ptr(), nbytes, _cur(device.index)), "lfa_group_norm_backward")
+                                       _ptr(ws), nbytes, _cur(device.index)), "lfa_group_norm_backward")
     return dx, dgamma, dbeta
 
 

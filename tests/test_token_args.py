@@ -78,14 +78,13 @@ def test_decay_gradients_may_not_overlap_themselves(lib):
 
 
 @pytest.mark.parametrize("kw", [dict(Q=None), dict(K=None), dict(V=None), dict(O=None), dict(ld=None), dict(Q=A + 8),
-                                dict(O=A + 2), dict(S0=A + 4), dict(S=A + 8), dict(ws=None), dict(ws=A + 16), dict(n=0),
-                                dict(O=A), dict(O=3 * A)])
+                                dict(O=A + 2), dict(S0=A + 4), dict(S=A + 8), dict(O=A), dict(O=3 * A)])
 def test_decay_forward_refuses_pointers(lib, kw):
     assert _forward(lib, _dc(), **kw) == BAD
 
 
 @pytest.mark.parametrize("kw", [dict(Q=None), dict(dO=None), dict(dQ=None), dict(dK=A + 2), dict(dV=None), dict(dS=A + 4),
-                                dict(dS0=A + 4), dict(n=0), dict(dQ=A), dict(dK=4 * A), dict(dQ=6 * A), dict(dV=5 * A),
+                                dict(dS0=A + 4), dict(dQ=A), dict(dK=4 * A), dict(dQ=6 * A), dict(dV=5 * A),
                                 dict(S0=8 * A, dS0=8 * A), dict(dS=8 * A, dS0=8 * A)])
 def test_decay_backward_refuses_pointers(lib, kw):
     assert _backward(lib, _dc(), **kw) == BAD
@@ -110,6 +109,11 @@ def test_decay_workspace_sizes(lib):
         for bwd in (0, 1):
             n = lib.lfa_decay_workspace_size(_dc(B=1, heads=1, N=N), bwd)
             assert n >= 256 and n % 256 == 0
+    c = _dc(B=1, heads=1, N=65536)          # split along the sequence: the states need room
+    for call, bwd in ((_forward, 0), (_backward, 1)):
+        n = lib.lfa_decay_workspace_size(c, bwd)
+        assert n > 256
+        assert call(lib, c, ws=None) == BAD and call(lib, c, ws=A + 16, n=n) == BAD and call(lib, c, n=n - 1) == BAD
 
 
 def _rc(**kw):
@@ -166,9 +170,12 @@ def test_norm_refuses_pointers(lib):
     f, b, c = lib.lfa_group_norm, lib.lfa_group_norm_backward, _nc()
     n = 1 << 30
     for p in ([None, A, A, 2 * A, A, A, A, n], [A, A, None, 2 * A, A, A, A, n], [A, None, A, 2 * A, A, A, A, n],
-              [A, A, A, None, A, A, A, n], [A, A, A, 2 * A, None, A, A, n], [A, A, A, 2 * A, A, A, None, n],
-              [A, A, A, 2 * A, A, A, A, 0], [A, A, A, 2 * A, A, A, A + 16, n], [A + 2, A, A, 2 * A, A, A, A, n]):
+              [A, A, A, None, A, A, A, n], [A, A, A, 2 * A, None, A, A, n], [A + 2, A, A, 2 * A, A, A, A, n]):
         assert f(c, *p, None) == BAD
+    big = _nc(N=1 << 16)                     # in row chunks: needs a workspace
+    assert lib.lfa_group_norm_workspace_size(big, 0) > 256
+    for p in ([A, A, A, 2 * A, A, A, None, n], [A, A, A, 2 * A, A, A, A, 256], [A, A, A, 2 * A, A, A, A + 16, n]):
+        assert f(big, *p, None) == BAD
     for p in ([None, A, A, A, A, A, 2 * A, A, A, A, n], [A, None, A, A, A, A, 2 * A, A, A, A, n],
               [A, A, None, A, A, A, 2 * A, A, A, A, n], [A, A, A, A, A, A, 2 * A, None, A, A, n],
               [A, A, A, A, None, None, 2 * A, A, A, A, n], [A, A, A, A, A, A, None, A, A, A, n],
@@ -225,3 +232,12 @@ def test_dense_form_is_the_recurrence():
             st = torch.exp(ld.double())[:, None, None] * st + k[b, :, t, :, None] * v[b, :, t, None, :]
             assert torch.allclose(o[b, :, t], 0.5 * (q[b, :, t, None] @ st)[:, 0], atol=1e-12)
         assert torch.allclose(S[b], st, atol=1e-12)
+
+
+def test_a_small_workspace_is_not_taken_for_none(lib):
+    # the backward's channel sums of 8 channels are 64 bytes: the size must still differ from "none is used"
+    for C, groups in ((8, 1), (8, 8), (4, 2)):
+        c = _nc(B=1, N=1, C=C, groups=groups, dtype=lfa.LFA_F32)
+        n = lib.lfa_group_norm_workspace_size(c, 1)
+        assert n > 256
+        assert lib.lfa_group_norm_backward(c, A, A, A, A, A, A, 2 * A, A, A, None, 0, None) == BAD
