@@ -11,27 +11,225 @@
 //   R'  = l^n R + c_state sum_j l^(n-j) y_j z_j^T.
 // Every power of l in use has an exponent >= 0, so nothing overflows however small l is. R is carried in fp32;
 // with l near 1 the rounding of l^n would bias every chunk alike, so there l^n R is R + expm1(n log l) R.
-#include "lfa_token.h"
+#include <string.h>
 
 #include "lfa_internal.h"
+#include "lfa_token.h"
 
 namespace lfa {
 namespace {
 
-// ---- CUDA-core run (fp32 arithmetic throughout) ------------------------------------------------------
-constexpr int kCC = 32;          // tokens per step
-constexpr int kCB = 64;          // columns of Z a CTA takes
-constexpr int kCT = 256;
-constexpr int kCStride = kDecayMaxD + 4;
+// ---- fp32 tensors: the run on CUDA cores --------------------------------------------------------------
+// A block takes CB columns of one segment of a unit's tokens and walks it 64 tokens at a time, everything staged in
+// shared memory; the state R [da][CB] lives there. A thread has a 4 x 4 tile of each product, which makes 64
+// multiply-adds per eight 16-byte reads; above the diagonal nothing is computed, by the rows of a warp.
+// STATE: the segment's own state only.
+constexpr int kCC = 64;   // tokens per step
 
+constexpr int CB = 64;    // columns of z a block takes
+
+template <int DA>
 struct CoreSmem {
-  float X[kCC][kCStride];
-  float Y[kCC][kCStride];
-  float Z[kCC][kCB + 4];
+  float X[kCC][DA + 4];
+  float Y[kCC][DA + 4];
+  float Z[kCC][CB + 4];
   float P[kCC][kCC + 4];
-  float R[kDecayMaxD][kCB + 4];
+  float R[DA][CB + 4];
   float pw[kCC + 1];
 };
+
+__device__ __forceinline__ void fma4(float4& a, float s, const float4& v) {
+  a.x = fmaf(s, v.x, a.x);
+  a.y = fmaf(s, v.y, a.y);
+  a.z = fmaf(s, v.z, a.z);
+  a.w = fmaf(s, v.w, a.w);
+}
+__device__ __forceinline__ float dot4(const float4& a, const float4& b, float c) {
+  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+__device__ __forceinline__ float part(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+struct CoreArgs {
+  DecayArgs a;
+  int segs, seg_chunks;        // chunks of kDecayChunk tokens
+  const float* seg_init[3];    // segs > 1: R at each segment's start, [units][segs]
+  float* local[2];             // STATE: where the segments' own states go
+};
+
+template <int DA, bool STATE>
+__global__ void __launch_bounds__(4 * CB) k_decay_core(const __grid_constant__ CoreArgs ca) {
+  extern __shared__ float4 smem_f4[];
+  CoreSmem<DA>& s = *reinterpret_cast<CoreSmem<DA>*>(smem_f4);
+  constexpr int NT = 4 * CB, TJ = CB / 4, NQ = kCC / TJ;
+  const DecayArgs& a = ca.a;
+  const int jx = blockIdx.z % a.njobs, seg = blockIdx.z / a.njobs;
+  const DecayJob& jb = a.job[jx];
+  const int c0 = blockIdx.y * CB, u = blockIdx.x, b = u / a.heads, h = u % a.heads, t = threadIdx.x;
+  if (c0 >= jb.db) return;
+  const int da = jb.da, nb = min(CB, jb.db - c0), L = unit_length(a.lengths, b, a.N);
+  const bool rev = jb.rev;
+  const int nch = (L + kDecayChunk - 1) / kDecayChunk;   // the sequence's chunks, in whole segments
+  const int lo = seg * ca.seg_chunks, hi = min(lo + ca.seg_chunks, nch);
+  if (hi <= lo && !(L == 0 && seg == 0 && !STATE)) return;
+  if (STATE && (rev ? seg == 0 : hi == nch)) return;     // nothing follows this segment
+  const bool ends = !STATE && jb.fin && (L == 0 || (rev ? seg == 0 : hi == nch));
+  const int t_lo = lo * kDecayChunk, t_hi = min(L, hi * kDecayChunk), steps = (t_hi - t_lo + kCC - 1) / kCC;
+  const float ld = decay_log(a.log_decay[h]);
+  const float* X = static_cast<const float*>(jb.X) + b * jb.xs[0] + h * jb.xs[1];
+  const float* Y = static_cast<const float*>(jb.Y) + b * jb.ys[0] + h * jb.ys[1];
+  const float* Z = static_cast<const float*>(jb.Z) + b * jb.zs[0] + h * jb.zs[1] + c0;
+  float* O = static_cast<float*>(jb.O) + b * jb.os[0] + h * jb.os[1] + c0;
+  const size_t dd = (size_t)da * jb.db;
+  for (int n = t; n <= kCC; n += NT) s.pw[n] = expf(ld * n);
+  {
+    const bool split = ca.segs > 1 && L > 0;
+    const float* src = STATE ? nullptr : split ? ca.seg_init[jx] : jb.init;
+    const size_t at = split ? ((size_t)u * ca.segs + seg) * dd : u * dd;
+    const float f0 = L > 0 && !split && jb.init_decays ? expf(ld) : 1.f;
+    for (int e = t; e < DA * CB; e += NT) {
+      const int r = e / CB, c = e % CB;
+      s.R[r][c] = src && r < da && c < nb
+                      ? f0 * src[at + (jb.trans ? (size_t)(c0 + c) * da + r : (size_t)r * jb.db + c0 + c)]
+                      : 0.f;
+    }
+  }
+  const int ti = t / TJ, tj = t % TJ, i0 = 4 * ti, cc = 4 * tj;
+  const int w0 = (t & ~31) / TJ * 4, w1 = w0 + 128 / TJ;   // rows of this thread's warp
+  constexpr int NX = kCC * DA / 4 / NT, NZ = kCC * CB / 4 / NT;   // 16-byte vectors of a thread
+  float4 xr[STATE ? 1 : NX], yr[NX], zr[NZ];                      // the next step's, on their way
+  auto start = [&](int si) { return t_lo + (rev ? steps - 1 - si : si) * kCC; };
+  auto fetch = [&](int si) {
+    const int t0 = start(si), nv = min(kCC, t_hi - t0);
+    const float4 zero = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int e = t + i * NT, r = e / (DA / 4), c = e % (DA / 4) * 4;
+      const bool on = r < nv && c < da;
+      if (!STATE) xr[STATE ? 0 : i] = zero;
+      yr[i] = zero;
+      if (on) {
+        if (!STATE) xr[STATE ? 0 : i] = *reinterpret_cast<const float4*>(X + (t0 + r) * jb.xs[2] + c);
+        yr[i] = *reinterpret_cast<const float4*>(Y + (t0 + r) * jb.ys[2] + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NZ; ++i) {
+      const int e = t + i * NT, r = e / TJ, c = e % TJ * 4;
+      zr[i] = zero;
+      if (r < nv && c < nb) zr[i] = *reinterpret_cast<const float4*>(Z + (t0 + r) * jb.zs[2] + c);
+    }
+  };
+  if (steps > 0) fetch(0);
+  for (int si = 0; si < steps; ++si) {
+    const int t0 = start(si), nv = min(kCC, t_hi - t0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int e = t + i * NT, r = e / (DA / 4), c = e % (DA / 4) * 4;
+      if (!STATE) *reinterpret_cast<float4*>(&s.X[r][c]) = xr[STATE ? 0 : i];
+      *reinterpret_cast<float4*>(&s.Y[r][c]) = yr[i];
+    }
+#pragma unroll
+    for (int i = 0; i < NZ; ++i) {
+      const int e = t + i * NT, r = e / TJ, c = e % TJ * 4;
+      *reinterpret_cast<float4*>(&s.Z[r][c]) = zr[i];
+    }
+    __syncthreads();
+    if (si + 1 < steps) fetch(si + 1);
+    if constexpr (!STATE) {
+      {   // P = c_intra decay^|i-j| x_i . y_j on the causal side
+        float acc[4][NQ] = {};
+        for (int k = 0; k < da; k += 4) {
+          float4 x[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) x[p] = *reinterpret_cast<const float4*>(&s.X[i0 + p][k]);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if (rev ? TJ * q + TJ <= w0 : TJ * q >= w1) continue;   // wholly on the other side, for the warp
+            const float4 y = *reinterpret_cast<const float4*>(&s.Y[tj + TJ * q][k]);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) acc[p][q] = dot4(x[p], y, acc[p][q]);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          if (rev ? TJ * q + TJ <= w0 : TJ * q >= w1) continue;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const int j = tj + TJ * q, n = rev ? j - i0 - p : i0 + p - j;
+            s.P[i0 + p][j] = n >= 0 ? jb.c_intra * s.pw[n] * acc[p][q] : 0.f;
+          }
+        }
+      }
+      float4 acc[4] = {};
+      for (int k = 0; k < da; k += 4) {
+        float4 x[4], r[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          x[p] = *reinterpret_cast<const float4*>(&s.X[i0 + p][k]);
+          r[p] = *reinterpret_cast<const float4*>(&s.R[k + p][cc]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int p = 0; p < 4; ++p) fma4(acc[p], part(x[p], q), r[q]);
+      }
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int n = rev ? nv - 1 - i0 - p : i0 + p;
+        const float f = n >= 0 ? jb.c_inter * s.pw[n] : 0.f;
+        acc[p] = make_float4(acc[p].x * f, acc[p].y * f, acc[p].z * f, acc[p].w * f);
+      }
+      __syncwarp();   // P's rows are used by the warp that wrote them
+      for (int j = rev ? w0 : 0; j < (rev ? kCC : w1); j += 4) {
+        float4 w[4], z[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          w[p] = *reinterpret_cast<const float4*>(&s.P[i0 + p][j]);
+          z[p] = *reinterpret_cast<const float4*>(&s.Z[j + p][cc]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int p = 0; p < 4; ++p) fma4(acc[p], part(w[p], q), z[q]);
+      }
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        if (i0 + p < nv && cc < nb) *reinterpret_cast<float4*>(O + (t0 + i0 + p) * jb.os[2] + cc) = acc[p];
+      __syncthreads();   // R has been read
+    }
+    {   // R' = l^n R + c_state sum_j l^(n-j) y_j z_j^T (the run's last step: l^-fin_sub of that)
+      const int sub = !STATE && ends && !rev && si == steps - 1 ? jb.fin_sub : 0;
+      const Decay dec(ld * (nv - sub));
+      for (int r0 = 4 * ti; r0 < da; r0 += 64) {
+        float4 acc[4] = {};
+#pragma unroll 4
+        for (int j = 0; j < nv; ++j) {
+          const float w = jb.c_state * s.pw[(rev ? j + 1 : nv - j) - sub];
+          const float4 y = *reinterpret_cast<const float4*>(&s.Y[j][r0]);
+          float4 z = *reinterpret_cast<const float4*>(&s.Z[j][cc]);
+          z = make_float4(z.x * w, z.y * w, z.z * w, z.w * w);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) fma4(acc[p], part(y, p), z);
+        }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          float4* rp = reinterpret_cast<float4*>(&s.R[r0 + p][cc]);
+          const float4 r = *rp;
+          *rp = make_float4(dec(r.x) + acc[p].x, dec(r.y) + acc[p].y, dec(r.z) + acc[p].z, dec(r.w) + acc[p].w);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (STATE || ends) {
+    float* dst = STATE ? ca.local[jx] + ((size_t)u * ca.segs + seg) * dd : jb.fin + u * dd;
+    for (int e = t; e < da * CB; e += NT) {
+      const int r = e / CB, c = e % CB;
+      if (c < nb) dst[(size_t)r * jb.db + c0 + c] = s.R[r][c];   // a returned state is never a transposed one
+    }
+  }
+}
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T* p);
@@ -51,145 +249,6 @@ template <>
 __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float4 v) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-
-// grid: (units, column slices, jobs)
-template <typename T>
-__global__ void __launch_bounds__(kCT) k_decay_core(const __grid_constant__ DecayArgs a) {
-  extern __shared__ float4 smem_f4[];
-  CoreSmem& s = *reinterpret_cast<CoreSmem*>(smem_f4);
-  const DecayJob& jb = a.job[blockIdx.z];
-  const int c0 = blockIdx.y * kCB, u = blockIdx.x, b = u / a.heads, h = u % a.heads, t = threadIdx.x;
-  if (c0 >= jb.db) return;
-  const int da = jb.da, nb = min(kCB, jb.db - c0);
-  const float ld = decay_log(a.log_decay[h]);
-  const int L = unit_length(a.lengths, b, a.N);
-  const T* X = static_cast<const T*>(jb.X) + b * jb.xs[0] + h * jb.xs[1];
-  const T* Y = static_cast<const T*>(jb.Y) + b * jb.ys[0] + h * jb.ys[1];
-  const T* Z = static_cast<const T*>(jb.Z) + b * jb.zs[0] + h * jb.zs[1] + c0;
-  T* O = static_cast<T*>(jb.O) + b * jb.os[0] + h * jb.os[1] + c0;
-  const size_t st0 = (size_t)u * da * jb.db;
-  for (int n = t; n <= kCC; n += kCT) s.pw[n] = expf(ld * n);
-  const float f0 = (L > 0 && jb.init_decays) ? expf(ld) : 1.f;
-  for (int e = t; e < da * kCB; e += kCT) {
-    const int r = e / kCB, c = e % kCB;
-    float v = 0.f;
-    if (jb.init && c < nb)
-      v = f0 * jb.init[st0 + (jb.trans ? (size_t)(c0 + c) * da + r : (size_t)r * jb.db + c0 + c)];
-    s.R[r][c] = v;
-  }
-  const int nch = (L + kCC - 1) / kCC;
-  for (int ci = 0; ci < nch; ++ci) {
-    const int t0 = (jb.rev ? nch - 1 - ci : ci) * kCC, nv = min(kCC, L - t0);
-    __syncthreads();
-    for (int e = t; e < kCC * (da >> 2); e += kCT) {
-      const int r = e / (da >> 2), c = (e % (da >> 2)) * 4;
-      const bool on = r < nv;
-      *reinterpret_cast<float4*>(&s.X[r][c]) = on ? load4(X + (t0 + r) * jb.xs[2] + c) : make_float4(0, 0, 0, 0);
-      *reinterpret_cast<float4*>(&s.Y[r][c]) = on ? load4(Y + (t0 + r) * jb.ys[2] + c) : make_float4(0, 0, 0, 0);
-    }
-    for (int e = t; e < kCC * (kCB / 4); e += kCT) {
-      const int r = e / (kCB / 4), c = (e % (kCB / 4)) * 4;
-      *reinterpret_cast<float4*>(&s.Z[r][c]) =
-          (r < nv && c < nb) ? load4(Z + (t0 + r) * jb.zs[2] + c) : make_float4(0, 0, 0, 0);
-    }
-    __syncthreads();
-    {   // P = c_intra decay^|i-j| x_i . y_j on the causal side
-      const int i = t >> 3;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k = 0; k < da; k += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(&s.X[i][k]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 y = *reinterpret_cast<const float4*>(&s.Y[(t & 7) + 8 * q][k]);
-          acc[q] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, acc[q]))));
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int j = (t & 7) + 8 * q, n = jb.rev ? j - i : i - j;
-        s.P[i][j] = n >= 0 ? jb.c_intra * s.pw[n] * acc[q] : 0.f;
-      }
-    }
-    __syncthreads();
-    {
-      const int i0 = 2 * (t >> 4), c = 4 * (t & 15);
-      float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
-      for (int k = 0; k < da; k += 4) {
-        const float4 x0 = *reinterpret_cast<const float4*>(&s.X[i0][k]), x1 = *reinterpret_cast<const float4*>(&s.X[i0 + 1][k]);
-        const float xa[2][4] = {{x0.x, x0.y, x0.z, x0.w}, {x1.x, x1.y, x1.z, x1.w}};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 r = *reinterpret_cast<const float4*>(&s.R[k + q][c]);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            acc[p].x = fmaf(xa[p][q], r.x, acc[p].x);
-            acc[p].y = fmaf(xa[p][q], r.y, acc[p].y);
-            acc[p].z = fmaf(xa[p][q], r.z, acc[p].z);
-            acc[p].w = fmaf(xa[p][q], r.w, acc[p].w);
-          }
-        }
-      }
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int n = jb.rev ? nv - 1 - (i0 + p) : i0 + p;
-        const float f = n >= 0 ? jb.c_inter * s.pw[n] : 0.f;
-        acc[p].x *= f; acc[p].y *= f; acc[p].z *= f; acc[p].w *= f;
-      }
-      for (int j = 0; j < kCC; ++j) {
-        const float4 z = *reinterpret_cast<const float4*>(&s.Z[j][c]);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const float w = s.P[i0 + p][j];
-          acc[p].x = fmaf(w, z.x, acc[p].x);
-          acc[p].y = fmaf(w, z.y, acc[p].y);
-          acc[p].z = fmaf(w, z.z, acc[p].z);
-          acc[p].w = fmaf(w, z.w, acc[p].w);
-        }
-      }
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        if (i0 + p < nv && c < nb) store4(O + (t0 + i0 + p) * jb.os[2] + c, acc[p]);
-    }
-    __syncthreads();
-    {   // R' = l^n R + c_state sum_j l^(n-j) y_j z_j^T (the run's last chunk: l^-fin_sub of that)
-      const int sub = ci == nch - 1 ? jb.fin_sub : 0, c = 4 * (t & 15);
-      const Decay dec(ld * (nv - sub));
-      for (int r0 = 4 * (t >> 4); r0 < da; r0 += 64) {
-        float acc[4][4] = {};
-        for (int j = 0; j < nv; ++j) {
-          const float w = jb.c_state * s.pw[(jb.rev ? j + 1 : nv - j) - sub];
-          const float4 y = *reinterpret_cast<const float4*>(&s.Y[j][r0]);
-          float4 z = *reinterpret_cast<const float4*>(&s.Z[j][c]);
-          z.x *= w; z.y *= w; z.z *= w; z.w *= w;
-          const float ya[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            acc[q][0] = fmaf(ya[q], z.x, acc[q][0]);
-            acc[q][1] = fmaf(ya[q], z.y, acc[q][1]);
-            acc[q][2] = fmaf(ya[q], z.z, acc[q][2]);
-            acc[q][3] = fmaf(ya[q], z.w, acc[q][3]);
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float4* rp = reinterpret_cast<float4*>(&s.R[r0 + q][c]);
-          float4 r = *rp;
-          r.x = dec(r.x) + acc[q][0];
-          r.y = dec(r.y) + acc[q][1];
-          r.z = dec(r.z) + acc[q][2];
-          r.w = dec(r.w) + acc[q][3];
-          *rp = r;
-        }
-      }
-    }
-  }
-  __syncthreads();
-  if (jb.fin)
-    for (int e = t; e < da * kCB; e += kCT) {
-      const int r = e / kCB, c = e % kCB;
-      if (c < nb) jb.fin[st0 + (jb.trans ? (size_t)(c0 + c) * da + r : (size_t)r * jb.db + c0 + c)] = s.R[r][c];
-    }
 }
 
 // ---- one token --------------------------------------------------------------------------------------
@@ -263,21 +322,76 @@ __global__ void __launch_bounds__(kStepT) k_decay_step(const __grid_constant__ D
   }
 }
 
-template <typename T>
-cudaError_t run_core(const DecayArgs& a, cudaStream_t st) {
+template <int DA, bool STATE>
+cudaError_t run_core(const CoreArgs& c, int db, cudaStream_t st) {
+  constexpr int bytes = (int)sizeof(CoreSmem<DA>);
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = raise_smem(k_decay_core<T>, (int)sizeof(CoreSmem), done);
+  const cudaError_t e = raise_smem(k_decay_core<DA, STATE>, bytes, done);
   if (e != cudaSuccess) return e;
-  int db = 0;
-  for (int j = 0; j < a.njobs; ++j) db = a.job[j].db > db ? a.job[j].db : db;
-  k_decay_core<T><<<dim3(a.B * a.heads, ceil_div(db, kCB), a.njobs), kCT, sizeof(CoreSmem), st>>>(a);
+  k_decay_core<DA, STATE><<<dim3(c.a.B * c.a.heads, ceil_div(db, CB), c.a.njobs * c.segs), 4 * CB, bytes, st>>>(c);
   return cudaGetLastError();
+}
+template <bool STATE>
+cudaError_t run_core(const CoreArgs& c, cudaStream_t st) {
+  int da = 0, db = 0;
+  for (int j = 0; j < c.a.njobs; ++j) {
+    da = c.a.job[j].da > da ? c.a.job[j].da : da;
+    db = c.a.job[j].db > db ? c.a.job[j].db : db;
+  }
+  return da <= 64 ? run_core<64, STATE>(c, db, st) : run_core<128, STATE>(c, db, st);
+}
+
+cudaError_t launch_core(const DecayArgs& a, cudaStream_t st) {
+  const DecaySplit sp = decay_split(a.B, a.heads, a.N, a.njobs, LFA_F32);
+  CoreArgs c;
+  memset(&c, 0, sizeof(c));
+  c.a = a;
+  c.segs = sp.segs;
+  c.seg_chunks = sp.seg_chunks;
+  if (sp.segs > 1) {
+    CoreArgs s = c;
+    PrefixRun p[2];
+    s.a.njobs = state_runs(a, s.a.job, p);
+    const size_t states = (size_t)a.B * a.heads * sp.segs * a.job[0].da * a.job[0].db;
+    for (int i = 0; i < s.a.njobs; ++i) s.local[i] = a.ws + i * states;
+    cudaError_t e = run_core<true>(s, st);
+    if (e != cudaSuccess) return e;
+    e = launch_prefix(a, sp, p, s.a.njobs, st);
+    if (e != cudaSuccess) return e;
+    for (int i = 0; i < a.njobs; ++i) c.seg_init[i] = a.ws + (i == 0 ? 0 : states);
+  }
+  return run_core<false>(c, st);
 }
 
 }  // namespace
 
+// Runs whose end states are wanted segment by segment: the first one's and, in the backward, the last one's
+// (y = q, z = dO; the other reverse run has the same state transposed). States are [dk][dv].
+int state_runs(const DecayArgs& a, DecayJob* jobs, PrefixRun* p) {
+  const int n = a.njobs > 1 ? 2 : 1;
+  DecayJob run[2] = {a.job[0], a.job[a.njobs - 1]};
+  for (int i = 0; i < n; ++i) {
+    DecayJob j = run[i];
+    if (j.trans) {   // the same sums with y and z exchanged
+      const DecayJob o = j;
+      j.Y = o.Z;
+      j.Z = o.Y;
+      memcpy(j.ys, o.zs, sizeof(j.ys));
+      memcpy(j.zs, o.ys, sizeof(j.zs));
+      j.da = o.db;
+      j.db = o.da;
+      j.trans = 0;
+    }
+    p[i].init = j.init;
+    p[i].rev = j.rev;
+    p[i].init_decays = j.init_decays;
+    jobs[i] = j;
+  }
+  return n;
+}
+
 cudaError_t launch_decay(const DecayArgs& a, int dtype, cudaStream_t st) {
-  return dtype == LFA_BF16 ? launch_decay_tc(a, st) : run_core<float>(a, st);
+  return dtype == LFA_BF16 ? launch_decay_tc(a, st) : launch_core(a, st);
 }
 
 cudaError_t launch_decay_step(const DecayStepArgs& a, int dtype, cudaStream_t st) {

@@ -692,18 +692,42 @@ cudaError_t run(const TcArgs& a, int dp, int parts, int units, int njobs, cudaSt
 
 }  // namespace
 
-// One CTA fills an SM. With fewer than 148 of them the sequences are cut so that about 148 run at once, in
+// bf16: one CTA fills an SM. With fewer than 148 of them the sequences are cut so that about 148 run at once, in
 // segments of at least 4 chunks (below that the extra launches and the second reading of y and z cost more).
+// fp32: blocks of 256 threads share an SM, and arithmetic bounds them, so units of fewer blocks than SMs are cut
+// for two blocks an SM, down to single chunks.
 DecaySplit decay_split(int B, int heads, int N, int njobs, int dtype) {
   const int nch = ceil_div(N, kC);
   const long long ctas = (long long)B * heads * njobs;
-  int segs = dtype == LFA_BF16 && ctas < 148 ? (int)(148 / ctas) : 1;
-  if (segs > nch / 4) segs = nch / 4;
+  int segs = 1;
+  if (ctas < 148) segs = (int)((dtype == LFA_BF16 ? 148 : 296) / ctas);
+  const int most = dtype == LFA_BF16 ? nch / 4 : nch;
+  if (segs > most) segs = most;
   if (segs < 1) segs = 1;
   DecaySplit s;
   s.seg_chunks = ceil_div(nch, segs);
   s.segs = ceil_div(nch, s.seg_chunks);
   return s;
+}
+
+cudaError_t launch_prefix(const DecayArgs& a, const DecaySplit& sp, const PrefixRun* r, int n, cudaStream_t st) {
+  PrefixArgs p;
+  memset(&p, 0, sizeof(p));
+  p.st = a.ws;
+  for (int i = 0; i < n; ++i) {
+    p.init[i] = r[i].init;
+    p.rev[i] = r[i].rev;
+    p.init_decays[i] = r[i].init_decays;
+  }
+  p.log_decay = a.log_decay;
+  p.lengths = a.lengths;
+  p.heads = a.heads;
+  p.N = a.N;
+  p.segs = sp.segs;
+  p.seg_chunks = sp.seg_chunks;
+  p.dd = a.job[0].da * a.job[0].db;
+  k_decay_prefix<<<dim3(a.B * a.heads, ceil_div(p.dd, 256), n), 64, 0, st>>>(p);
+  return cudaGetLastError();
 }
 
 size_t decay_workspace_floats(int B, int heads, int N, int dk, int dv, int njobs, int dtype) {
@@ -744,44 +768,22 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
   // states before the segments: run 0 forwards, and for the backward its last run (y = q, z = dO)
   const size_t states = (size_t)units * sp.segs * dd;
   if (sp.segs > 1) {
-    const int ns = a.njobs > 1 ? 2 : 1;
-    PrefixArgs p;
-    memset(&p, 0, sizeof(p));
-    p.st = a.ws;
+    DecayJob jobs[2];
+    PrefixRun p[2];
+    const int ns = state_runs(a, jobs, p);
     for (int i = 0; i < ns; ++i) {
-      // the state as [dk][dv]: forwards y = k, z = v (the backward's run 0 has it transposed)
-      DecayJob j = a.job[i == 0 ? 0 : 2];
-      if (j.trans) {
-        DecayJob s = j;
-        s.Y = j.Z; s.Z = j.Y;
-        memcpy(s.ys, j.zs, sizeof(s.ys));
-        memcpy(s.zs, j.ys, sizeof(s.zs));
-        s.da = j.db; s.db = j.da;
-        j = s;
-      }
       TcJob& o = t.job[i];
-      if (!maps(&o, a, j, false)) return cudaErrorInvalidValue;
-      o.da = j.da;
-      o.db = j.db;
-      o.rev = j.rev;
-      o.c_state = j.c_state;
+      if (!maps(&o, a, jobs[i], false)) return cudaErrorInvalidValue;
+      o.da = jobs[i].da;
+      o.db = jobs[i].db;
+      o.rev = jobs[i].rev;
+      o.c_state = jobs[i].c_state;
       o.local = a.ws + i * states;
-      p.init[i] = j.init;
-      p.rev[i] = j.rev;
-      p.init_decays[i] = j.init_decays;
     }
-    const cudaError_t e = run<true>(t, dp, parts, units, ns, st);
+    cudaError_t e = run<true>(t, dp, parts, units, ns, st);
     if (e != cudaSuccess) return e;
-    p.log_decay = a.log_decay;
-    p.lengths = a.lengths;
-    p.heads = a.heads;
-    p.N = a.N;
-    p.segs = sp.segs;
-    p.seg_chunks = sp.seg_chunks;
-    p.dd = dd;
-    k_decay_prefix<<<dim3(units, ceil_div(dd, 256), ns), 64, 0, st>>>(p);
-    const cudaError_t e2 = cudaGetLastError();
-    if (e2 != cudaSuccess) return e2;
+    e = launch_prefix(a, sp, p, ns, st);
+    if (e != cudaSuccess) return e;
   }
   for (int i = 0; i < a.njobs; ++i) {
     const DecayJob& j = a.job[i];

@@ -92,6 +92,13 @@ struct NormArgs {
 };
 
 cudaError_t launch_decay(const DecayArgs& a, int dtype, cudaStream_t st);
+// The end states of a call's segments, carried over the segments (in place in a.ws): initial state and direction.
+struct PrefixRun {
+  const float* init;
+  int rev, init_decays;
+};
+int state_runs(const DecayArgs& a, DecayJob* jobs, PrefixRun* p);
+cudaError_t launch_prefix(const DecayArgs& a, const DecaySplit& sp, const PrefixRun* p, int n, cudaStream_t st);
 cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st);
 cudaError_t decay_take_status(int* out, cudaStream_t st);
 cudaError_t launch_decay_step(const DecayStepArgs& a, int dtype, cudaStream_t st);

@@ -171,6 +171,7 @@ void run_rotary(const RotaryArgs& a, cudaStream_t st) {
 // reading comes from the 126 MB L2 as far as the tensor fits there. All sums are joined in a fixed order.
 constexpr int kNT = 256;         // threads per block
 constexpr int kNRows = 8;        // rows a thread has in flight
+constexpr int kNormWave = 4 * 148;   // blocks that run at once
 constexpr int kMaxChunks = 64;   // row chunks per sample (large groups)
 
 using sm100::add2;
@@ -388,10 +389,10 @@ __global__ void __launch_bounds__(kNT) k_norm_small(const __grid_constant__ Smal
 }
 
 // The same for groups of one vector per thread (T a power of two): a thread keeps its channels over all the samples it
-// takes (every teams-th (sample, group); teams is a multiple of G), U of them in flight.
+// takes (every teams-th (sample, group); teams is a multiple of G), U at once and the next U on their way.
 template <typename T, int VB, int ACT, bool BACKWARD>
-__global__ void __launch_bounds__(kNT) k_norm_rows(const __grid_constant__ SmallArgs s, int teams) {
-  constexpr int V = VB / sizeof(T), U = BACKWARD ? 2 : 4;
+__global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __grid_constant__ SmallArgs s, int teams) {
+  constexpr int V = VB / sizeof(T), U = 2;
   const NormArgs& a = s.a;
   const int tl = threadIdx.x & (s.T - 1), team = blockIdx.x * (kNT / s.T) + threadIdx.x / s.T;
   const long long total = (long long)a.B * a.G;
@@ -411,25 +412,38 @@ __global__ void __launch_bounds__(kNT) k_norm_rows(const __grid_constant__ Small
   const T* dy = static_cast<const T*>(a.dy);
   T* y = static_cast<T*>(a.y);
   // the block's threads stay together (they shuffle), whatever teams still have a sample
+  Raw<VB> nv[U], nw[U];
+  float nm[U], nr[U];
+  auto load = [&](long long id, long long from) {   // U samples; zeros where there is none
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long iu = id + (long long)u * teams;
+      const bool on = iu < total;
+#pragma unroll
+      for (int i = 0; i < (VB + 3) / 4; ++i) nv[u].w[i] = nw[u].w[i] = 0u;
+      if (on && has) {
+        nv[u] = raw_load<VB>(x + from + u * step);
+        if (BACKWARD) nw[u] = raw_load<VB>(dy + from + u * step);
+      }
+      if (BACKWARD) {
+        nm[u] = on ? a.mean[iu] : 0.f;
+        nr[u] = on ? a.rstd[iu] : 0.f;
+      }
+    }
+  };
+  load(team, at);
   for (long long id0 = (long long)blockIdx.x * (kNT / s.T); id0 < total; id0 += (long long)U * teams, at += U * step) {
     const long long id = id0 + threadIdx.x / s.T;
     Raw<VB> v[U], w[U];
     float m[U], rs[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long iu = id + (long long)u * teams;
-      const bool on = iu < total;
-#pragma unroll
-      for (int i = 0; i < (VB + 3) / 4; ++i) v[u].w[i] = w[u].w[i] = 0u;
-      if (on && has) {
-        v[u] = raw_load<VB>(x + at + u * step);
-        if (BACKWARD) w[u] = raw_load<VB>(dy + at + u * step);
-      }
-      if (BACKWARD) {
-        m[u] = on ? a.mean[iu] : 0.f;
-        rs[u] = on ? a.rstd[iu] : 0.f;
-      }
+      v[u] = nv[u];
+      w[u] = nw[u];
+      m[u] = nm[u];
+      rs[u] = nr[u];
     }
+    load(id + (long long)U * teams, at + U * step);   // the next ones, meanwhile
     if constexpr (!BACKWARD) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -733,7 +747,7 @@ __device__ __forceinline__ void chan_stats(const NormArgs& a, int b, int c, int 
 }
 
 template <typename T, int VB, int ACT, bool ONE>
-__global__ void __launch_bounds__(kNT) k_norm_apply(const __grid_constant__ RowArgs p) {
+__global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_norm_apply(const __grid_constant__ RowArgs p) {
   constexpr int V = VB / sizeof(T), NP = (V + 1) / 2;
   const NormArgs& a = p.a;
   const Lane l = lane_of<V>(p, a.N);
@@ -764,9 +778,9 @@ __global__ void __launch_bounds__(kNT) k_norm_apply(const __grid_constant__ RowA
 
 // per-channel sums of dz and dz xhat over a chunk's rows: of one sample, or (FLAT) of all samples' rows in turn
 template <typename T, int VB, int ACT, bool ONE, bool FLAT>
-__global__ void __launch_bounds__(kNT) k_norm_bsum(const __grid_constant__ RowArgs p) {
+__global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_norm_bsum(const __grid_constant__ RowArgs p) {
   constexpr int V = VB / sizeof(T);
-  constexpr int R = 4;   // rows in flight, of two tensors
+  constexpr int R = 2;   // rows in flight, of two tensors; four blocks an SM cover the rest
   extern __shared__ float sm[];
   const NormArgs& a = p.a;
   const int dg = a.C / a.G;
@@ -881,9 +895,9 @@ __global__ void __launch_bounds__(kNT) k_norm_bjoin(const __grid_constant__ RowA
 }
 
 template <typename T, int VB, int ACT, bool ONE>
-__global__ void __launch_bounds__(kNT) k_norm_dx(const __grid_constant__ RowArgs p, const float* m12) {
+__global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_norm_dx(const __grid_constant__ RowArgs p, const float* m12) {
   constexpr int V = VB / sizeof(T), NP = (V + 1) / 2;
-  constexpr int R = 4;
+  constexpr int R = 2;
   const NormArgs& a = p.a;
   const int dg = a.C / a.G;
   const Lane l = lane_of<V>(p, a.N);
@@ -973,7 +987,7 @@ Plan plan_norm(int B, int N, int C, int G, int es, bool backward) {
   r.colblocks = ceil_div(cv, r.cw);
   const long long rows = p.small ? (long long)B * N : N;
   const int samples = p.small ? 1 : B;
-  long long want = kWave / ((long long)samples * r.colblocks < kWave ? samples * r.colblocks : kWave);   // one wave
+  long long want = kNormWave / ((long long)samples * r.colblocks < kNormWave ? samples * r.colblocks : kNormWave);   // one wave
   const long long most = (rows + r.rl * kNRows - 1) / (r.rl * kNRows);
   if (want > most) want = most;
   if (want < 1) want = 1;
@@ -996,7 +1010,8 @@ void rows_launch(const Plan& p, cudaStream_t st) {
   for (int d = per; d > 1; d /= 2)
     if (unit % 2 == 0) unit /= 2;
   const long long teams = (long long)p.s.a.B * G, need = (teams + per - 1) / per;
-  long long blocks = need < kWave ? need : kWave;
+  const int wave = BACKWARD ? 2 * 148 : kNormWave;
+  long long blocks = need < wave ? need : wave;
   blocks = (blocks + unit - 1) / unit * unit;
   k_norm_rows<T, VB, ACT, BACKWARD><<<(unsigned)blocks, kNT, 0, st>>>(p.s, (int)(blocks * per));
 }
