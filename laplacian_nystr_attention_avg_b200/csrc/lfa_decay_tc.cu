@@ -12,7 +12,7 @@
 // starts from zero in every chunk and is added to R by CUDA cores: tensor-core accumulation truncates and would
 // drift over thousands of chunks. All widths are padded to DP = 64 or 128 by TMA's zero fill.
 //
-// Warps: 4 for P, 4 for y's decayed rows, 8 for R and the epilogue, one thread each to issue TMA loads, the products
+// Warps: 4 or 8 for P, 4 or 8 for y's decayed rows, 8 for R and the epilogue, one thread each to issue TMA loads, the products
 // of the state and those of the output. Every hand-over is an mbarrier; every wait is bounded (on expiry the device's status
 // word is set, the CTA stops waiting for anything and drains what it has in flight).
 //
@@ -69,7 +69,8 @@ struct Cfg {
   static constexpr int kStep = 4096 / DP;
   static constexpr int kBufs = DP == 128 && PARTS == 3 && !STATE ? 1 : 2;
   static constexpr int kSteps = kC / kStep;
-  static constexpr int kVec = kStep * DP / 8 / 128;
+  static constexpr int kYW = STATE && DP == 64 ? 8 : 4;   // warps that form them
+  static constexpr int kVec = kStep * DP / 8 / (32 * kYW);
   static constexpr int kPart = kStep * DP * 2;
   static constexpr int kOffR = kOffPart + kBufs * PARTS * kPart;
   static constexpr int kOffBar = kOffR + (STATE ? 0 : DP * DP * 2);
@@ -79,15 +80,18 @@ struct Cfg {
   static constexpr int kWt = PARTS == 3 ? 16 : 8;
   static constexpr int kSmem = kOffWt + kWt * (kC + 1);
   static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
-  // warps: 4 for P (not STATE), 4 for y's decayed rows, 8 for the state and the epilogue, loads, products (two)
-  static constexpr int kY0 = STATE ? 0 : 4;
-  static constexpr int kR0 = kY0 + 4;
+  // warps: P (not STATE), y's decayed rows, 8 for the state and the epilogue, loads, products (two)
+  static constexpr int kPW = STATE ? 0 : DP == 64 ? 8 : 4;
+  static constexpr int kY0 = kPW;
+  static constexpr int kR0 = kY0 + kYW;
   static constexpr int kLoad = kR0 + 8;
   static constexpr int kMma = kLoad + 1;      // products of the state
   static constexpr int kMmaO = kMma + 1;      // products of the output (not STATE)
   static constexpr int kThreads = 32 * (STATE ? kMma + 1 : kMmaO + 1);
-  // 608 threads have 96 registers each; with up to 64 of them R, the state warps take 16 more from the y warps (32
-  // each): 128 64 + 256 112 + 224 96 = 608 96
+  // DP 64: 736 threads have 80 registers each; the state warps take 16 more from the P warps (8 each) and the y warps
+  // (16 each): 256 72 + 128 64 + 256 96 + 96 80 = 736 80. DP 128: 608 threads with 96; the state warps, R being 64 of
+  // theirs, take 16 more from the y warps (32 each): 128 96 + 128 64 + 256 112 + 96 96 = 608 96
+  static constexpr int kRegsP = DP == 64 ? 72 : 96, kRegsY = 64, kRegsR = DP == 64 ? 96 : 112;
   static constexpr bool kSplitRegs = !STATE;
   // tensor memory columns. DP 64: S, P (bf16 pairs), two sets of Oz and Ox, D. DP 128: no room for all of that; P
   // goes over the first half of S's columns, row by row as S is read, and there is one set of Oz and Ox
@@ -183,30 +187,31 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
 __device__ __forceinline__ uint32_t packf2(uint64_t v) { return pack2(f2_lo(v), f2_hi(v)); }
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 
-// The P warps of a run of n chunks: P = c_intra l^|i-j| S on the causal side, in bf16 (thread = token row i).
-// pi holds c_intra l^n after 32 zeros; beside the diagonal block l^|i-j| is l^(distance of i to the block) pb[c].
-// nv0: valid tokens of the first chunk, where a reverse run finds its sequence's ragged end (forwards, columns
-// behind the end are above the diagonal).
+// The P warps of a run of n chunks: P = c_intra l^|i-j| S on the causal side, in bf16 (thread = token row i; with
+// two warps for a quarter of the rows, they take its blocks of 32 columns in turn). pi holds c_intra l^n after 32 zeros; beside
+// the diagonal block l^|i-j| is l^(distance of i to the block) pb[c]. nv0: valid tokens of the first chunk, where a
+// reverse run finds its sequence's ragged end (forwards, columns behind the end are above the diagonal).
 template <class C, bool REV>
 __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bars, uint32_t tmem, const float* pi,
                                         const float* pb, int nv0) {
-  const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, i = 32 * q + lane;
+  const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, i = 32 * q + lane, first = threadIdx.x >> 7;
   const uint32_t quad = tmem + ((uint32_t)(32 * q) << 16), srow = quad + C::kTs, prow = quad + C::kTp;
   const float* pd = pi + (REV ? -lane : lane);
   // the other side of the diagonal is zero: once where P has its own columns, else in every chunk
   auto zeros = [&]() {
     uint32_t w[16] = {};
-    for (int cb = REV ? 0 : q + 1; cb < (REV ? q : 4); ++cb) tmem_st16(prow + 16 * cb, w);
+    for (int cb = first; cb < 4; cb += C::kPW / 4)
+      if (REV ? cb < q : cb > q) tmem_st16(prow + 16 * cb, w);
   };
   if (C::kOwnP) zeros();
-  const int b0 = REV ? q : 0, b1 = REV ? 4 : q + 1;   // blocks of 32 columns
   for (int k = 0; k < n; ++k) {
     const bool ragged = REV && k == 0 && nv0 < kC;
     wait(kSFull, k);
     if (C::kOwnP && k > 0) wait(kOFull + (k - 1) % C::kNO, (k - 1) / C::kNO);   // P's columns are free
     tc_fence_after();
 #pragma unroll 1
-    for (int cb = b0; cb < b1; ++cb) {
+    for (int cb = first; cb < 4; cb += C::kPW / 4) {
+      if (REV ? cb < q : cb > q) continue;
       uint32_t v[32];
       tmem_ld32_async(srow + 32 * cb, v);
       if (cb == q) {
@@ -230,11 +235,6 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
           v[c + 3] = (uint32_t)(y >> 32);
         }
       }
-      if (C::kOwnP && cb + 1 == b1) {   // S has been read
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + kSRead);
-      }
       if (ragged && nv0 < 32 * cb + 32) {   // columns of tokens behind the end may hold anything
 #pragma unroll
         for (int c = 0; c < 32; ++c)
@@ -245,7 +245,13 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
       for (int c = 0; c < 16; ++c) w[c] = pack2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
       tmem_st16(prow + 16 * cb, w);   // on S's columns where it has none of its own: on those read before
     }
-    if (!C::kOwnP) zeros();
+    if (C::kOwnP) {   // S has been read
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kSRead);
+    } else {
+      zeros();
+    }
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
@@ -287,9 +293,10 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
   const Waiter wait{bars, gave_up};
   if (t == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bars + i, i >= kEmptyY && i < kEmptyX                                             ? (STATE ? 4 : 5)
-                          : i >= kEmptyZ && i < kSFull                                            ? (STATE ? 1 : 2)
-                          : i == kSRead || i == kPReady || (i >= kYdReady && i < kPartFree) || i == kZClean ? 4
+      mbar_init(bars + i, i >= kEmptyY && i < kEmptyX                                    ? C::kYW + (STATE ? 0 : 1)
+                          : i >= kEmptyZ && i < kSFull                                   ? (STATE ? 1 : 2)
+                          : (i >= kYdReady && i < kPartFree) || i == kZClean             ? C::kYW
+                          : i == kSRead || i == kPReady                                    ? C::kPW
                           : i == kDRead || i == kRbReady || (i >= kOFree && i < kZClean)          ? 8
                                                                                                   : 1);
     mbar_init_fence();
@@ -429,15 +436,16 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
       wait.drain(kFin + 1, 0);
     }
   } else if (!STATE && warp < C::kY0) {
+    if constexpr (C::kSplitRegs && C::kRegsP == 72) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (rev)
       weights<C, true>(n, wait, bars, tmem, pi, pb, L - (c_hi - 1) * kC);
     else
       weights<C, false>(n, wait, bars, tmem, pi, pb, kC);
   } else if (warp < C::kR0) {
     // y's decayed rows, in steps of kStep tokens into one of two buffers
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsY));
     const int ty = t - 32 * C::kY0;
-    constexpr int CH = DP / 8, RS = 128 / CH;   // 16-byte vectors of a row, rows per pass (a multiple of 8)
+    constexpr int CH = DP / 8, RS = 32 * C::kYW / CH;   // 16-byte vectors of a row, rows per pass (a multiple of 8)
     const int ch = ty % CH, rr = ty / CH;
     const uint32_t at = (ch >> 3) * kPanelB + sw128(rr, ch & 7);   // rows RS apart have the same place in the swizzle
     unsigned char* d0 = sm + C::kOffPart + (ch >> 3) * (C::kStep * 128) + sw128(rr, ch & 7);
@@ -493,10 +501,10 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
       }
     }
   } else if (warp < C::kLoad) {
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsR));
     // state and epilogue: R row and half of its columns per thread (DP 64: M = 64 puts row 16 q + lane in
     // lane < 16); in the epilogue thread = token row, the same half of O's columns
-    constexpr int NR = DP / 2, NT = DP == 64 ? 32 : 16;   // columns of R, columns read at once
+    constexpr int NR = DP / 2, NT = 16;   // columns of R, columns read at once
     const int q = warp & 3, half = (warp - C::kR0) >> 2, i = 32 * q + lane;
     const bool live = DP == 128 || lane < 16, trans = jb.trans;
     const int row = DP == 128 ? i : 16 * q + lane, col = half * NR;
