@@ -72,8 +72,13 @@ struct Cfg {
   static constexpr int kYW = STATE && DP == 64 ? 8 : 4;   // warps that form them
   static constexpr int kVec = kStep * DP / 8 / (32 * kYW);
   static constexpr int kPart = kStep * DP * 2;
-  static constexpr int kOffR = kOffPart + kBufs * PARTS * kPart;
-  static constexpr int kOffBar = kOffR + (STATE ? 0 : DP * DP * 2);
+  // DP 64: the first two parts share the product's 128 rows (M = 64 runs at half the speed): rows 64 .. 127 of D,
+  // and of R with it, are the second part's; a third part has zeros for company. Their sum is formed in x R's
+  // product (two tiles of R) and where a state is written.
+  static constexpr bool kStack = DP == 64;
+  static constexpr int kOffZero = kOffPart + kBufs * PARTS * kPart;
+  static constexpr int kOffR = kOffZero + (kStack && PARTS == 3 ? kPart : 0);
+  static constexpr int kOffBar = kOffR + (STATE ? 0 : DP * DP * 2 * (kStack ? 2 : 1));
   static constexpr int kOffPb = kOffBar + 384;
   static constexpr int kOffPi = kOffPb + 4 * 32;
   static constexpr int kOffWt = kOffPi + 4 * (32 + kC);
@@ -91,7 +96,7 @@ struct Cfg {
   // DP 64: 736 threads have 80 registers each; the state warps take 16 more from the P warps (8 each) and the y warps
   // (16 each): 256 72 + 128 64 + 256 96 + 96 80 = 736 80. DP 128: 608 threads with 96; the state warps, R being 64 of
   // theirs, take 16 more from the y warps (32 each): 128 96 + 128 64 + 256 112 + 96 96 = 608 96
-  static constexpr int kRegsP = DP == 64 ? 72 : 96, kRegsY = 64, kRegsR = DP == 64 ? 96 : 112;
+  static constexpr int kRegsP = DP == 64 ? 72 : 96, kRegsR = DP == 64 ? 96 : 112;
   static constexpr bool kSplitRegs = !STATE;
   // tensor memory columns. DP 64: S, P (bf16 pairs), two sets of Oz and Ox, D. DP 128: no room for all of that; P
   // goes over the first half of S's columns, row by row as S is read, and there is one set of Oz and Ox
@@ -314,6 +319,11 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
     *reinterpret_cast<uint2*>(wt + i * C::kWt) = make_uint2(pack2(f, f), pack2(f1, f1));
     if (PARTS == 3) *reinterpret_cast<uint32_t*>(wt + i * C::kWt + 8) = pack2(f2, f2);
   }
+  if (C::kStack && PARTS == 3) {
+    for (int i = t; i < C::kPart / 16; i += C::kThreads)
+      *reinterpret_cast<uint4*>(sm + C::kOffZero + 16 * i) = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -382,8 +392,10 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
           if (k >= C::kNO) wait(kOFree + k % C::kNO, k / C::kNO - 1);
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            mma_bf16(ox, x + ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16, d_rb + kk * 128, id_o, kk > 0);
+          for (int kk = 0; kk < (C::kStack ? 2 : 1) * DP / 16; ++kk) {   // stacked: x again, times the second tile of R
+            const int kx = kk % (DP / 16);
+            mma_bf16(ox, x + ((kx >> 2) * kPanelB + (kx & 3) * 32) / 16, d_rb + kk * 128, id_o, kk > 0);
+          }
           mma_commit(bars + kXDone);
           mma_commit(bars + kEmptyX + sx);
           if (C::kOwnP && k + 1 < n) scores(k + 1);
@@ -406,8 +418,8 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
       // D of every chunk: its own thread, so that the state runs ahead of the outputs
       const uint32_t base = smem_u32(sm);
       const uint64_t d_z = desc_sw128(base + C::kOffZ, kPanelB, 1024),
-                     d_part = desc_sw128(base + C::kOffPart, C::kStep * 128, 1024);
-      constexpr uint32_t id_d = idesc(1, DP, DP, 1, 1);
+                     d_part = desc_sw128(base + C::kOffPart, C::kStack ? C::kPart : C::kStep * 128, 1024);
+      constexpr uint32_t id_d = idesc(1, 128, DP, 1, 1);
       for (int k = 0; k < n; ++k) {
         const int sz = k % C::kNZ;
         const uint64_t z = d_z + sz * (C::kTile / 16);
@@ -421,11 +433,15 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
           tc_fence_after();
           if (carry) {
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p)
+            for (int p = 0; p < PARTS; p += C::kStack ? 2 : 1) {
+              uint64_t part = d_part + (PARTS * buf + p) * (C::kPart / 16);
+              if (C::kStack && p == 2)   // with the zeros behind the last buffer
+                part = desc_sw128(base + C::kOffPart + (PARTS * buf + p) * C::kPart,
+                                  C::kOffZero - C::kOffPart - (PARTS * buf + p) * C::kPart, 1024);
 #pragma unroll
               for (int kk = 0; kk < C::kStep / 16; ++kk)
-                mma_bf16(tmem + C::kTd, d_part + (PARTS * buf + p) * (C::kPart / 16) + kk * 128,
-                         z + (s * C::kStep + 16 * kk) * 8, id_d, s + p + kk > 0);
+                mma_bf16(tmem + C::kTd, part + kk * 128, z + (s * C::kStep + 16 * kk) * 8, id_d, s + p + kk > 0);
+            }
           }
           mma_commit(bars + kPartFree + buf);
         }
@@ -443,7 +459,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
       weights<C, false>(n, wait, bars, tmem, pi, pb, kC);
   } else if (warp < C::kR0) {
     // y's decayed rows, in steps of kStep tokens into one of two buffers
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsY));
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(64));
     const int ty = t - 32 * C::kY0;
     constexpr int CH = DP / 8, RS = 32 * C::kYW / CH;   // 16-byte vectors of a row, rows per pass (a multiple of 8)
     const int ch = ty % CH, rr = ty / CH;
@@ -502,12 +518,12 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
     }
   } else if (warp < C::kLoad) {
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsR));
-    // state and epilogue: R row and half of its columns per thread (DP 64: M = 64 puts row 16 q + lane in
-    // lane < 16); in the epilogue thread = token row, the same half of O's columns
+    // state and epilogue: a row of R and half of its columns per thread (stacked: rows 64 .. 127 are the second
+    // part's share of rows 0 .. 63); in the epilogue thread = token row, the same half of O's columns
     constexpr int NR = DP / 2, NT = 16;   // columns of R, columns read at once
     const int q = warp & 3, half = (warp - C::kR0) >> 2, i = 32 * q + lane;
-    const bool live = DP == 128 || lane < 16, trans = jb.trans;
-    const int row = DP == 128 ? i : 16 * q + lane, col = half * NR;
+    const bool trans = jb.trans, second = C::kStack && i >= DP;
+    const int row = i % DP, col = half * NR;
     const uint32_t quad = tmem + ((uint32_t)(32 * q) << 16) + col;
     uint64_t R[NR / 2];   // pairs of columns
     {
@@ -517,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
 #pragma unroll
       for (int c = 0; c < NR; c += 4) {   // da and db are multiples of 8
         float4 r = make_float4(0, 0, 0, 0);
-        if (src && live && row < da && col + c < db) {
+        if (src && !second && row < da && col + c < db) {
           const float* p = src + at + (trans ? (size_t)(col + c) * da + row : (size_t)row * db + col + c);
           r = trans ? make_float4(p[0], p[da], p[2 * da], p[3 * da]) : *reinterpret_cast<const float4*>(p);
         }
@@ -594,13 +610,11 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
       if (k > 0) update(k - 1);
       if (!STATE) {
         if (k > 0) wait(kXDone, k - 1);
-        if (live) {
 #pragma unroll
-          for (int g = 0; g < NR; g += 8) {
-            const int cc = col + g;
-            *reinterpret_cast<uint4*>(sm + C::kOffR + (cc >> 6) * (DP * 128) + sw128(row, (cc & 63) >> 3)) =
-                make_uint4(packf2(R[g / 2]), packf2(R[g / 2 + 1]), packf2(R[g / 2 + 2]), packf2(R[g / 2 + 3]));
-          }
+        for (int g = 0; g < NR; g += 8) {
+          const int cc = col + g;
+          *reinterpret_cast<uint4*>(sm + C::kOffR + (second ? DP : cc >> 6 << 7) * 128 + sw128(row, (cc & 63) >> 3)) =
+              make_uint4(packf2(R[g / 2]), packf2(R[g / 2 + 1]), packf2(R[g / 2 + 2]), packf2(R[g / 2 + 3]));
         }
         fence_async_smem();
         __syncwarp();
@@ -612,7 +626,22 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
     if (STATE || ends) {
       update(n - 1);
       float* dst = STATE ? jb.local + ((size_t)u * a.segs + seg) * dd : jb.fin + u * dd;
-      if (live && row < da) {
+      if constexpr (C::kStack) {   // the second part's share, through the parts' memory: their last product is done
+        float4* share = reinterpret_cast<float4*>(sm + C::kOffPart) + half * (DP * NR / 4) + row;
+        if (second)
+#pragma unroll
+          for (int c = 0; c < NR; c += 4)
+            share[c / 4 * DP] = make_float4(f2_lo(R[c / 2]), f2_hi(R[c / 2]), f2_lo(R[c / 2 + 1]), f2_hi(R[c / 2 + 1]));
+        named_bar_sync(1, 256);
+        if (!second)
+#pragma unroll
+          for (int c = 0; c < NR; c += 4) {
+            const float4 v = share[c / 4 * DP];
+            R[c / 2] = add2(R[c / 2], f2(v.x, v.y));
+            R[c / 2 + 1] = add2(R[c / 2 + 1], f2(v.z, v.w));
+          }
+      }
+      if (!second && row < da) {
 #pragma unroll
         for (int c = 0; c < NR; c += 4)
           if (col + c < db)   // a returned state is never a transposed one
