@@ -114,6 +114,34 @@ enum Bar {
 };
 static_assert(kNumBars * 8 <= 368, "barriers overlap the TMEM slot");
 
+// The products are issued by one lane of a warp whose lanes stay together, so that descriptors and loop counters are
+// uniform over the warp (in a branch of one lane each product spent about 80 cycles on moving them there).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}\n" : "=r"(p));
+  return p;
+}
+__device__ __forceinline__ void mma_by(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead));
+}
+// A in tensor memory: lane = row, 16-bit K elements 2c, 2c + 1 in column c
+__device__ __forceinline__ void mma_ta_by(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc), "r"(lead));
+}
+__device__ __forceinline__ void commit_by(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+
 struct Waiter {
   uint64_t* bars;
   volatile int* gave_up;
@@ -362,95 +390,95 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
     }
   } else if (!STATE && warp == C::kMmaO) {
     if constexpr (!STATE) {
-      if (lane == 0) {
-        // S, Ox, Oz of every chunk in turn. Descriptors of a ring's first tile; b bytes further is + b / 16
-        const uint32_t base = smem_u32(sm);
-        const uint64_t d_y = desc_sw128(base, 16, 1024), d_x = desc_sw128(base + C::kOffX, 16, 1024),
-                       d_z = desc_sw128(base + C::kOffZ, kPanelB, 1024), d_rb = desc_sw128(base + C::kOffR, DP * 128, 1024);
-        constexpr uint32_t id_s = idesc(1, kC, kC, 0, 0), id_o = idesc(1, kC, DP, 0, 1);
-        auto scores = [&](int k) {
-          const int sy = k % C::kNY, sx = k % C::kNX;
-          const uint64_t y = d_y + sy * (C::kTile / 16), x = d_x + sx * (C::kTile / 16);
-          wait(kFullY + sy, k / C::kNY);
-          wait(kFullX + sx, k / C::kNX);
-          if (k > 0) wait(C::kOwnP ? kSRead : kOFull, k - 1);   // S has been read; without its own columns, P used (kNO 1)
-          tc_fence_after();
+      const uint32_t lead = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const int steps = __shfl_sync(0xffffffffu, n, 0);
+      // S, Ox, Oz of every chunk in turn. Descriptors of a ring's first tile; b bytes further is + b / 16
+      const uint32_t base = smem_u32(sm);
+      const uint64_t d_y = desc_sw128(base, 16, 1024), d_x = desc_sw128(base + C::kOffX, 16, 1024),
+                     d_z = desc_sw128(base + C::kOffZ, kPanelB, 1024), d_rb = desc_sw128(base + C::kOffR, DP * 128, 1024);
+      constexpr uint32_t id_s = idesc(1, kC, kC, 0, 0), id_o = idesc(1, kC, DP, 0, 1);
+      auto scores = [&](int k) {
+        const int sy = k % C::kNY, sx = k % C::kNX;
+        const uint64_t y = d_y + sy * (C::kTile / 16), x = d_x + sx * (C::kTile / 16);
+        wait(kFullY + sy, k / C::kNY);
+        wait(kFullX + sx, k / C::kNX);
+        if (k > 0) wait(C::kOwnP ? kSRead : kOFull, k - 1);   // S has been read; without its own columns, P used (kNO 1)
+        tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk) {
-            const int off = ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16;
-            mma_bf16(tmem + C::kTs, x + off, y + off, id_s, kk > 0);
-          }
-          mma_commit(bars + kSFull);
-          mma_commit(bars + kEmptyY + sy);
-        };
-        scores(0);
-        for (int k = 0; k < n; ++k) {
-          const int sx = k % C::kNX, sz = k % C::kNZ;
-          const uint64_t x = d_x + sx * (C::kTile / 16), z = d_z + sz * (C::kTile / 16);
-          const uint32_t oz = tmem + C::kToz + (k % C::kNO) * 2 * DP, ox = oz + DP;
-          wait(kRbReady, k);
-          if (k >= C::kNO) wait(kOFree + k % C::kNO, k / C::kNO - 1);
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < (C::kStack ? 2 : 1) * DP / 16; ++kk) {   // stacked: x again, times the second tile of R
-            const int kx = kk % (DP / 16);
-            mma_bf16(ox, x + ((kx >> 2) * kPanelB + (kx & 3) * 32) / 16, d_rb + kk * 128, id_o, kk > 0);
-          }
-          mma_commit(bars + kXDone);
-          mma_commit(bars + kEmptyX + sx);
-          if (C::kOwnP && k + 1 < n) scores(k + 1);
-          wait(kFullZ + sz, k / C::kNZ);
-          if (valid(chunk(k)) < kC) wait(kZClean, 0);
-          wait(kPReady, k);
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kC / 16; ++kk) mma_bf16_ta(oz, tmem + C::kTp + 8 * kk, z + kk * 128, id_o, kk > 0);
-          mma_commit(bars + kOFull + k % C::kNO);
-          mma_commit(bars + kEmptyZ + sz);
-          if (!C::kOwnP && k + 1 < n) scores(k + 1);
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          const int off = ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16;
+          mma_by(lead, tm + C::kTs, x + off, y + off, id_s, kk > 0);
         }
-        mma_commit(bars + kFin);
-        wait.drain(kFin, 0);
+        commit_by(lead, bars + kSFull);
+        commit_by(lead, bars + kEmptyY + sy);
+      };
+      scores(0);
+      for (int k = 0; k < steps; ++k) {
+        const int sx = k % C::kNX, sz = k % C::kNZ;
+        const uint64_t x = d_x + sx * (C::kTile / 16), z = d_z + sz * (C::kTile / 16);
+        const uint32_t oz = tm + C::kToz + (k % C::kNO) * 2 * DP, ox = oz + DP;
+        wait(kRbReady, k);
+        if (k >= C::kNO) wait(kOFree + k % C::kNO, k / C::kNO - 1);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < (C::kStack ? 2 : 1) * DP / 16; ++kk) {   // stacked: x again, times the second tile of R
+          const int kx = kk % (DP / 16);
+          mma_by(lead, ox, x + ((kx >> 2) * kPanelB + (kx & 3) * 32) / 16, d_rb + kk * 128, id_o, kk > 0);
+        }
+        commit_by(lead, bars + kXDone);
+        commit_by(lead, bars + kEmptyX + sx);
+        if (C::kOwnP && k + 1 < steps) scores(k + 1);
+        wait(kFullZ + sz, k / C::kNZ);
+        if (valid(chunk(k)) < kC) wait(kZClean, 0);
+        wait(kPReady, k);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kC / 16; ++kk) mma_ta_by(lead, oz, tm + C::kTp + 8 * kk, z + kk * 128, id_o, kk > 0);
+        commit_by(lead, bars + kOFull + k % C::kNO);
+        commit_by(lead, bars + kEmptyZ + sz);
+        if (!C::kOwnP && k + 1 < steps) scores(k + 1);
       }
+      commit_by(lead, bars + kFin);
+      wait.drain(kFin, 0);
     }
   } else if (warp == C::kMma) {
-    if (lane == 0) {
-      // D of every chunk: its own thread, so that the state runs ahead of the outputs
-      const uint32_t base = smem_u32(sm);
-      const uint64_t d_z = desc_sw128(base + C::kOffZ, kPanelB, 1024),
-                     d_part = desc_sw128(base + C::kOffPart, C::kStack ? C::kPart : C::kStep * 128, 1024);
-      constexpr uint32_t id_d = idesc(1, 128, DP, 1, 1);
-      for (int k = 0; k < n; ++k) {
-        const int sz = k % C::kNZ;
-        const uint64_t z = d_z + sz * (C::kTile / 16);
-        const bool carry = STATE || ends || k < n - 1;
-        wait(kFullZ + sz, k / C::kNZ);
-        if (k > 0) wait(kDRead, k - 1);
+    const uint32_t lead = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const int steps = __shfl_sync(0xffffffffu, n, 0);
+    // D of every chunk: its own thread, so that the state runs ahead of the outputs
+    const uint32_t base = smem_u32(sm);
+    const uint64_t d_z = desc_sw128(base + C::kOffZ, kPanelB, 1024),
+                   d_part = desc_sw128(base + C::kOffPart, C::kStack ? C::kPart : C::kStep * 128, 1024);
+    constexpr uint32_t id_d = idesc(1, 128, DP, 1, 1);
+    for (int k = 0; k < steps; ++k) {
+      const int sz = k % C::kNZ;
+      const uint64_t z = d_z + sz * (C::kTile / 16);
+      const bool carry = STATE || ends || k < n - 1;
+      wait(kFullZ + sz, k / C::kNZ);
+      if (k > 0) wait(kDRead, k - 1);
 #pragma unroll 1
-        for (int s = 0; s < C::kSteps; ++s) {
-          const int g = k * C::kSteps + s, buf = g % C::kBufs;
-          wait(kYdReady + buf, g / C::kBufs);
-          tc_fence_after();
-          if (carry) {
+      for (int s = 0; s < C::kSteps; ++s) {
+        const int g = k * C::kSteps + s, buf = g % C::kBufs;
+        wait(kYdReady + buf, g / C::kBufs);
+        tc_fence_after();
+        if (carry) {
 #pragma unroll
-            for (int p = 0; p < PARTS; p += C::kStack ? 2 : 1) {
-              uint64_t part = d_part + (PARTS * buf + p) * (C::kPart / 16);
-              if (C::kStack && p == 2)   // with the zeros behind the last buffer
-                part = desc_sw128(base + C::kOffPart + (PARTS * buf + p) * C::kPart,
-                                  C::kOffZero - C::kOffPart - (PARTS * buf + p) * C::kPart, 1024);
+          for (int p = 0; p < PARTS; p += C::kStack ? 2 : 1) {
+            uint64_t part = d_part + (PARTS * buf + p) * (C::kPart / 16);
+            if (C::kStack && p == 2)   // with the zeros behind the last buffer
+              part = desc_sw128(base + C::kOffPart + (PARTS * buf + p) * C::kPart,
+                                C::kOffZero - C::kOffPart - (PARTS * buf + p) * C::kPart, 1024);
 #pragma unroll
-              for (int kk = 0; kk < C::kStep / 16; ++kk)
-                mma_bf16(tmem + C::kTd, part + kk * 128, z + (s * C::kStep + 16 * kk) * 8, id_d, s + p + kk > 0);
-            }
+            for (int kk = 0; kk < C::kStep / 16; ++kk)
+              mma_by(lead, tm + C::kTd, part + kk * 128, z + (s * C::kStep + 16 * kk) * 8, id_d, s + p + kk > 0);
           }
-          mma_commit(bars + kPartFree + buf);
         }
-        if (carry) mma_commit(bars + kDFull);
-        mma_commit(bars + kEmptyZ + sz);
+        commit_by(lead, bars + kPartFree + buf);
       }
-      mma_commit(bars + kFin + 1);
-      wait.drain(kFin + 1, 0);
+      if (carry) commit_by(lead, bars + kDFull);
+      commit_by(lead, bars + kEmptyZ + sz);
     }
+    commit_by(lead, bars + kFin + 1);
+    wait.drain(kFin + 1, 0);
   } else if (!STATE && warp < C::kY0) {
     if constexpr (C::kSplitRegs && C::kRegsP == 72) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (rev)
