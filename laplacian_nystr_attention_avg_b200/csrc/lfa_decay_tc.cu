@@ -95,8 +95,8 @@ struct Cfg {
   static constexpr int kThreads = 32 * (STATE ? kMma + 1 : kMmaO + 1);
   // DP 64: 736 threads have 80 registers each; the state warps take 16 more from the P warps (8 each) and the y warps
   // (16 each): 256 72 + 128 64 + 256 96 + 96 80 = 736 80. DP 128: 608 threads with 96; the state warps, R being 64 of
-  // theirs, take 16 more from the y warps (32 each): 128 96 + 128 64 + 256 112 + 96 96 = 608 96
-  static constexpr int kRegsP = DP == 64 ? 72 : 96, kRegsR = DP == 64 ? 96 : 112;
+  // theirs, take 16 more from the P and y warps (16 each): 128 80 + 128 80 + 256 112 + 96 96 = 608 96
+  static constexpr int kRegsP = DP == 64 ? 72 : 80, kRegsY = DP == 64 ? 64 : 80, kRegsR = DP == 64 ? 96 : 112;
   static constexpr bool kSplitRegs = !STATE;
   // tensor memory columns. DP 64: S, P (bf16 pairs), two sets of Oz and Ox, D. DP 128: no room for all of that; P
   // goes over the first half of S's columns, row by row as S is read, and there is one set of Oz and Ox
@@ -240,8 +240,8 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
   for (int k = 0; k < n; ++k) {
     const bool ragged = REV && k == 0 && nv0 < kC;
     wait(kSFull, k);
-    if (C::kOwnP && k > 0) wait(kOFull + (k - 1) % C::kNO, (k - 1) / C::kNO);   // P's columns are free
     tc_fence_after();
+    bool used = !C::kOwnP || k == 0;   // P's columns are free
 #pragma unroll 1
     for (int cb = first; cb < 4; cb += C::kPW / 4) {
       if (REV ? cb < q : cb > q) continue;
@@ -276,6 +276,11 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
       uint32_t w[16];
 #pragma unroll
       for (int c = 0; c < 16; ++c) w[c] = pack2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+      if (!used) {
+        wait(kOFull + (k - 1) % C::kNO, (k - 1) / C::kNO);
+        tc_fence_after();
+        used = true;
+      }
       tmem_st16(prow + 16 * cb, w);   // on S's columns where it has none of its own: on those read before
     }
     if (C::kOwnP) {   // S has been read
@@ -427,7 +432,6 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
         }
         commit_by(lead, bars + kXDone);
         commit_by(lead, bars + kEmptyX + sx);
-        if (C::kOwnP && k + 1 < steps) scores(k + 1);
         wait(kFullZ + sz, k / C::kNZ);
         if (valid(chunk(k)) < kC) wait(kZClean, 0);
         wait(kPReady, k);
@@ -436,7 +440,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
         for (int kk = 0; kk < kC / 16; ++kk) mma_ta_by(lead, oz, tm + C::kTp + 8 * kk, z + kk * 128, id_o, kk > 0);
         commit_by(lead, bars + kOFull + k % C::kNO);
         commit_by(lead, bars + kEmptyZ + sz);
-        if (!C::kOwnP && k + 1 < steps) scores(k + 1);
+        if (k + 1 < steps) scores(k + 1);
       }
       commit_by(lead, bars + kFin);
       wait.drain(kFin, 0);
@@ -480,14 +484,14 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
     commit_by(lead, bars + kFin + 1);
     wait.drain(kFin + 1, 0);
   } else if (!STATE && warp < C::kY0) {
-    if constexpr (C::kSplitRegs && C::kRegsP == 72) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsP));
     if (rev)
       weights<C, true>(n, wait, bars, tmem, pi, pb, L - (c_hi - 1) * kC);
     else
       weights<C, false>(n, wait, bars, tmem, pi, pb, kC);
   } else if (warp < C::kR0) {
     // y's decayed rows, in steps of kStep tokens into one of two buffers
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(64));
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsY));
     const int ty = t - 32 * C::kY0;
     constexpr int CH = DP / 8, RS = 32 * C::kYW / CH;   // 16-byte vectors of a row, rows per pass (a multiple of 8)
     const int ch = ty % CH, rr = ty / CH;
@@ -523,18 +527,20 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
               *reinterpret_cast<uint4*>(z + (st * C::kStep + e * RS) * 128) = v[e];
             }
         }
+        uint4 o[C::kVec][3];
+#pragma unroll
+        for (int e = 0; e < C::kVec; ++e) {
+          split<PARTS>(v[e].x, w[e], w3[e], o[e][0].x, o[e][1].x, o[e][2].x);
+          split<PARTS>(v[e].y, w[e], w3[e], o[e][0].y, o[e][1].y, o[e][2].y);
+          split<PARTS>(v[e].z, w[e], w3[e], o[e][0].z, o[e][1].z, o[e][2].z);
+          split<PARTS>(v[e].w, w[e], w3[e], o[e][0].w, o[e][1].w, o[e][2].w);
+        }
         if (g >= C::kBufs) wait(kPartFree + buf, g / C::kBufs - 1);
         unsigned char* d = d0 + PARTS * buf * C::kPart;
 #pragma unroll
-        for (int e = 0; e < C::kVec; ++e) {
-          uint4 o[3];
-          split<PARTS>(v[e].x, w[e], w3[e], o[0].x, o[1].x, o[2].x);
-          split<PARTS>(v[e].y, w[e], w3[e], o[0].y, o[1].y, o[2].y);
-          split<PARTS>(v[e].z, w[e], w3[e], o[0].z, o[1].z, o[2].z);
-          split<PARTS>(v[e].w, w[e], w3[e], o[0].w, o[1].w, o[2].w);
+        for (int e = 0; e < C::kVec; ++e)
 #pragma unroll
-          for (int p = 0; p < PARTS; ++p) *reinterpret_cast<uint4*>(d + e * RS * 128 + p * C::kPart) = o[p];
-        }
+          for (int p = 0; p < PARTS; ++p) *reinterpret_cast<uint4*>(d + e * RS * 128 + p * C::kPart) = o[e][p];
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + kYdReady + buf);
