@@ -527,6 +527,8 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
               *reinterpret_cast<uint4*>(z + (st * C::kStep + e * RS) * 128) = v[e];
             }
         }
+        // (three parts take long enough to be formed before their one buffer is free)
+        if (PARTS == 2 && g >= C::kBufs) wait(kPartFree + buf, g / C::kBufs - 1);
         uint4 o[C::kVec][3];
 #pragma unroll
         for (int e = 0; e < C::kVec; ++e) {
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
           split<PARTS>(v[e].z, w[e], w3[e], o[e][0].z, o[e][1].z, o[e][2].z);
           split<PARTS>(v[e].w, w[e], w3[e], o[e][0].w, o[e][1].w, o[e][2].w);
         }
-        if (g >= C::kBufs) wait(kPartFree + buf, g / C::kBufs - 1);
+        if (PARTS == 3 && g >= C::kBufs) wait(kPartFree + buf, g / C::kBufs - 1);
         unsigned char* d = d0 + PARTS * buf * C::kPart;
 #pragma unroll
         for (int e = 0; e < C::kVec; ++e)
