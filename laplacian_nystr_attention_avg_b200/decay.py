@@ -116,6 +116,10 @@ def _switched(device: int, stream):
                 yield
 
 
+# the plain query: CUDA is up wherever there is a CUDA tensor
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _in(device: int, stream):
     """Context in which a run of calls and allocations goes to `stream` of the device."""
     if stream is None and device == torch.cuda.current_device():
@@ -125,8 +129,7 @@ def _in(device: int, stream):
 
 def _elsewhere(t, stream) -> bool:
     """Whether a call on tensor t has to leave the current device or stream (see _switched)."""
-    return (isinstance(t, torch.Tensor) and t.is_cuda
-            and (stream is not None or t.get_device() != torch.cuda.current_device()))
+    return isinstance(t, torch.Tensor) and t.is_cuda and (stream is not None or t.get_device() != _current_device())
 
 
 def _cur(device: int) -> int:
@@ -139,7 +142,7 @@ _plans = {}
 
 
 def _sig(t):
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+    return None if t is None else (t.size(), t.stride(), t.dtype, t.get_device())
 
 
 def _plan(kind, extra, tensors, check):
