@@ -86,11 +86,20 @@ __global__ void __launch_bounds__(4 * CB) k_decay_core(const __grid_constant__ C
     const float* src = STATE ? nullptr : split ? ca.seg_init[jx] : jb.init;
     const size_t at = split ? ((size_t)u * ca.segs + seg) * dd : u * dd;
     const float f0 = L > 0 && !split && jb.init_decays ? expf(ld) : 1.f;
-    for (int e = t; e < DA * CB; e += NT) {
-      const int r = e / CB, c = e % CB;
-      s.R[r][c] = src && r < da && c < nb
-                      ? f0 * src[at + (jb.trans ? (size_t)(c0 + c) * da + r : (size_t)r * jb.db + c0 + c)]
-                      : 0.f;
+    float4 v[DA * TJ / NT];   // read together
+#pragma unroll
+    for (int i = 0; i < DA * TJ / NT; ++i) {
+      const int e = t + i * NT, r = e / TJ, c = e % TJ * 4;
+      v[i] = make_float4(0, 0, 0, 0);
+      if (src && r < da && c < nb) {
+        const float* p = src + at + (jb.trans ? (size_t)(c0 + c) * da + r : (size_t)r * jb.db + c0 + c);
+        v[i] = jb.trans ? make_float4(p[0], p[da], p[2 * da], p[3 * da]) : *reinterpret_cast<const float4*>(p);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < DA * TJ / NT; ++i) {
+      const int e = t + i * NT;
+      *reinterpret_cast<float4*>(&s.R[e / TJ][e % TJ * 4]) = make_float4(v[i].x * f0, v[i].y * f0, v[i].z * f0, v[i].w * f0);
     }
   }
   const int ti = t / TJ, tj = t % TJ, i0 = 4 * ti, cc = 4 * tj;
@@ -137,65 +146,67 @@ __global__ void __launch_bounds__(4 * CB) k_decay_core(const __grid_constant__ C
     __syncthreads();
     if (si + 1 < steps) fetch(si + 1);
     if constexpr (!STATE) {
-      {   // P = c_intra decay^|i-j| x_i . y_j on the causal side
-        float acc[4][NQ] = {};
-        for (int k = 0; k < da; k += 4) {
-          float4 x[4];
+      if (w0 < nv) {   // (a warp's rows may all lie behind the end)
+        {   // P = c_intra decay^|i-j| x_i . y_j on the causal side
+          float acc[4][NQ] = {};
+          for (int k = 0; k < da; k += 4) {
+            float4 x[4];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) x[p] = *reinterpret_cast<const float4*>(&s.X[i0 + p][k]);
+            for (int p = 0; p < 4; ++p) x[p] = *reinterpret_cast<const float4*>(&s.X[i0 + p][k]);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              if (rev ? TJ * q + TJ <= w0 : TJ * q >= w1) continue;   // wholly on the other side, for the warp
+              const float4 y = *reinterpret_cast<const float4*>(&s.Y[tj + TJ * q][k]);
+#pragma unroll
+              for (int p = 0; p < 4; ++p) acc[p][q] = dot4(x[p], y, acc[p][q]);
+            }
+          }
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
-            if (rev ? TJ * q + TJ <= w0 : TJ * q >= w1) continue;   // wholly on the other side, for the warp
-            const float4 y = *reinterpret_cast<const float4*>(&s.Y[tj + TJ * q][k]);
+            if (rev ? TJ * q + TJ <= w0 : TJ * q >= w1) continue;
 #pragma unroll
-            for (int p = 0; p < 4; ++p) acc[p][q] = dot4(x[p], y, acc[p][q]);
+            for (int p = 0; p < 4; ++p) {
+              const int j = tj + TJ * q, n = rev ? j - i0 - p : i0 + p - j;
+              s.P[i0 + p][j] = n >= 0 ? jb.c_intra * s.pw[n] * acc[p][q] : 0.f;
+            }
           }
         }
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if (rev ? TJ * q + TJ <= w0 : TJ * q >= w1) continue;
+        float4 acc[4] = {};
+        for (int k = 0; k < da; k += 4) {
+          float4 x[4], r[4];
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
-            const int j = tj + TJ * q, n = rev ? j - i0 - p : i0 + p - j;
-            s.P[i0 + p][j] = n >= 0 ? jb.c_intra * s.pw[n] * acc[p][q] : 0.f;
+            x[p] = *reinterpret_cast<const float4*>(&s.X[i0 + p][k]);
+            r[p] = *reinterpret_cast<const float4*>(&s.R[k + p][cc]);
           }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) fma4(acc[p], part(x[p], q), r[q]);
         }
-      }
-      float4 acc[4] = {};
-      for (int k = 0; k < da; k += 4) {
-        float4 x[4], r[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          x[p] = *reinterpret_cast<const float4*>(&s.X[i0 + p][k]);
-          r[p] = *reinterpret_cast<const float4*>(&s.R[k + p][cc]);
+          const int n = rev ? nv - 1 - i0 - p : i0 + p;
+          const float f = n >= 0 ? jb.c_inter * s.pw[n] : 0.f;
+          acc[p] = make_float4(acc[p].x * f, acc[p].y * f, acc[p].z * f, acc[p].w * f);
+        }
+        __syncwarp();   // P's rows are used by the warp that wrote them
+        for (int j = rev ? w0 : 0; j < (rev ? nv : w1); j += 4) {   // z is zero behind the end
+          float4 w[4], z[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            w[p] = *reinterpret_cast<const float4*>(&s.P[i0 + p][j]);
+            z[p] = *reinterpret_cast<const float4*>(&s.Z[j + p][cc]);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) fma4(acc[p], part(w[p], q), z[q]);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int p = 0; p < 4; ++p) fma4(acc[p], part(x[p], q), r[q]);
+        for (int p = 0; p < 4; ++p)
+          if (i0 + p < nv && cc < nb) *reinterpret_cast<float4*>(O + (t0 + i0 + p) * jb.os[2] + cc) = acc[p];
       }
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int n = rev ? nv - 1 - i0 - p : i0 + p;
-        const float f = n >= 0 ? jb.c_inter * s.pw[n] : 0.f;
-        acc[p] = make_float4(acc[p].x * f, acc[p].y * f, acc[p].z * f, acc[p].w * f);
-      }
-      __syncwarp();   // P's rows are used by the warp that wrote them
-      for (int j = rev ? w0 : 0; j < (rev ? kCC : w1); j += 4) {
-        float4 w[4], z[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          w[p] = *reinterpret_cast<const float4*>(&s.P[i0 + p][j]);
-          z[p] = *reinterpret_cast<const float4*>(&s.Z[j + p][cc]);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int p = 0; p < 4; ++p) fma4(acc[p], part(w[p], q), z[q]);
-      }
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-        if (i0 + p < nv && cc < nb) *reinterpret_cast<float4*>(O + (t0 + i0 + p) * jb.os[2] + cc) = acc[p];
       __syncthreads();   // R has been read
     }
     {   // R' = l^n R + c_state sum_j l^(n-j) y_j z_j^T (the run's last step: l^-fin_sub of that)
@@ -224,9 +235,10 @@ __global__ void __launch_bounds__(4 * CB) k_decay_core(const __grid_constant__ C
   __syncthreads();
   if (STATE || ends) {
     float* dst = STATE ? ca.local[jx] + ((size_t)u * ca.segs + seg) * dd : jb.fin + u * dd;
-    for (int e = t; e < da * CB; e += NT) {
-      const int r = e / CB, c = e % CB;
-      if (c < nb) dst[(size_t)r * jb.db + c0 + c] = s.R[r][c];   // a returned state is never a transposed one
+    for (int e = t; e < da * TJ; e += NT) {
+      const int r = e / TJ, c = e % TJ * 4;
+      if (c < nb)   // a returned state is never a transposed one
+        *reinterpret_cast<float4*>(dst + (size_t)r * jb.db + c0 + c) = *reinterpret_cast<const float4*>(&s.R[r][c]);
     }
   }
 }

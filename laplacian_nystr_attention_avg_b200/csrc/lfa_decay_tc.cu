@@ -7,10 +7,10 @@
 //   Oz = P z,  Ox = x bf16(R)               (M 128, N db; K 128 and K da)
 //   O  = Oz + c_inter l^i Ox                (epilogue warps, fp32, rounded once)
 //   D  = (y c_state l^(n-j))^T z            (M da, N db, K 128 tokens), R' = l^n R + D   (state warps)
-// The decayed rows of y enter as bf16 parts (value and remainders, one product each): two parts (2^-17) where R
-// only meets x, whose products are rounded to bf16 anyway, three (2^-25) in calls that return a state. D
-// starts from zero in every chunk and is added to R by CUDA cores: tensor-core accumulation truncates and would
-// drift over thousands of chunks. All widths are padded to DP = 64 or 128 by TMA's zero fill.
+// The decayed rows of y enter as two bf16 parts (value and remainder, one product each: about 2^-17; a third part
+// left 1.4e-6 instead of 3.9e-6 of a state's norm, the rest being the tensor cores' own sums, and cost 16 to 20 % of
+// the time). D starts from zero in every chunk and is added to R by CUDA cores: tensor-core accumulation truncates
+// and would drift over thousands of chunks. All widths are padded to DP = 64 or 128 by TMA's zero fill.
 //
 // Warps: 4 or 8 for P, 4 or 8 for y's decayed rows, 8 for R and the epilogue, one thread each to issue TMA loads, the products
 // of the state and those of the output. Every hand-over is an mbarrier; every wait is bounded (on expiry the device's status
@@ -54,7 +54,7 @@ struct TcArgs {
   int heads, N, segs, seg_chunks;
 };
 
-template <int DP, bool STATE, int PARTS>
+template <int DP, bool STATE>
 struct Cfg {
   static constexpr int kTile = DP / 64 * kPanelB;   // bytes of a token tile
   // rings of tiles. At 128 channels five fit: x is done with first (S, then Ox), y and z are held longer
@@ -64,26 +64,21 @@ struct Cfg {
   static constexpr int kOffX = kNY * kTile;
   static constexpr int kOffZ = kOffX + kNX * kTile;
   static constexpr int kOffPart = kOffZ + kNZ * kTile;
-  // y's decayed rows are formed in steps of kStep tokens, kVec 16-byte vectors per thread, in kBufs buffers of PARTS
-  // parts
+  // y's decayed rows are formed in steps of kStep tokens, kVec 16-byte vectors per thread, in two buffers of two parts
   static constexpr int kStep = 4096 / DP;
-  static constexpr int kBufs = DP == 128 && PARTS == 3 && !STATE ? 1 : 2;
   static constexpr int kSteps = kC / kStep;
   static constexpr int kYW = STATE && DP == 64 ? 8 : 4;   // warps that form them
   static constexpr int kVec = kStep * DP / 8 / (32 * kYW);
-  static constexpr int kPart = kStep * DP * 2;
-  // DP 64: the first two parts share the product's 128 rows (M = 64 runs at half the speed): rows 64 .. 127 of D,
-  // and of R with it, are the second part's; a third part has zeros for company. Their sum is formed in x R's
-  // product (two tiles of R) and where a state is written.
+  static constexpr int kPart = kStep * DP * 2;             // bytes of one part of a step
+  // DP 64: the two parts share the product's 128 rows (M = 64 runs at half the speed): rows 64 .. 127 of D, and of R
+  // with it, are the second part's. Their sum is formed in x R's product (two tiles of R) and where a state is written.
   static constexpr bool kStack = DP == 64;
-  static constexpr int kOffZero = kOffPart + kBufs * PARTS * kPart;
-  static constexpr int kOffR = kOffZero + (kStack && PARTS == 3 ? kPart : 0);
+  static constexpr int kOffR = kOffPart + 4 * kPart;
   static constexpr int kOffBar = kOffR + (STATE ? 0 : DP * DP * 2 * (kStack ? 2 : 1));
   static constexpr int kOffPb = kOffBar + 384;
   static constexpr int kOffPi = kOffPb + 4 * 32;
   static constexpr int kOffWt = kOffPi + 4 * (32 + kC);
-  static constexpr int kWt = PARTS == 3 ? 16 : 8;
-  static constexpr int kSmem = kOffWt + kWt * (kC + 1);
+  static constexpr int kSmem = kOffWt + 8 * (kC + 1);
   static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
   // warps: P (not STATE), y's decayed rows, 8 for the state and the epilogue, loads, products (two)
   static constexpr int kPW = STATE ? 0 : DP == 64 ? 8 : 4;
@@ -172,43 +167,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// y w for a pair y of bf16 and w = w.x + w.y + w3 in bf16 parts, as a + b + c in bf16: a = y w.x rounded, its
-// remainder y w.x - a is a bf16 itself (8 by 8 bits make 16), and so on down; about 2^-17 of y w
-// is left out with two parts, 2^-25 with three
+// y w for a pair y of bf16 and w = w.x + w.y in bf16 parts, as a + b in bf16: a = y w.x rounded; its remainder
+// y w.x - a is a bf16 itself (8 by 8 bits make 16). About 2^-17 of y w is left out.
 __device__ __forceinline__ __nv_bfloat162 as_b2(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); }
 __device__ __forceinline__ uint32_t as_u(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
-template <int PARTS>
-__device__ __forceinline__ void split(uint32_t y, uint2 w, uint32_t w3, uint32_t& a, uint32_t& b, uint32_t& c) {
+__device__ __forceinline__ void split(uint32_t y, uint2 w, uint32_t& a, uint32_t& b) {
   const __nv_bfloat162 y2 = as_b2(y), wx = as_b2(w.x), wy = as_b2(w.y);
-  const __nv_bfloat162 hi = __hmul2(y2, wx), rem = __hfma2(y2, wx, __hneg2(hi));
-  const __nv_bfloat162 mid = __hfma2(y2, wy, rem);
+  const __nv_bfloat162 hi = __hmul2(y2, wx);
   a = as_u(hi);
-  b = as_u(mid);
-  if (PARTS == 3) c = as_u(__hfma2(y2, as_b2(w3), __hfma2(y2, wy, __hsub2(rem, mid))));
-}
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* r) {
-  if constexpr (N == 32) {
-    tmem_ld32_async(at, r);
-    tmem_wait_ld(r);
-  } else {
-    tmem_ld16_async(at, r);
-    tmem_wait_ld16(r);
-  }
-}
-template <int N>
-__device__ __forceinline__ void tmem_ld2(uint32_t at0, uint32_t* r0, uint32_t at1, uint32_t* r1) {
-  if constexpr (N == 32) {
-    tmem_ld32_async(at0, r0);
-    tmem_ld32_async(at1, r1);
-    tmem_wait_ld(r0);
-    tmem_wait_ld(r1);
-  } else {
-    tmem_ld16_async(at0, r0);
-    tmem_ld16_async(at1, r1);
-    tmem_wait_ld16(r0);
-    tmem_wait_ld16(r1);
-  }
+  b = as_u(__hfma2(y2, wy, __hfma2(y2, wx, __hneg2(hi))));
 }
 
 // one 32-byte store (a whole sector)
@@ -297,9 +264,9 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
   }
 }
 
-template <int DP, bool STATE, int PARTS>
-__global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc(const __grid_constant__ TcArgs a) {
-  using C = Cfg<DP, STATE, PARTS>;
+template <int DP, bool STATE>
+__global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const __grid_constant__ TcArgs a) {
+  using C = Cfg<DP, STATE>;
   extern __shared__ __align__(1024) unsigned char sm[];
   const TcJob& jb = a.job[blockIdx.z];
   const int u = blockIdx.x, seg = blockIdx.y, b = u / a.heads, h = u % a.heads;
@@ -326,7 +293,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
   volatile int* gave_up = reinterpret_cast<volatile int*>(sm + C::kOffBar + 372);
   float* pb = reinterpret_cast<float*>(sm + C::kOffPb);        // rev: l^c, else l^(31-c), c = 0 .. 31
   float* pi = reinterpret_cast<float*>(sm + C::kOffPi) + 32;   // c_intra l^0 .. c_intra l^127 after 32 zeros
-  unsigned char* wt = sm + C::kOffWt;                          // c_state l^n in bf16 parts, each twice in a word
+  uint2* wt = reinterpret_cast<uint2*>(sm + C::kOffWt);        // c_state l^n in two bf16 parts, each twice in a word
   const float ld = decay_log(a.log_decay[h]);
   const Waiter wait{bars, gave_up};
   if (t == 0) {
@@ -348,14 +315,8 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
       pi[i - 32] = 0.f;
     }
     if (i < kC) pi[i] = jb.c_intra * w;
-    const float f = jb.c_state * w, f1 = f - bf_lo(pack2(f, f)), f2 = f1 - bf_lo(pack2(f1, f1));
-    *reinterpret_cast<uint2*>(wt + i * C::kWt) = make_uint2(pack2(f, f), pack2(f1, f1));
-    if (PARTS == 3) *reinterpret_cast<uint32_t*>(wt + i * C::kWt + 8) = pack2(f2, f2);
-  }
-  if (C::kStack && PARTS == 3) {
-    for (int i = t; i < C::kPart / 16; i += C::kThreads)
-      *reinterpret_cast<uint4*>(sm + C::kOffZero + 16 * i) = make_uint4(0, 0, 0, 0);
-    fence_async_smem();
+    const float f = jb.c_state * w, f1 = f - bf_lo(pack2(f, f));
+    wt[i] = make_uint2(pack2(f, f), pack2(f1, f1));
   }
   tc_fence_before();
   __syncthreads();
@@ -461,20 +422,16 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
       if (k > 0) wait(kDRead, k - 1);
 #pragma unroll 1
       for (int s = 0; s < C::kSteps; ++s) {
-        const int g = k * C::kSteps + s, buf = g % C::kBufs;
-        wait(kYdReady + buf, g / C::kBufs);
+        const int g = k * C::kSteps + s, buf = g & 1;
+        wait(kYdReady + buf, g >> 1);
         tc_fence_after();
         if (carry) {
 #pragma unroll
-          for (int p = 0; p < PARTS; p += C::kStack ? 2 : 1) {
-            uint64_t part = d_part + (PARTS * buf + p) * (C::kPart / 16);
-            if (C::kStack && p == 2)   // with the zeros behind the last buffer
-              part = desc_sw128(base + C::kOffPart + (PARTS * buf + p) * C::kPart,
-                                C::kOffZero - C::kOffPart - (PARTS * buf + p) * C::kPart, 1024);
+          for (int p = 0; p < (C::kStack ? 1 : 2); ++p)
 #pragma unroll
             for (int kk = 0; kk < C::kStep / 16; ++kk)
-              mma_by(lead, tm + C::kTd, part + kk * 128, z + (s * C::kStep + 16 * kk) * 8, id_d, s + p + kk > 0);
-          }
+              mma_by(lead, tm + C::kTd, d_part + (2 * buf + p) * (C::kPart / 16) + kk * 128,
+                     z + (s * C::kStep + 16 * kk) * 8, id_d, s + p + kk > 0);
         }
         commit_by(lead, bars + kPartFree + buf);
       }
@@ -501,23 +458,20 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
       const int c = chunk(k), nv = valid(c), sub = (!STATE && c == nch - 1) ? jb.fin_sub : 0;
       const unsigned char* y = sm + (k % C::kNY) * C::kTile + at;
       unsigned char* z = sm + C::kOffZ + (k % C::kNZ) * C::kTile + at;
-      const unsigned char* w0 = wt + ((rev ? 1 : nv) - sub) * C::kWt;   // row r: r weights on (rev) or back
-      const int ws = rev ? C::kWt : -C::kWt;
+      const uint2* w0 = wt + (rev ? 1 : nv) - sub;   // row r: r weights on (rev) or back
+      const int ws = rev ? 1 : -1;
       wait(kFullY + k % C::kNY, k / C::kNY);
       if (nv < kC) wait(kFullZ + k % C::kNZ, k / C::kNZ);
 #pragma unroll 1
       for (int st = 0; st < C::kSteps; ++st) {
-        const int g = k * C::kSteps + st, buf = g % C::kBufs;
+        const int g = k * C::kSteps + st, buf = g & 1;
         uint4 v[C::kVec];
         uint2 w[C::kVec];
-        uint32_t w3[C::kVec];
 #pragma unroll
         for (int e = 0; e < C::kVec; ++e) {
           const int r = st * C::kStep + rr + e * RS;
-          const unsigned char* wp = w0 + (r < nv ? r : 0) * ws;
           v[e] = *reinterpret_cast<const uint4*>(y + (st * C::kStep + e * RS) * 128);
-          w[e] = *reinterpret_cast<const uint2*>(wp);
-          w3[e] = PARTS == 3 ? *reinterpret_cast<const uint32_t*>(wp + 8) : 0u;
+          w[e] = w0[(r < nv ? r : 0) * ws];
         }
         if (nv < kC) {   // rows behind the sequence's end may hold anything
 #pragma unroll
@@ -527,22 +481,18 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
               *reinterpret_cast<uint4*>(z + (st * C::kStep + e * RS) * 128) = v[e];
             }
         }
-        // (three parts take long enough to be formed before their one buffer is free)
-        if (PARTS == 2 && g >= C::kBufs) wait(kPartFree + buf, g / C::kBufs - 1);
-        uint4 o[C::kVec][3];
+        if (g >= 2) wait(kPartFree + buf, (g >> 1) - 1);
+        unsigned char* d = d0 + 2 * buf * C::kPart;
 #pragma unroll
         for (int e = 0; e < C::kVec; ++e) {
-          split<PARTS>(v[e].x, w[e], w3[e], o[e][0].x, o[e][1].x, o[e][2].x);
-          split<PARTS>(v[e].y, w[e], w3[e], o[e][0].y, o[e][1].y, o[e][2].y);
-          split<PARTS>(v[e].z, w[e], w3[e], o[e][0].z, o[e][1].z, o[e][2].z);
-          split<PARTS>(v[e].w, w[e], w3[e], o[e][0].w, o[e][1].w, o[e][2].w);
+          uint4 hi, lo;
+          split(v[e].x, w[e], hi.x, lo.x);
+          split(v[e].y, w[e], hi.y, lo.y);
+          split(v[e].z, w[e], hi.z, lo.z);
+          split(v[e].w, w[e], hi.w, lo.w);
+          *reinterpret_cast<uint4*>(d + e * RS * 128) = hi;
+          *reinterpret_cast<uint4*>(d + e * RS * 128 + C::kPart) = lo;
         }
-        if (PARTS == 3 && g >= C::kBufs) wait(kPartFree + buf, g / C::kBufs - 1);
-        unsigned char* d = d0 + PARTS * buf * C::kPart;
-#pragma unroll
-        for (int e = 0; e < C::kVec; ++e)
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) *reinterpret_cast<uint4*>(d + e * RS * 128 + p * C::kPart) = o[e][p];
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + kYdReady + buf);
@@ -587,7 +537,8 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
 #pragma unroll
       for (int c0 = 0; c0 < NR; c0 += NT) {
         uint32_t d[NT];
-        tmem_ld<NT>(quad + C::kTd + c0, d);
+        tmem_ld16_async(quad + C::kTd + c0, d);
+        tmem_wait_ld16(d);
         if (c0 + NT == NR) {
           tc_fence_before();
           __syncwarp();
@@ -618,7 +569,10 @@ __global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc
 #pragma unroll
       for (int c0 = 0; c0 < NR; c0 += NT) {
         uint32_t z[NT], x[NT];
-        tmem_ld2<NT>(oz + c0, z, ox + c0, x);
+        tmem_ld16_async(oz + c0, z);
+        tmem_ld16_async(ox + c0, x);
+        tmem_wait_ld16(z);
+        tmem_wait_ld16(x);
         if (c0 + NT == NR) {
           tc_fence_before();
           __syncwarp();
@@ -748,19 +702,18 @@ bool maps(TcJob* t, const DecayArgs& a, const DecayJob& j, bool with_x) {
          make_tmap_tokens_bf16(&t->z, j.Z, j.db, a.N, a.heads, a.B, j.zs, kC);
 }
 
-template <int DP, bool STATE, int PARTS>
+template <int DP, bool STATE>
 cudaError_t run(const TcArgs& a, int units, int njobs, cudaStream_t st) {
-  using C = Cfg<DP, STATE, PARTS>;
+  using C = Cfg<DP, STATE>;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = raise_smem(k_decay_tc<DP, STATE, PARTS>, C::kSmem, done);
+  const cudaError_t e = raise_smem(k_decay_tc<DP, STATE>, C::kSmem, done);
   if (e != cudaSuccess) return e;
-  k_decay_tc<DP, STATE, PARTS><<<dim3(units, a.segs, njobs), C::kThreads, C::kSmem, st>>>(a);
+  k_decay_tc<DP, STATE><<<dim3(units, a.segs, njobs), C::kThreads, C::kSmem, st>>>(a);
   return cudaGetLastError();
 }
 template <bool STATE>
-cudaError_t run(const TcArgs& a, int dp, int parts, int units, int njobs, cudaStream_t st) {
-  if (dp == 64) return parts == 2 ? run<64, STATE, 2>(a, units, njobs, st) : run<64, STATE, 3>(a, units, njobs, st);
-  return parts == 2 ? run<128, STATE, 2>(a, units, njobs, st) : run<128, STATE, 3>(a, units, njobs, st);
+cudaError_t run(const TcArgs& a, int dp, int units, int njobs, cudaStream_t st) {
+  return dp == 64 ? run<64, STATE>(a, units, njobs, st) : run<128, STATE>(a, units, njobs, st);
 }
 
 }  // namespace
@@ -831,11 +784,10 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
   t.N = a.N;
   t.segs = sp.segs;
   t.seg_chunks = sp.seg_chunks;
-  int dp = 64, parts = 2;   // three parts of y's decayed rows where a state is returned
+  int dp = 64;
   for (int i = 0; i < a.njobs; ++i) {
     const DecayJob& j = a.job[i];
     if (j.da > 64 || j.db > 64) dp = 128;
-    if (j.fin) parts = 3;
   }
   const int dd = a.job[0].da * a.job[0].db;
   // states before the segments: run 0 forwards, and for the backward its last run (y = q, z = dO)
@@ -853,7 +805,7 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
       o.c_state = jobs[i].c_state;
       o.local = a.ws + i * states;
     }
-    cudaError_t e = run<true>(t, dp, parts, units, ns, st);
+    cudaError_t e = run<true>(t, dp, units, ns, st);
     if (e != cudaSuccess) return e;
     e = launch_prefix(a, sp, p, ns, st);
     if (e != cudaSuccess) return e;
@@ -878,7 +830,7 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
     o.c_intra = j.c_intra;
     o.c_state = j.c_state;
   }
-  return run<false>(t, dp, parts, units, a.njobs, st);
+  return run<false>(t, dp, units, a.njobs, st);
 }
 
 }  // namespace lfa
