@@ -296,7 +296,20 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   uint2* wt = reinterpret_cast<uint2*>(sm + C::kOffWt);        // c_state l^n in two bf16 parts, each twice in a word
   const float ld = decay_log(a.log_decay[h]);
   const Waiter wait{bars, gave_up};
-  if (t == 0) {
+  // chunk of step k, and its valid tokens
+  auto chunk = [&](int k) { return rev ? c_hi - 1 - k : c_lo + k; };
+  auto valid = [&](int c) { return min(kC, L - c * kC); };
+  // tile k of a tensor into its ring
+  auto load = [&](const CUtensorMap* m, int off, int ring, int full, int empty, int k) {
+    const int s = k % ring;
+    if (k >= ring) wait(empty + s, k / ring - 1);
+    if (*gave_up) return false;
+    mbar_expect_tx(bars + full + s, C::kTile);
+    for (int p = 0; p < DP / 64; ++p)
+      tma_load_4d(sm + off + s * C::kTile + p * kPanelB, m, 64 * p, chunk(k) * kC, h, b, bars + full + s);
+    return true;
+  };
+  if (t == 32 * C::kLoad) {
     for (int i = 0; i < kNumBars; ++i)
       mbar_init(bars + i, i >= kEmptyY && i < kEmptyX                                    ? C::kYW + (STATE ? 0 : 1)
                           : i >= kEmptyZ && i < kSFull                                   ? (STATE ? 1 : 2)
@@ -306,6 +319,10 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
                                                                                                   : 1);
     mbar_init_fence();
     *gave_up = 0;
+    // the first chunk is under way while the rest is set up
+    load(&jb.y, 0, C::kNY, kFullY, kEmptyY, 0);
+    load(&jb.z, C::kOffZ, C::kNZ, kFullZ, kEmptyZ, 0);
+    if (!STATE) load(&jb.x, C::kOffX, 1 > C::kNX ? 1 : C::kNX, kFullX, kEmptyX, 0);
   }
   if (warp == C::kMma) tmem_alloc(tmem_slot, C::kTmem);
   for (int i = t; i <= kC; i += C::kThreads) {
@@ -322,24 +339,11 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // chunk of step k, and its valid tokens
-  auto chunk = [&](int k) { return rev ? c_hi - 1 - k : c_lo + k; };
-  auto valid = [&](int c) { return min(kC, L - c * kC); };
-
   if (warp == C::kLoad) {
     if (lane == 0) {
       // y, z, x of every chunk in turn, each tensor in a ring of its own
-      auto load = [&](const CUtensorMap* m, int off, int ring, int full, int empty, int k) {
-        const int s = k % ring;
-        if (k >= ring) wait(empty + s, k / ring - 1);
-        if (*gave_up) return false;
-        mbar_expect_tx(bars + full + s, C::kTile);
-        for (int p = 0; p < DP / 64; ++p)
-          tma_load_4d(sm + off + s * C::kTile + p * kPanelB, m, 64 * p, chunk(k) * kC, h, b, bars + full + s);
-        return true;
-      };
-      int ny = 0, nx = 0, nz = 0;   // loads issued
-      for (int k = 0; k < n; ++k) {
+      int ny = 1, nx = 1, nz = 1;   // loads issued
+      for (int k = 1; k < n; ++k) {
         if (!load(&jb.y, 0, C::kNY, kFullY, kEmptyY, k)) break;
         ++ny;
         if (!load(&jb.z, C::kOffZ, C::kNZ, kFullZ, kEmptyZ, k)) break;
