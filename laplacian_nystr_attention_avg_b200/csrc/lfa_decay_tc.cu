@@ -12,9 +12,9 @@
 // the time). D starts from zero in every chunk and is added to R by CUDA cores: tensor-core accumulation truncates
 // and would drift over thousands of chunks. All widths are padded to DP = 64 or 128 by TMA's zero fill.
 //
-// Warps: 4 or 8 for P, 4 or 8 for y's decayed rows, 8 for R and the epilogue, one thread each to issue TMA loads, the products
-// of the state and those of the output. Every hand-over is an mbarrier; every wait is bounded (on expiry the device's status
-// word is set, the CTA stops waiting for anything and drains what it has in flight).
+// Warps: 4 or 8 for P, 4 or 8 for y's decayed rows, 8 for R and the epilogue, one each to issue TMA loads, the
+// products of the state and those of the output. Every hand-over is an mbarrier; every wait is bounded (on expiry
+// the device's status word is set, the CTA stops waiting for anything and drains what it has in flight).
 //
 // Few units over long sequences: segments run at once. k_decay_tc<.., true> sums up each segment's own
 // state, k_decay_prefix carries them over the segments, and the main kernel starts every segment from its state.
@@ -104,8 +104,8 @@ struct Cfg {
 };
 enum Bar {
   kFullY = 0, kFullX = 3, kFullZ = 6, kEmptyY = 9, kEmptyX = 12, kEmptyZ = 15, kSFull = 18, kSRead, kPReady,
-  kYdReady, kPartFree = kYdReady + 2, kDFull = kPartFree + 2, kDRead, kRbReady, kXDone, kOFull, kOFree = kOFull + 2, kZClean = kOFree + 2, kFin,
-  kNumBars = kFin + 2
+  kYdReady, kPartFree = kYdReady + 2, kDFull = kPartFree + 2, kDRead, kRbReady, kXDone, kOFull, kOFree = kOFull + 2,
+  kZClean = kOFree + 2, kFin, kNumBars = kFin + 2
 };
 static_assert(kNumBars * 8 <= 368, "barriers overlap the TMEM slot");
 
@@ -188,9 +188,10 @@ __device__ __forceinline__ uint32_t packf2(uint64_t v) { return pack2(f2_lo(v), 
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 
 // The P warps of a run of n chunks: P = c_intra l^|i-j| S on the causal side, in bf16 (thread = token row i; with
-// two warps for a quarter of the rows, they take its blocks of 32 columns in turn). pi holds c_intra l^n after 32 zeros; beside
-// the diagonal block l^|i-j| is l^(distance of i to the block) pb[c]. nv0: valid tokens of the first chunk, where a
-// reverse run finds its sequence's ragged end (forwards, columns behind the end are above the diagonal).
+// two warps for a quarter of the rows, they take its blocks of 32 columns in turn). pi holds c_intra l^n after 32
+// zeros; beside the diagonal block l^|i-j| is l^(distance of i to the block) pb[c]. nv0: valid tokens of the first
+// chunk, where a reverse run finds its sequence's ragged end (forwards, columns behind the end are above the
+// diagonal).
 template <class C, bool REV>
 __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bars, uint32_t tmem, const float* pi,
                                         const float* pb, int nv0) {
@@ -314,9 +315,9 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       mbar_init(bars + i, i >= kEmptyY && i < kEmptyX                                    ? C::kYW + (STATE ? 0 : 1)
                           : i >= kEmptyZ && i < kSFull                                   ? (STATE ? 1 : 2)
                           : (i >= kYdReady && i < kPartFree) || i == kZClean             ? C::kYW
-                          : i == kSRead || i == kPReady                                    ? C::kPW
-                          : i == kDRead || i == kRbReady || (i >= kOFree && i < kZClean)          ? 8
-                                                                                                  : 1);
+                          : i == kSRead || i == kPReady                                  ? (STATE ? 1 : C::kPW)
+                          : i == kDRead || i == kRbReady || (i >= kOFree && i < kZClean) ? 8
+                                                                                         : 1);
     mbar_init_fence();
     *gave_up = 0;
     // the first chunk is under way while the rest is set up

@@ -216,7 +216,7 @@ lfa_status lfa_rotary(const lfa_rotary_config* c, const void* x, const void* x2,
   if (c->d < 8 || c->d > 256 || c->d % (16 / elem(c->dtype)) != 0) return LFA_ERR_UNSUPPORTED;
   if (c->rot < 2 || c->rot % 2 != 0 || c->rot > c->d) return LFA_ERR_INVALID_ARG;
   if (c->rot > 128 || c->heads > 4096 || c->heads2 > 4096 || c->N > (1 << 28)) return LFA_ERR_UNSUPPORTED;
-  if ((long long)c->B * c->N >= (1ll << 31)) return LFA_ERR_UNSUPPORTED;
+  if ((long long)c->B * c->N > (1ll << 30)) return LFA_ERR_UNSUPPORTED;
   if (!ok16(x) || !ok16(y) || !positions || !freqs) return LFA_ERR_INVALID_ARG;
   if (c->heads2 > 0 ? (!ok16(x2) || !ok16(y2)) : (x2 || y2)) return LFA_ERR_INVALID_ARG;
   lfa::RotaryArgs a;
@@ -228,6 +228,7 @@ lfa_status lfa_rotary(const lfa_rotary_config* c, const void* x, const void* x2,
                         !strides(c->y2_stride, c->B, c->heads2, c->N, c->d, c->dtype, true, a.y2s)))
     return LFA_ERR_INVALID_ARG;
   if (x == y && memcmp(a.xs, a.ys, sizeof(a.xs)) != 0) return LFA_ERR_INVALID_ARG;
+  if (x2 && (y == y2 || y == x2 || y2 == x)) return LFA_ERR_INVALID_ARG;
   if (x2 && x2 == y2 && memcmp(a.x2s, a.y2s, sizeof(a.x2s)) != 0) return LFA_ERR_INVALID_ARG;
   a.B = c->B;
   a.N = c->N;

@@ -2,8 +2,8 @@
 backward, single token), rotary positions, group norm with an activation, and the layer they make up.
 
 Argument checks and marshalling only: every step runs in the library's CUDA kernels. Attention tensors are
-[B, heads, N, d] with any strides for batch, head and token (a transposed [B, N, heads, d] needs no copy),
-bfloat16 or float32, channels contiguous. Work is enqueued on `stream` (default: the current stream of the
+[B, heads, N, d] with any strides for batch, head and token (a transposed [B, N, heads, d] needs no copy;
+broadcast ones are refused), bfloat16 or float32, channels contiguous. Work is enqueued on `stream` (default: the current stream of the
 tensors' device); buffers that a call makes itself belong to that stream.
 """
 from __future__ import annotations
@@ -82,6 +82,8 @@ def _tokens(t: torch.Tensor, name: str, shape, dtype, device) -> Tuple[int, ...]
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}: channels must be contiguous (strides {st})")
+    if 0 in st and any(n > 1 and a == 0 for n, a in zip(shape, st)):   # three zeros mean contiguous to the library
+        raise ValueError(f"{name}: a broadcast tensor (strides {st}); give a contiguous copy")
     return st
 
 
@@ -500,6 +502,8 @@ class DecayAttention:
     def _rotate(self, q, k, positions, inverse):
         if self.freqs is None:
             return q, k
+        if positions is None:
+            raise ValueError("positions: needed with freqs")
         return rotary(q, positions, self.freqs, x2=k, layout=self.layout, mscale=self.mscale, inverse=inverse)
 
     def forward(self, q, k, v, positions=None, *, S0=None, lengths=None, stream=None):
@@ -536,7 +540,8 @@ class DecayAttention:
         B, heads, dv = v.shape
         with _in(_first(v, "v", 3).index, stream):
             if self.freqs is not None:
-                qr, kr = self._rotate(q.unsqueeze(2), k.unsqueeze(2), positions.view(-1, 1), False)
+                pos = None if positions is None else positions.unsqueeze(-1)
+                qr, kr = self._rotate(q.unsqueeze(2), k.unsqueeze(2), pos, False)
                 q, k = qr.squeeze(2), kr.squeeze(2)
             o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
             decay_step(q, k, v, self.log_decay, S, scale=self.scale, slots=slots, O=o)

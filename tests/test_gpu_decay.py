@@ -19,7 +19,7 @@ import math
 import pytest
 import torch
 
-from laplacian_nystr_attention_avg_b200 import decay
+from laplacian_nystr_attention_avg_b200 import decay, lfa
 from tests import token_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -329,3 +329,76 @@ def test_other_stream_and_graph(dtype):
     torch.cuda.synchronize()
     for o in outs:
         assert all(torch.equal(a, b) for a, b in zip(want, o) if a is not None)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU have workspaces of their own."""
+    sets = [_inputs(1, 4, 3000, 64, 64, BF, seed=i) for i in range(2)]
+    want = [decay.decay_forward(q, k, v, ld, S0=S0, return_state=True) + decay.decay_backward(q, k, v, ld, v, S0=S0)
+            for q, k, v, ld, S0, _, _ in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [None, None]
+    for _ in range(4):
+        for i, (q, k, v, ld, S0, _, _) in enumerate(sets):
+            got[i] = decay.decay_forward(q, k, v, ld, S0=S0, return_state=True, stream=streams[i]) + \
+                decay.decay_backward(q, k, v, ld, v, S0=S0, stream=streams[i])
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, g) if a is not None)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_offsets_beyond_32_bits(dtype):
+    """Batches more than 2^31 elements apart in one buffer, inputs and output."""
+    d, H, N, far = 64, 2, 150, (1 << 31) + 64
+    g = torch.Generator("cuda").manual_seed(9)
+    buf = torch.empty(far + 4 * H * N * d, dtype=dtype, device="cuda")
+
+    def place(i):
+        t = buf.as_strided((2, H, N, d), (far, N * d, d, 1), i * H * N * d)
+        t.copy_(torch.randn((2, H, N, d), generator=g, device="cuda"))
+        return t
+
+    q, k, v, O = (place(i) for i in range(4))
+    ld = _log_decay(H)
+    decay.decay_forward(q, k, v, ld, O=O)
+    want, _ = decay.decay_forward(q.contiguous(), k.contiguous(), v.contiguous(), ld)
+    assert torch.equal(O, want)
+    grads = decay.decay_backward(q, k, v, ld, v.contiguous(), dQ=O, dK=None, dV=None)[0] if dtype == F32 else None
+    if grads is not None:
+        want = decay.decay_backward(q.contiguous(), k.contiguous(), v.contiguous(), ld, v.contiguous())[0]
+        assert torch.equal(grads, want)
+
+
+def test_step_in_a_pool_beyond_32_bits():
+    H, d, n = 16, 128, 8300     # 8300 x 262144 floats: the last slots lie behind element 2^31
+    S = torch.empty((n, H, d, d), device="cuda")
+    g = torch.Generator("cuda").manual_seed(2)
+    slots = torch.tensor([0, 8299, 8192], dtype=torch.int32, device="cuda")
+    S[slots.long()] = torch.randn((3, H, d, d), generator=g, device="cuda")
+    small = S[slots.long()].clone()
+    q, k, v = (torch.randn((3, H, d), generator=g, device="cuda") for _ in range(3))
+    ld = _log_decay(H)
+    o = decay.decay_step(q, k, v, ld, S, slots=slots)
+    assert torch.equal(o, decay.decay_step(q, k, v, ld, small))
+    assert torch.equal(S[slots.long()], small)
+
+
+def test_refused_on_the_device():
+    q, k, v, ld, _, _, _ = _inputs(2, 2, 40, 16, 16, F32)
+    with pytest.raises(ValueError):
+        decay.decay_forward(q[:1].expand(2, -1, -1, -1), k, v, ld)
+    with pytest.raises(ValueError):
+        decay.decay_forward(q, k, v, ld, O=torch.zeros_like(v[:1]).expand(2, -1, -1, -1))
+    with pytest.raises(ValueError):
+        decay.decay_forward(q, k, v, ld, O=torch.zeros(2, 2, 16, 40, device="cuda").transpose(2, 3))
+    with pytest.raises(lfa.LfaError):
+        decay.decay_forward(q, k, v, ld, O=v)
+    with pytest.raises(ValueError):
+        decay.decay_forward(q, k.cpu(), v, ld)
+    with pytest.raises(TypeError):
+        decay.decay_forward(q, k.double(), v, ld)
+    with pytest.raises(ValueError):
+        decay.decay_backward(q, k, v, ld, v, dQ=torch.empty_like(q).transpose(1, 2).contiguous().transpose(1, 2))
+    assert torch.isfinite(decay.decay_forward(q, k, v, ld)[0]).all()

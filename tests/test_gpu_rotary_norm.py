@@ -249,6 +249,25 @@ def test_repeated_calls_graph_and_stream(dtype):
     assert all(torch.equal(a, b) for a, b in zip(want, out))
 
 
+def test_more_than_32_bits_of_elements():
+    """2.3e9 elements: rows from both ends against the same rows alone."""
+    B, C, G = 70000, 32768, 64
+    x = torch.empty((B, 1, C), dtype=BF, device="cuda")
+    x.copy_(torch.arange(C, device="cuda").remainder(97).to(BF) * 0.1)
+    x[0] += 1
+    x[-1] *= -2
+    y, mean, rstd = decay.group_norm(x, G, act="silu")
+    rows = torch.tensor([0, 1, B // 2, B - 1], device="cuda")
+    want, m, r = decay.group_norm(x[rows].contiguous(), G, act="silu")
+    assert torch.equal(y[rows], want) and torch.equal(mean[rows], m) and torch.equal(rstd[rows], r)
+    freqs, _ = decay.rotary_frequencies(128)
+    pos = torch.arange(B, device="cuda", dtype=torch.int32).view(1, B)
+    v = x.view(1, B, C // 128, 128).transpose(1, 2)
+    z, _ = decay.rotary(v, pos, freqs, out=y.view(1, B, C // 128, 128).transpose(1, 2))
+    w, _ = decay.rotary(v[:, :, rows].contiguous(), pos[:, rows].contiguous(), freqs)
+    assert torch.equal(z[:, :, rows], w)
+
+
 # ---- the layer -----------------------------------------------------------------------------------------
 
 def _layer(B, N, H, dk, dv, seed=0):

@@ -130,7 +130,7 @@ def _rc(**kw):
     (dict(B=0), BAD), (dict(N=0), BAD), (dict(heads=0), BAD), (dict(heads2=-1), BAD), (dict(mscale=math.nan), BAD),
     (dict(rot=0), BAD), (dict(rot=31), BAD), (dict(rot=66), BAD), (dict(d=4), UNSUP), (dict(d=60), UNSUP), (dict(d=264), UNSUP),
     (dict(d=256, rot=130), UNSUP), (dict(dtype=5), UNSUP), (dict(y_stride=(960, 320, 32)), BAD), (dict(x_stride=(960, 320, 65)), BAD),
-    (dict(B=1 << 12, N=1 << 20), UNSUP),
+    (dict(B=1 << 11, N=1 << 20), UNSUP),
 ])
 def test_rotary_refuses_configs(lib, kw, want):
     assert lib.lfa_rotary(_rc(**kw), A, None, A, A, 2 * A, None, None) == want
@@ -146,6 +146,9 @@ def test_rotary_refuses_pointers(lib):
     assert r(c, A, A, A, A, 2 * A, 3 * A, None) == BAD                # a second tensor without heads2
     assert r(_rc(heads2=2), A, None, A, A, 2 * A, None, None) == BAD  # heads2 without a second tensor
     assert r(_rc(x_stride=(960, 64, 192)), A, None, A, A, A, None, None) == BAD   # in place, other strides
+    two = _rc(heads2=3)
+    assert r(two, A, 2 * A, A, A, 3 * A, 3 * A, None) == BAD           # one output for both
+    assert r(two, A, 2 * A, A, A, 2 * A, A, None) == BAD               # crossed over
 
 
 def _nc(**kw):
@@ -241,3 +244,14 @@ def test_a_small_workspace_is_not_taken_for_none(lib):
         n = lib.lfa_group_norm_workspace_size(c, 1)
         assert n > 256
         assert lib.lfa_group_norm_backward(c, A, A, A, A, A, A, 2 * A, A, A, None, 0, None) == BAD
+
+
+@pytest.mark.parametrize("shape,strides", [((2, 2, 4, 8), (0, 0, 0, 1)), ((2, 2, 4, 8), (0, 32, 8, 1)),
+                                           ((2, 1, 1, 8), (0, 0, 0, 1)), ((2, 3, 8), (0, 0, 1)), ((1, 3, 8), (8, 0, 1))])
+def test_broadcast_tensors_are_refused(shape, strides):
+    """All strides zero would read as contiguous to the library, beyond the tensor's memory."""
+    t = torch.zeros(1024).as_strided(shape, strides)
+    with pytest.raises(ValueError, match="broadcast"):
+        decay._tokens(t, "q", shape, torch.float32, t.device)
+    one = torch.zeros(8).as_strided((1, 1, 1, 8), (0, 0, 0, 1))   # a single row is not broadcast
+    assert decay._tokens(one, "q", (1, 1, 1, 8), torch.float32, one.device) == (0, 0, 0, 1)
