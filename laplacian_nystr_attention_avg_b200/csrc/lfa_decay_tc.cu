@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
         }
         commit_by(lead, bars + kXDone);
         commit_by(lead, bars + kEmptyX + sx);
+        if (C::kOwnP && k + 1 < steps) scores(k + 1);
         wait(kFullZ + sz, k / C::kNZ);
         if (valid(chunk(k)) < kC) wait(kZClean, 0);
         wait(kPReady, k);
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
         for (int kk = 0; kk < kC / 16; ++kk) mma_ta_by(lead, oz, tm + C::kTp + 8 * kk, z + kk * 128, id_o, kk > 0);
         commit_by(lead, bars + kOFull + k % C::kNO);
         commit_by(lead, bars + kEmptyZ + sz);
-        if (k + 1 < steps) scores(k + 1);
+        if (!C::kOwnP && k + 1 < steps) scores(k + 1);
       }
       commit_by(lead, bars + kFin);
       wait.drain(kFin, 0);
