@@ -93,19 +93,20 @@ struct Cfg {
   // theirs, take 16 more from the P and y warps (16 each): 128 80 + 128 80 + 256 112 + 96 96 = 608 96
   static constexpr int kRegsP = DP == 64 ? 72 : 80, kRegsY = DP == 64 ? 64 : 80, kRegsR = DP == 64 ? 96 : 112;
   static constexpr bool kSplitRegs = !STATE;
-  // tensor memory columns. DP 64: S, P (bf16 pairs), two sets of Oz and Ox, D. DP 128: no room for all of that; P
-  // goes over the first half of S's columns, row by row as S is read, and there is one set of Oz and Ox
+  // tensor memory columns. DP 64: two sets of S, so that the next scores are there when the P warps, its longest
+  // chain, are; P (bf16 pairs), Oz, Ox, D. DP 128: no room for that; P goes over the first half of S's columns, row
+  // by row as S is read
   static constexpr bool kOwnP = DP == 64;
-  static constexpr int kNO = DP == 64 ? 2 : 1;
-  static constexpr int kTs = 0, kTp = kOwnP ? kC : 0, kToz = STATE ? 0 : kOwnP ? kC + kC / 2 : kC;
-  static constexpr int kTd = STATE ? 0 : kToz + kNO * 2 * DP;
+  static constexpr int kNS = kOwnP ? 2 : 1;   // sets of S
+  static constexpr int kTs = 0, kTp = kOwnP ? 2 * kC : 0, kToz = STATE ? 0 : kOwnP ? 2 * kC + kC / 2 : kC;
+  static constexpr int kTd = STATE ? 0 : kToz + 2 * DP;
   static constexpr int kTmem = STATE ? DP : 512;
   static_assert(kTd + DP <= kTmem, "tensor memory");
 };
 enum Bar {
-  kFullY = 0, kFullX = 3, kFullZ = 6, kEmptyY = 9, kEmptyX = 12, kEmptyZ = 15, kSFull = 18, kSRead, kPReady,
-  kYdReady, kPartFree = kYdReady + 2, kDFull = kPartFree + 2, kDRead, kRbReady, kXDone, kOFull, kOFree = kOFull + 2,
-  kZClean = kOFree + 2, kFin, kNumBars = kFin + 2
+  kFullY = 0, kFullX = 3, kFullZ = 6, kEmptyY = 9, kEmptyX = 12, kEmptyZ = 15, kSFull = 18, kSRead = 20,
+  kPReady = 22, kYdReady, kPartFree = kYdReady + 2, kDFull = kPartFree + 2, kDRead, kRbReady, kXDone, kOFull, kOFree,
+  kZClean, kFin, kNumBars = kFin + 2
 };
 static_assert(kNumBars * 8 <= 368, "barriers overlap the TMEM slot");
 
@@ -207,14 +208,15 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
   if (C::kOwnP) zeros();
   for (int k = 0; k < n; ++k) {
     const bool ragged = REV && k == 0 && nv0 < kC;
-    wait(kSFull, k);
+    wait(kSFull + k % C::kNS, k / C::kNS);
+    const uint32_t sk = srow + k % C::kNS * kC;
     tc_fence_after();
     bool used = !C::kOwnP || k == 0;   // P's columns are free
 #pragma unroll 1
     for (int cb = first; cb < 4; cb += C::kPW / 4) {
       if (REV ? cb < q : cb > q) continue;
       uint32_t v[32];
-      tmem_ld32_async(srow + 32 * cb, v);
+      tmem_ld32_async(sk + 32 * cb, v);
       if (cb == q) {
         tmem_wait_ld(v);
 #pragma unroll
@@ -245,7 +247,7 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
 #pragma unroll
       for (int c = 0; c < 16; ++c) w[c] = pack2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
       if (!used) {
-        wait(kOFull + (k - 1) % C::kNO, (k - 1) / C::kNO);
+        wait(kOFull, k - 1);
         tc_fence_after();
         used = true;
       }
@@ -254,7 +256,9 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
     if (C::kOwnP) {   // S has been read
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + kSRead);
+      if (lane == 0) mbar_arrive(bars + kSRead + k % C::kNS);
+      // a warp without a block may be ahead of the others: not by a chunk, or its arrival would count for theirs
+      if (!used) wait(kOFull, k - 1);
     } else {
       zeros();
     }
@@ -315,8 +319,8 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       mbar_init(bars + i, i >= kEmptyY && i < kEmptyX                                    ? C::kYW + (STATE ? 0 : 1)
                           : i >= kEmptyZ && i < kSFull                                   ? (STATE ? 1 : 2)
                           : (i >= kYdReady && i < kPartFree) || i == kZClean             ? C::kYW
-                          : i == kSRead || i == kPReady                                  ? (STATE ? 1 : C::kPW)
-                          : i == kDRead || i == kRbReady || (i >= kOFree && i < kZClean) ? 8
+                          : (i >= kSRead && i <= kPReady)                                 ? (STATE ? 1 : C::kPW)
+                          : i == kDRead || i == kRbReady || i == kOFree                  ? 8
                                                                                          : 1);
     mbar_init_fence();
     *gave_up = 0;
@@ -373,23 +377,24 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
         const uint64_t y = d_y + sy * (C::kTile / 16), x = d_x + sx * (C::kTile / 16);
         wait(kFullY + sy, k / C::kNY);
         wait(kFullX + sx, k / C::kNX);
-        if (k > 0) wait(C::kOwnP ? kSRead : kOFull, k - 1);   // S has been read; without its own columns, P used (kNO 1)
+        if (k >= C::kNS) C::kOwnP ? wait(kSRead + k % C::kNS, k / C::kNS - 1) : wait(kOFull, k - 1);   // S (and P over it) used
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk) {
           const int off = ((kk >> 2) * kPanelB + (kk & 3) * 32) / 16;
-          mma_by(lead, tm + C::kTs, x + off, y + off, id_s, kk > 0);
+          mma_by(lead, tm + C::kTs + k % C::kNS * kC, x + off, y + off, id_s, kk > 0);
         }
-        commit_by(lead, bars + kSFull);
+        commit_by(lead, bars + kSFull + k % C::kNS);
         commit_by(lead, bars + kEmptyY + sy);
       };
       scores(0);
       for (int k = 0; k < steps; ++k) {
         const int sx = k % C::kNX, sz = k % C::kNZ;
         const uint64_t x = d_x + sx * (C::kTile / 16), z = d_z + sz * (C::kTile / 16);
-        const uint32_t oz = tm + C::kToz + (k % C::kNO) * 2 * DP, ox = oz + DP;
+        const uint32_t oz = tm + C::kToz, ox = oz + DP;
+        if (C::kOwnP && k + 1 < steps) scores(k + 1);
         wait(kRbReady, k);
-        if (k >= C::kNO) wait(kOFree + k % C::kNO, k / C::kNO - 1);
+        if (k > 0) wait(kOFree, k - 1);
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < (C::kStack ? 2 : 1) * DP / 16; ++kk) {   // stacked: x again, times the second tile of R
@@ -398,14 +403,13 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
         }
         commit_by(lead, bars + kXDone);
         commit_by(lead, bars + kEmptyX + sx);
-        if (C::kOwnP && k + 1 < steps) scores(k + 1);
         wait(kFullZ + sz, k / C::kNZ);
         if (valid(chunk(k)) < kC) wait(kZClean, 0);
         wait(kPReady, k);
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kC / 16; ++kk) mma_ta_by(lead, oz, tm + C::kTp + 8 * kk, z + kk * 128, id_o, kk > 0);
-        commit_by(lead, bars + kOFull + k % C::kNO);
+        commit_by(lead, bars + kOFull);
         commit_by(lead, bars + kEmptyZ + sz);
         if (!C::kOwnP && k + 1 < steps) scores(k + 1);
       }
@@ -569,8 +573,8 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       float fk = f;
       if (rev && nv < kC) fk = i < nv ? c_inter * expf(ld * (nv - 1 - i)) : 0.f;
       const uint64_t ff = f2(fk, fk);
-      const uint32_t oz = quad + C::kToz + (k % C::kNO) * 2 * DP, ox = oz + DP;
-      wait(kOFull + k % C::kNO, k / C::kNO);
+      const uint32_t oz = quad + C::kToz, ox = oz + DP;
+      wait(kOFull, k);
       tc_fence_after();
 #pragma unroll
       for (int c0 = 0; c0 < NR; c0 += NT) {
@@ -582,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
         if (c0 + NT == NR) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bars + kOFree + k % C::kNO);
+          if (lane == 0) mbar_arrive(bars + kOFree);
         }
 #pragma unroll
         for (int g = 0; g < NT; g += 16) {
