@@ -202,10 +202,13 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
   // the other side of the diagonal is zero: once where P has its own columns, else in every chunk
   auto zeros = [&]() {
     uint32_t w[16] = {};
-    for (int cb = first; cb < 4; cb += C::kPW / 4)
+    for (int cb = 0; cb < 4; ++cb)
       if (REV ? cb < q : cb > q) tmem_st16(prow + 16 * cb, w);
   };
-  if (C::kOwnP) zeros();
+  if (C::kOwnP) {
+    if (q == (REV ? 3 : 0) && first == (REV ? 0 : 1)) return;   // the one of eight that has no block at all
+    zeros();
+  }
   for (int k = 0; k < n; ++k) {
     const bool ragged = REV && k == 0 && nv0 < kC;
     wait(kSFull + k % C::kNS, k / C::kNS);
@@ -257,8 +260,6 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + kSRead + k % C::kNS);
-      // a warp without a block may be ahead of the others: not by a chunk, or its arrival would count for theirs
-      if (!used) wait(kOFull, k - 1);
     } else {
       zeros();
     }
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       mbar_init(bars + i, i >= kEmptyY && i < kEmptyX                                    ? C::kYW + (STATE ? 0 : 1)
                           : i >= kEmptyZ && i < kSFull                                   ? (STATE ? 1 : 2)
                           : (i >= kYdReady && i < kPartFree) || i == kZClean             ? C::kYW
-                          : (i >= kSRead && i <= kPReady)                                 ? (STATE ? 1 : C::kPW)
+                          : i >= kSRead && i <= kPReady                                  ? (STATE ? 1 : C::kOwnP ? C::kPW - 1 : C::kPW)
                           : i == kDRead || i == kRbReady || i == kOFree                  ? 8
                                                                                          : 1);
     mbar_init_fence();
