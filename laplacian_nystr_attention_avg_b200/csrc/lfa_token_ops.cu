@@ -445,12 +445,16 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
     }
     load(id + (long long)U * teams, at + U * step);   // the next ones, meanwhile
     if constexpr (!BACKWARD) {
+      uint64_t d[U][NP];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float t = 0.f;
+        uint64_t t = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) t += raw_get<T>(v[u], i);
-        m[u] = t;   // threads without a vector hold zeros
+        for (int i = 0; i < NP; ++i) {
+          d[u][i] = raw_pair<T>(v[u], i);
+          t = add2(t, d[u][i]);   // threads without a vector hold zeros
+        }
+        m[u] = f2_lo(t) + f2_hi(t);
       }
       for (int o = s.T >> 1; o > 0; o >>= 1)
 #pragma unroll
@@ -458,13 +462,13 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         m[u] = __fdiv_rn(m[u], n);   // exact for constant groups
-        float t = 0.f;
+        uint64_t t = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float d = raw_get<T>(v[u], i) - m[u];
-          t = fmaf(d, d, t);
+        for (int i = 0; i < NP; ++i) {
+          d[u][i] = add2(d[u][i], V == 1 ? f2(-m[u], 0.f) : both(-m[u]));
+          t = fma2(d[u][i], d[u][i], t);
         }
-        rs[u] = has ? t : 0.f;
+        rs[u] = has ? f2_lo(t) + f2_hi(t) : 0.f;
       }
       for (int o = s.T >> 1; o > 0; o >>= 1)
 #pragma unroll
@@ -479,11 +483,9 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
             a.rstd[iu] = rs[u];
           }
           if (has) {
-            uint64_t o[NP];
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
-              o[i] = act2<ACT>(fma2(mul2(add2(raw_pair<T>(v[u], i), both(-m[u])), both(rs[u])), ga[i], be[i]));
-            raw_store<VB>(y + at + u * step, raw_make<T, VB>(o));
+            for (int i = 0; i < NP; ++i) d[u][i] = act2<ACT>(fma2(mul2(d[u][i], both(rs[u])), ga[i], be[i]));
+            raw_store<VB>(y + at + u * step, raw_make<T, VB>(d[u]));
           }
         }
       }
