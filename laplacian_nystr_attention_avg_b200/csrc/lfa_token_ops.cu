@@ -10,170 +10,6 @@
 namespace lfa {
 namespace {
 
-// ---- rotary positions -------------------------------------------------------------------------------
-// Pair i of a token at position p turns by th = p f_i: (a, b) -> mscale (a cos th - b sin th, a sin th + b cos th).
-// th is reduced in turns in 64 bits (p f / 2 pi minus its nearest whole number), so that far positions keep their
-// angle; the rest is fp32. A thread has one token and one unit of a head's channels (V pairs in two 16-byte
-// vectors, V / 2 pairs in one, or a single pair), forms their cosines and sines once, and goes over the heads.
-constexpr int kRThreads = 256;
-constexpr int kWave = 3 * 148;   // blocks of 256 threads with 80 registers that run at once
-constexpr int kRHeads = 2;   // heads read at once, one such group ahead
-
-template <typename T>
-struct Vec {
-  static constexpr int n = 16 / sizeof(T);
-  T v[n];
-};
-template <typename T>
-__device__ __forceinline__ Vec<T> vload(const T* p) {
-  Vec<T> r;
-  *reinterpret_cast<uint4*>(r.v) = *reinterpret_cast<const uint4*>(p);
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ void vstore(T* p, const Vec<T>& r) {
-  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.v);
-}
-__device__ __forceinline__ float2 turn(const RotaryArgs& a, double pos, int i) {
-  const double turns = pos * (a.freqs[i] * 0.15915494309189533577);
-  float sn, c;
-  sincospif(2.f * (float)(turns - rint(turns)), &sn, &c);
-  return make_float2(a.mscale * c, a.inverse ? -a.mscale * sn : a.mscale * sn);
-}
-
-// units of a head's row: MODE 0: half layout, rot / 2 a whole number of vectors; 1: interleaved; 2: half layout,
-// any even rot
-template <typename T, int MODE>
-__host__ __device__ __forceinline__ int rotary_units(int d, int rot) {
-  constexpr int V = 16 / sizeof(T);
-  return MODE == 0 ? rot / 2 / V + (d - rot) / V : MODE == 1 ? d / V : rot / 2 + d - rot;
-}
-
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kRThreads) k_rotary(const __grid_constant__ RotaryArgs a, int units, int tokens,
-                                                      int heads_each) {
-  constexpr int V = Vec<T>::n, NP = MODE == 0 ? V : MODE == 1 ? V / 2 : 1;   // pairs of a unit
-  const int tl = threadIdx.x / units, unit = threadIdx.x - tl * units, tok = blockIdx.x * tokens + tl;
-  if (tl >= tokens || tok >= a.B * a.N) return;
-  const int half = a.rot >> 1;
-  const int b = tok / a.N, n = tok - b * a.N;
-  // first pair of the unit, and its channels
-  const int pair = unit * NP, c0 = MODE == 2 ? unit : unit * V;
-  const bool turns = MODE == 1 ? c0 < a.rot : pair < half;
-  const int copy = MODE == 0 ? a.rot + (unit - half / V) * V : MODE == 1 ? c0 : half + unit;
-  const int all = a.heads + a.heads2;
-  const int h0 = blockIdx.y * heads_each, h1 = min(h0 + heads_each, all);
-  auto element = [&](int h, bool out) {   // of this token's row of head h, from x (y) or x2 (y2)
-    const bool second = h >= a.heads;
-    const long long* s = out ? (second ? a.y2s : a.ys) : (second ? a.x2s : a.xs);
-    return b * s[0] + (second ? h - a.heads : h) * s[1] + n * s[2];
-  };
-  struct Group {
-    Vec<T> p[kRHeads], q[kRHeads];
-    T sp[kRHeads], sq[kRHeads];
-  };
-  auto load = [&](Group& g, int h) {
-#pragma unroll
-    for (int e = 0; e < kRHeads; ++e)
-      if (h + e < h1) {
-        const T* x = static_cast<const T*>(h + e >= a.heads ? a.x2 : a.x) + element(h + e, false);
-        if constexpr (MODE == 2) {
-          g.sp[e] = x[turns ? c0 : copy];
-          if (turns) g.sq[e] = x[c0 + half];
-        } else {
-          g.p[e] = vload(x + (turns ? c0 : copy));
-          if (MODE == 0 && turns) g.q[e] = vload(x + c0 + half);
-        }
-      }
-  };
-  Group cur, next;
-  load(cur, h0);   // under way while the angles are formed
-  float2 w[NP];
-  if (turns) {
-    const double pos = (double)a.positions[tok];
-#pragma unroll
-    for (int i = 0; i < NP; ++i) w[i] = pair + i < half ? turn(a, pos, pair + i) : make_float2(1.f, 0.f);
-  }
-  for (int h = h0; h < h1; h += kRHeads) {
-    if (h + kRHeads < h1) load(next, h + kRHeads);
-#pragma unroll
-    for (int e = 0; e < kRHeads; ++e) {
-      if (h + e >= h1) break;
-      T* y = static_cast<T*>(h + e >= a.heads ? a.y2 : a.y) + element(h + e, true);
-      if (!turns) {
-        if constexpr (MODE == 2)
-          y[copy] = cur.sp[e];
-        else
-          vstore(y + copy, cur.p[e]);
-      } else if constexpr (MODE == 0) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float u = to_f<T>(cur.p[e].v[i]), v = to_f<T>(cur.q[e].v[i]);
-          cur.p[e].v[i] = from_f<T>(u * w[i].x - v * w[i].y);
-          cur.q[e].v[i] = from_f<T>(u * w[i].y + v * w[i].x);
-        }
-        vstore(y + c0, cur.p[e]);
-        vstore(y + c0 + half, cur.q[e]);
-      } else if constexpr (MODE == 1) {
-#pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          if (c0 + i < a.rot) {   // channels behind rot stay as they are, bit by bit
-            const float u = to_f<T>(cur.p[e].v[i]), v = to_f<T>(cur.p[e].v[i + 1]);
-            const float2 z = w[i / 2];
-            cur.p[e].v[i] = from_f<T>(u * z.x - v * z.y);
-            cur.p[e].v[i + 1] = from_f<T>(u * z.y + v * z.x);
-          }
-        }
-        vstore(y + c0, cur.p[e]);
-      } else {
-        const float u = to_f<T>(cur.sp[e]), v = to_f<T>(cur.sq[e]);
-        y[c0] = from_f<T>(u * w[0].x - v * w[0].y);
-        y[c0 + half] = from_f<T>(u * w[0].y + v * w[0].x);
-      }
-    }
-    cur = next;
-  }
-}
-
-template <typename T, int MODE>
-void rotary_launch(const RotaryArgs& a, cudaStream_t st) {
-  const int units = rotary_units<T, MODE>(a.d, a.rot), tokens = kRThreads / units;   // units <= 256
-  const int tiles = ceil_div(a.B * a.N, tokens), all = a.heads + a.heads2;
-  // Heads are split over blocks, which form the angles once each (worth about three heads): as many parts as give
-  // the shortest run of whole waves, three blocks an SM at a time (4 x 4096 tokens, 32 heads: one part 57 us in
-  // 1.5 waves, two 51 us in 3).
-  int each = all;
-  long long best = 0;
-  for (int parts = 1; parts <= all; ++parts) {
-    const int e = ceil_div(all, parts);
-    const long long waves = ((long long)tiles * ceil_div(all, e) + kWave - 1) / kWave, cost = waves * (e + 3);
-    if (best == 0 || cost < best) {
-      best = cost;
-      each = e;
-    }
-  }
-  k_rotary<T, MODE><<<dim3(tiles, ceil_div(all, each)), kRThreads, 0, st>>>(a, units, tokens, each);
-}
-template <typename T>
-void run_rotary(const RotaryArgs& a, cudaStream_t st) {
-  if (a.interleaved)
-    rotary_launch<T, 1>(a, st);
-  else if ((a.rot / 2) % Vec<T>::n == 0)
-    rotary_launch<T, 0>(a, st);
-  else
-    rotary_launch<T, 2>(a, st);
-}
-
-// ---- group norm ---------------------------------------------------------------------------------------
-// Two ways through the data. Small groups (N C/G elements that one warp or one block holds in registers) are read
-// once: a team of threads per (sample, group) forms the mean, the variance about it and the output. Larger ones
-// take three launches: per-channel sums of row chunks, their combination per group, and the output; the second
-// reading comes from the 126 MB L2 as far as the tensor fits there. All sums are joined in a fixed order.
-constexpr int kNT = 256;         // threads per block
-constexpr int kNRows = 8;        // rows a thread has in flight
-constexpr int kNormWave = 4 * 148;   // blocks that run at once
-constexpr int kMaxChunks = 64;   // row chunks per sample (large groups)
-
 using sm100::add2;
 using sm100::f2;
 using sm100::f2_hi;
@@ -183,40 +19,6 @@ using sm100::mul2;
 
 // Channels go in pairs: the packed fp32 instructions take two at a time.
 __device__ __forceinline__ uint64_t both(float v) { return f2(v, v); }
-// 1 / (1 + exp(-z)): exponent and reciprocal within 2 units each (2^-22 relative)
-__device__ __forceinline__ float rcp_approx(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
-  const uint64_t t = mul2(z, both(-1.4426950408889634f));
-  const uint64_t d = add2(f2(sm100::ex2_approx(f2_lo(t)), sm100::ex2_approx(f2_hi(t))), both(1.f));
-  return f2(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d)));
-}
-__device__ __forceinline__ uint64_t normal_cdf2(uint64_t z) {   // 0.5 (1 + erf(z / sqrt 2))
-  return f2(fmaf(0.5f, erff(f2_lo(z) * 0.70710678118654752f), 0.5f), fmaf(0.5f, erff(f2_hi(z) * 0.70710678118654752f), 0.5f));
-}
-template <int ACT>
-__device__ __forceinline__ uint64_t act2(uint64_t z) {
-  if (ACT == LFA_ACT_SILU) return mul2(z, sigmoid2(z));
-  if (ACT == LFA_ACT_GELU) return mul2(z, normal_cdf2(z));
-  return z;
-}
-template <int ACT>
-__device__ __forceinline__ uint64_t slope2(uint64_t z) {
-  if (ACT == LFA_ACT_SILU) {   // p + z p (1 - p)
-    const uint64_t p = sigmoid2(z);
-    return fma2(mul2(z, p), fma2(p, both(-1.f), both(1.f)), p);
-  }
-  if (ACT == LFA_ACT_GELU) {
-    const uint64_t t = mul2(mul2(z, z), both(-0.72134752044448170f));
-    const uint64_t e = f2(sm100::ex2_approx(f2_lo(t)), sm100::ex2_approx(f2_hi(t)));
-    return fma2(mul2(z, both(0.3989422804014327f)), e, normal_cdf2(z));
-  }
-  return both(1.f);
-}
-
 // VB bytes of a row, and its elements in fp32
 template <int VB>
 struct Raw {
@@ -267,6 +69,209 @@ __device__ __forceinline__ Raw<VB> raw_make(const uint64_t* v) {
   }
   return r;
 }
+// ---- rotary positions -------------------------------------------------------------------------------
+// Pair i of a token at position p turns by th = p f_i: (a, b) -> mscale (a cos th - b sin th, a sin th + b cos th).
+// th is reduced in turns in 64 bits (p f / 2 pi minus its nearest whole number), so that far positions keep their
+// angle; the rest is fp32. A thread has one token and one unit of a head's channels (V pairs in two 16-byte
+// vectors, V / 2 pairs in one, or a single pair), forms their cosines and sines once, and goes over the heads.
+constexpr int kRThreads = 256;
+constexpr int kWave = 3 * 148;   // blocks of 256 threads with 80 registers that run at once
+constexpr int kRHeads = 2;   // heads read at once, one such group ahead
+
+__device__ __forceinline__ float2 turn(const RotaryArgs& a, double pos, int i) {
+  const double turns = pos * (a.freqs[i] * 0.15915494309189533577);
+  float sn, c;
+  sincospif(2.f * (float)(turns - rint(turns)), &sn, &c);
+  return make_float2(a.mscale * c, a.inverse ? -a.mscale * sn : a.mscale * sn);
+}
+
+// Units of a head's row. MODE 0: half layout, rot / 2 a whole number of vectors: the two vectors of V pairs, or two
+// vectors to copy; 1: interleaved, a vector; 2: half layout, any even rot: a pair, or a channel to copy
+template <typename T, int MODE>
+__host__ __device__ __forceinline__ int rotary_units(int d, int rot) {
+  constexpr int V = 16 / sizeof(T);
+  return MODE == 0 ? rot / 2 / V + ((d - rot) / V + 1) / 2 : MODE == 1 ? d / V : rot / 2 + d - rot;
+}
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kRThreads, 3) k_rotary(const __grid_constant__ RotaryArgs a, int units, int tokens,
+                                                      int heads_each) {
+  constexpr int V = 16 / sizeof(T), NP = MODE == 0 ? V : MODE == 1 ? V / 2 : 1;   // pairs of a unit
+  const int tl = threadIdx.x / units, unit = threadIdx.x - tl * units, tok = blockIdx.x * tokens + tl;
+  if (tl >= tokens || tok >= a.B * a.N) return;
+  const int half = a.rot >> 1;
+  const int b = tok / a.N, n = tok - b * a.N;
+  const int pair = unit * NP;   // the unit's first
+  const bool turns = pair < half;
+  // channels of the unit's first and second part
+  const int cp = MODE == 1 ? unit * V : turns ? pair : MODE == 0 ? a.rot + (2 * unit - a.rot / V) * V : half + unit;
+  const int cq = turns ? cp + half : cp + V;
+  const bool two = MODE == 1 ? false : turns || (MODE == 0 && cq < a.d);
+  const int all = a.heads + a.heads2;
+  const int h0 = blockIdx.y * heads_each, h1 = min(h0 + heads_each, all);
+  const T* const x1 = static_cast<const T*>(a.x) + b * a.xs[0] + n * a.xs[2];
+  const T* const x2 = static_cast<const T*>(a.x2) + b * a.x2s[0] + n * a.x2s[2];
+  T* const y1 = static_cast<T*>(a.y) + b * a.ys[0] + n * a.ys[2];
+  T* const y2 = static_cast<T*>(a.y2) + b * a.y2s[0] + n * a.y2s[2];
+  struct Group {
+    Raw<16> p[kRHeads], q[kRHeads];
+    T sp[kRHeads], sq[kRHeads];
+  };
+  auto load = [&](Group& g, int h) {
+#pragma unroll
+    for (int e = 0; e < kRHeads; ++e)
+      if (h + e < h1) {
+        const int k = h + e - a.heads;
+        const T* x = k >= 0 ? x2 + k * a.x2s[1] : x1 + (h + e) * a.xs[1];
+        if constexpr (MODE == 2) {
+          g.sp[e] = x[cp];
+          if (two) g.sq[e] = x[cq];
+        } else {
+          g.p[e] = raw_load<16>(x + cp);
+          if (MODE == 0 && two) g.q[e] = raw_load<16>(x + cq);
+        }
+      }
+  };
+  Group cur, next;
+  load(cur, h0);   // under way while the angles are formed
+  float2 w[NP];
+  if (turns) {
+    const double pos = (double)a.positions[tok];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) w[i] = pair + i < half ? turn(a, pos, pair + i) : make_float2(1.f, 0.f);
+  }
+  for (int h = h0; h < h1; h += kRHeads) {
+    if (h + kRHeads < h1) load(next, h + kRHeads);
+#pragma unroll
+    for (int e = 0; e < kRHeads; ++e) {
+      if (h + e >= h1) break;
+      const int k = h + e - a.heads;
+      T* y = k >= 0 ? y2 + k * a.y2s[1] : y1 + (h + e) * a.ys[1];
+      if constexpr (MODE == 0) {
+        if (turns) {
+          uint64_t o[V / 2], r[V / 2];
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            const uint64_t u = raw_pair<T>(cur.p[e], i), v = raw_pair<T>(cur.q[e], i);
+            const uint64_t cs = f2(w[2 * i].x, w[2 * i + 1].x), sn = f2(w[2 * i].y, w[2 * i + 1].y);
+            o[i] = fma2(mul2(v, sn), both(-1.f), mul2(u, cs));
+            r[i] = fma2(v, cs, mul2(u, sn));
+          }
+          cur.p[e] = raw_make<T, 16>(o);
+          cur.q[e] = raw_make<T, 16>(r);
+        }
+        raw_store<16>(y + cp, cur.p[e]);
+        if (two) raw_store<16>(y + cq, cur.q[e]);
+      } else if constexpr (MODE == 1) {
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+          const float u = raw_get<T>(cur.p[e], i), v = raw_get<T>(cur.p[e], i + 1);
+          const float2 z = w[i / 2];
+          o[i] = u * z.x - v * z.y;
+          o[i + 1] = u * z.y + v * z.x;
+        }
+        const Raw<16> was = cur.p[e];
+        if (turns) {
+          uint64_t o2[V / 2];
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) o2[i] = f2(o[2 * i], o[2 * i + 1]);
+          cur.p[e] = raw_make<T, 16>(o2);
+#pragma unroll
+          for (int i = 0; i < V; i += 2)   // channels behind rot stay as they are, bit by bit
+            if (cp + i >= a.rot) {
+              if constexpr (sizeof(T) == 4) cur.p[e].w[i + 1] = was.w[i + 1];
+              cur.p[e].w[i * sizeof(T) / 4] = was.w[i * sizeof(T) / 4];
+            }
+        }
+        raw_store<16>(y + cp, cur.p[e]);
+      } else {
+        if (turns) {
+          const float u = to_f<T>(cur.sp[e]), v = to_f<T>(cur.sq[e]);
+          y[cp] = from_f<T>(u * w[0].x - v * w[0].y);
+          y[cq] = from_f<T>(u * w[0].y + v * w[0].x);
+        } else {
+          y[cp] = cur.sp[e];
+        }
+      }
+    }
+    cur = next;
+  }
+}
+
+template <typename T, int MODE>
+void rotary_launch(const RotaryArgs& a, cudaStream_t st) {
+  const int units = rotary_units<T, MODE>(a.d, a.rot), tokens = kRThreads / units;   // units <= 256
+  const int tiles = ceil_div(a.B * a.N, tokens), all = a.heads + a.heads2;
+  // Heads are split over blocks, which form the angles once each (worth about three heads): as many parts as give
+  // the shortest run of whole waves, three blocks an SM at a time (4 x 4096 tokens, 32 heads: one part 57 us in
+  // 1.5 waves, two 51 us in 3).
+  int each = all;
+  long long best = 0;
+  for (int parts = 1; parts <= all; ++parts) {
+    const int e = ceil_div(all, parts);
+    const long long waves = ((long long)tiles * ceil_div(all, e) + kWave - 1) / kWave, cost = waves * (e + 3);
+    if (best == 0 || cost < best) {
+      best = cost;
+      each = e;
+    }
+  }
+  k_rotary<T, MODE><<<dim3(tiles, ceil_div(all, each)), kRThreads, 0, st>>>(a, units, tokens, each);
+}
+template <typename T>
+void run_rotary(const RotaryArgs& a, cudaStream_t st) {
+  if (a.interleaved)
+    rotary_launch<T, 1>(a, st);
+  else if ((a.rot / 2) % (16 / (int)sizeof(T)) == 0)
+    rotary_launch<T, 0>(a, st);
+  else
+    rotary_launch<T, 2>(a, st);
+}
+
+// ---- group norm ---------------------------------------------------------------------------------------
+// Two ways through the data. Small groups (N C/G elements that one warp or one block holds in registers) are read
+// once: a team of threads per (sample, group) forms the mean, the variance about it and the output. Larger ones
+// take three launches: per-channel sums of row chunks, their combination per group, and the output; the second
+// reading comes from the 126 MB L2 as far as the tensor fits there. All sums are joined in a fixed order.
+constexpr int kNT = 256;         // threads per block
+constexpr int kNRows = 8;        // rows a thread has in flight
+constexpr int kNormWave = 4 * 148;   // blocks that run at once
+constexpr int kMaxChunks = 64;   // row chunks per sample (large groups)
+
+// 1 / (1 + exp(-z)): exponent and reciprocal within 2 units each (2^-22 relative)
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
+  const uint64_t t = mul2(z, both(-1.4426950408889634f));
+  const uint64_t d = add2(f2(sm100::ex2_approx(f2_lo(t)), sm100::ex2_approx(f2_hi(t))), both(1.f));
+  return f2(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d)));
+}
+__device__ __forceinline__ uint64_t normal_cdf2(uint64_t z) {   // 0.5 (1 + erf(z / sqrt 2))
+  return f2(fmaf(0.5f, erff(f2_lo(z) * 0.70710678118654752f), 0.5f), fmaf(0.5f, erff(f2_hi(z) * 0.70710678118654752f), 0.5f));
+}
+template <int ACT>
+__device__ __forceinline__ uint64_t act2(uint64_t z) {
+  if (ACT == LFA_ACT_SILU) return mul2(z, sigmoid2(z));
+  if (ACT == LFA_ACT_GELU) return mul2(z, normal_cdf2(z));
+  return z;
+}
+template <int ACT>
+__device__ __forceinline__ uint64_t slope2(uint64_t z) {
+  if (ACT == LFA_ACT_SILU) {   // p + z p (1 - p)
+    const uint64_t p = sigmoid2(z);
+    return fma2(mul2(z, p), fma2(p, both(-1.f), both(1.f)), p);
+  }
+  if (ACT == LFA_ACT_GELU) {
+    const uint64_t t = mul2(mul2(z, z), both(-0.72134752044448170f));
+    const uint64_t e = f2(sm100::ex2_approx(f2_lo(t)), sm100::ex2_approx(f2_hi(t)));
+    return fma2(mul2(z, both(0.3989422804014327f)), e, normal_cdf2(z));
+  }
+  return both(1.f);
+}
+
 // V values from channel c on of an fp32 array (`none` without one), in pairs; a single one has a zero beside it
 template <int V>
 __device__ __forceinline__ void load_pairs(const float* p, int c, float none, uint64_t* o) {
