@@ -753,6 +753,56 @@ __device__ __forceinline__ void chan_stats(const NormArgs& a, int b, int c, int 
   }
 }
 
+// A thread's next rows, kAhead of one or two tensors, on their way into slots of its own in shared memory: registers
+// for them would cost blocks on the SM (one row pair at a time in registers: 28 us where this takes 21; 32 x 3136 x 256).
+constexpr int kAhead = 4;
+template <int VB>
+__device__ __forceinline__ void stage_row(void* slot, const void* from) {
+  if constexpr (VB == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_u32(slot)), "l"(from) : "memory");
+  else if constexpr (VB >= 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(sm100::smem_u32(slot)), "l"(from), "n"(VB) : "memory");
+  else
+    *reinterpret_cast<uint16_t*>(slot) = *reinterpret_cast<const uint16_t*>(from);
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// f(row, a's raw vector, b's) for the rows of this thread, in order (NB 1: a alone)
+template <int VB, int NB, typename F>
+__device__ __forceinline__ void for_rows(const Lane& l, int rl, int C, int es, const void* a, const void* b, float* sm, F f) {
+  char* slots = reinterpret_cast<char*>(sm) + threadIdx.x * VB;
+  const int first = l.r0 + l.ty;
+  const size_t step = (size_t)rl * C * es;
+  const char* pa = static_cast<const char*>(a) + (size_t)first * C * es;
+  const char* pb = static_cast<const char*>(b) + (size_t)first * C * es;
+  int ahead = first, in = 0, out = 0;   // next row to fetch, and the slots of fetching and reading
+  auto fetch = [&]() {
+    if (ahead < l.r1) {
+      stage_row<VB>(slots + in * kNT * VB, pa);
+      if (NB == 2) stage_row<VB>(slots + (kAhead + in) * kNT * VB, pb);
+      pa += step;
+      pb += step;
+      ahead += rl;
+    }
+    stage_commit();
+    in = (in + 1) % kAhead;
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) fetch();
+  for (int r = first; r < l.r1; r += rl) {
+    fetch();
+    stage_wait<kAhead - 1>();
+    const Raw<VB> va = raw_load<VB>(slots + out * kNT * VB);
+    Raw<VB> vb = va;
+    if (NB == 2) vb = raw_load<VB>(slots + (kAhead + out) * kNT * VB);
+    out = (out + 1) % kAhead;
+    f(r, va, vb);
+  }
+  stage_wait<0>();
+}
+
 template <typename T, int VB, int ACT, bool ONE>
 __global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_norm_apply(const __grid_constant__ RowArgs p) {
   constexpr int V = VB / sizeof(T), NP = (V + 1) / 2;
@@ -787,7 +837,6 @@ __global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_nor
 template <typename T, int VB, int ACT, bool ONE, bool FLAT>
 __global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_norm_bsum(const __grid_constant__ RowArgs p) {
   constexpr int V = VB / sizeof(T);
-  constexpr int R = 2;   // rows in flight, of two tensors; four blocks an SM cover the rest
   extern __shared__ float sm[];
   const NormArgs& a = p.a;
   const int dg = a.C / a.G;
@@ -805,34 +854,24 @@ __global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_nor
     const size_t base = (size_t)l.b * a.N * a.C + l.c;
     const T* x = static_cast<const T*>(a.x) + base;
     const T* dy = static_cast<const T*>(a.dy) + base;
-    for (int r = l.r0 + l.ty; r < l.r1; r += p.rl * R) {
-      Raw<VB> v[R], w[R];
+    for_rows<VB, 2>(l, p.rl, a.C, sizeof(T), x, dy, sm, [&](int r, const Raw<VB>& v, const Raw<VB>& w) {
+      if (FLAT) chan_stats<V, ONE>(a, r / a.N, l.c, dg, k);
 #pragma unroll
-      for (int e = 0; e < R; ++e)
-        if (r + e * p.rl < l.r1) {
-          v[e] = raw_load<VB>(x + (size_t)(r + e * p.rl) * a.C);
-          w[e] = raw_load<VB>(dy + (size_t)(r + e * p.rl) * a.C);
-        }
-#pragma unroll
-      for (int e = 0; e < R; ++e)
-        if (r + e * p.rl < l.r1) {
-          if (FLAT) chan_stats<V, ONE>(a, (r + e * p.rl) / a.N, l.c, dg, k);
-#pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            uint64_t d = add2(raw_pair<T>(v[e], i), k.nm[i]);
-            if (FLAT) d = mul2(d, k.rs[i]);
-            const uint64_t dz = mul2(raw_pair<T>(w[e], i), slope2<ACT>(fma2(d, k.ga[i], k.be[i])));
-            s1[i] = add2(s1[i], dz);
-            s2[i] = fma2(dz, d, s2[i]);
-          }
-        }
-    }
+      for (int i = 0; i < NP; ++i) {
+        uint64_t d = add2(raw_pair<T>(v, i), k.nm[i]);
+        if (FLAT) d = mul2(d, k.rs[i]);
+        const uint64_t dz = mul2(raw_pair<T>(w, i), slope2<ACT>(fma2(d, k.ga[i], k.be[i])));
+        s1[i] = add2(s1[i], dz);
+        s2[i] = fma2(dz, d, s2[i]);
+      }
+    });
     if (!FLAT)
 #pragma unroll
       for (int i = 0; i < NP; ++i) s2[i] = mul2(s2[i], k.rs[i]);
   }
   const int width = p.cw * V, at = l.ty * width + (threadIdx.x % p.cw) * V;
   float* sq = sm + p.rl * width;
+  __syncthreads();   // the rows' slots are done with
   if (l.ty < p.rl)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -904,7 +943,7 @@ __global__ void __launch_bounds__(kNT) k_norm_bjoin(const __grid_constant__ RowA
 template <typename T, int VB, int ACT, bool ONE>
 __global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_norm_dx(const __grid_constant__ RowArgs p, const float* m12) {
   constexpr int V = VB / sizeof(T), NP = (V + 1) / 2;
-  constexpr int R = 2;
+  extern __shared__ float sm[];
   const NormArgs& a = p.a;
   const int dg = a.C / a.G;
   const Lane l = lane_of<V>(p, a.N);
@@ -924,27 +963,16 @@ __global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_nor
   const T* x = static_cast<const T*>(a.x) + base;
   const T* dy = static_cast<const T*>(a.dy) + base;
   T* dx = static_cast<T*>(a.y) + base;
-  for (int r = l.r0 + l.ty; r < l.r1; r += p.rl * R) {
-    Raw<VB> v[R], w[R];
+  for_rows<VB, 2>(l, p.rl, a.C, sizeof(T), x, dy, sm, [&](int r, const Raw<VB>& v, const Raw<VB>& w) {
+    uint64_t o[NP];
 #pragma unroll
-    for (int e = 0; e < R; ++e)
-      if (r + e * p.rl < l.r1) {
-        v[e] = raw_load<VB>(x + (size_t)(r + e * p.rl) * a.C);
-        w[e] = raw_load<VB>(dy + (size_t)(r + e * p.rl) * a.C);
-      }
-#pragma unroll
-    for (int e = 0; e < R; ++e)
-      if (r + e * p.rl < l.r1) {
-        uint64_t o[NP];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const uint64_t xh = mul2(add2(raw_pair<T>(v[e], i), k.nm[i]), k.rs[i]);
-          const uint64_t d = mul2(mul2(k.ga[i], raw_pair<T>(w[e], i)), slope2<ACT>(fma2(xh, k.ga[i], k.be[i])));
-          o[i] = mul2(k.rs[i], fma2(xh, m2[i], add2(d, m1[i])));
-        }
-        raw_store<VB>(dx + (size_t)(r + e * p.rl) * a.C, raw_make<T, VB>(o));
-      }
-  }
+    for (int i = 0; i < NP; ++i) {
+      const uint64_t xh = mul2(add2(raw_pair<T>(v, i), k.nm[i]), k.rs[i]);
+      const uint64_t d = mul2(mul2(k.ga[i], raw_pair<T>(w, i)), slope2<ACT>(fma2(xh, k.ga[i], k.be[i])));
+      o[i] = mul2(k.rs[i], fma2(xh, m2[i], add2(d, m1[i])));
+    }
+    raw_store<VB>(dx + (size_t)r * a.C, raw_make<T, VB>(o));
+  });
 }
 
 // ---- choice of the way, by sizes alone -----------------------------------------------------------------
@@ -1050,6 +1078,11 @@ void small_backward(const Plan& p, cudaStream_t st) {
 }
 template <typename T, int VB>
 size_t row_smem(const RowArgs& r) { return 2 * sizeof(float) * r.rl * r.cw * (VB / sizeof(T)); }
+template <typename T, int VB>
+size_t ahead_smem(const RowArgs& r) {   // the rows' slots, and the sums that follow there
+  const size_t slots = 2 * kAhead * kNT * VB, sums = row_smem<T, VB>(r);
+  return slots > sums ? slots : sums;
+}
 
 template <typename T, int VB, int ACT>
 void large_forward(const Plan& p, cudaStream_t st) {
@@ -1067,9 +1100,9 @@ void channel_sums(const Plan& p, cudaStream_t st) {
   const RowArgs& r = p.r;
   const dim3 grid(r.chunks * (FLAT ? 1 : r.a.B), r.colblocks);
   if (r.a.C / r.a.G % (VB / sizeof(T)) == 0)
-    k_norm_bsum<T, VB, ACT, true, FLAT><<<grid, kNT, row_smem<T, VB>(r), st>>>(r);
+    k_norm_bsum<T, VB, ACT, true, FLAT><<<grid, kNT, ahead_smem<T, VB>(r), st>>>(r);
   else
-    k_norm_bsum<T, VB, ACT, false, FLAT><<<grid, kNT, row_smem<T, VB>(r), st>>>(r);
+    k_norm_bsum<T, VB, ACT, false, FLAT><<<grid, kNT, ahead_smem<T, VB>(r), st>>>(r);
   const int groups = FLAT ? 0 : r.a.B * r.a.G, chan = r.a.dgamma ? ceil_div(r.a.C, 8) : 0;
   k_norm_bjoin<<<groups + chan, kNT, 0, st>>>(r, groups, (FLAT ? 1 : r.a.B) * r.chunks, r.a.ws + p.m12);
 }
@@ -1078,9 +1111,9 @@ void large_backward(const Plan& p, cudaStream_t st) {
   channel_sums<T, VB, ACT, false>(p, st);
   const dim3 grid(p.r.chunks * p.r.a.B, p.r.colblocks);
   if (p.r.a.C / p.r.a.G % (VB / sizeof(T)) == 0)
-    k_norm_dx<T, VB, ACT, true><<<grid, kNT, 0, st>>>(p.r, p.r.a.ws + p.m12);
+    k_norm_dx<T, VB, ACT, true><<<grid, kNT, ahead_smem<T, VB>(p.r), st>>>(p.r, p.r.a.ws + p.m12);
   else
-    k_norm_dx<T, VB, ACT, false><<<grid, kNT, 0, st>>>(p.r, p.r.a.ws + p.m12);
+    k_norm_dx<T, VB, ACT, false><<<grid, kNT, ahead_smem<T, VB>(p.r), st>>>(p.r, p.r.a.ws + p.m12);
 }
 
 // f.template operator()<T, VB, ACT>() for the vector's bytes and the activation
