@@ -163,26 +163,14 @@ __global__ void __launch_bounds__(kRThreads, 3) k_rotary(const __grid_constant__
         raw_store<16>(y + cp, cur.p[e]);
         if (two) raw_store<16>(y + cq, cur.q[e]);
       } else if constexpr (MODE == 1) {
-        float o[V];
-#pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          const float u = raw_get<T>(cur.p[e], i), v = raw_get<T>(cur.p[e], i + 1);
-          const float2 z = w[i / 2];
-          o[i] = u * z.x - v * z.y;
-          o[i + 1] = u * z.y + v * z.x;
-        }
-        const Raw<16> was = cur.p[e];
         if (turns) {
-          uint64_t o2[V / 2];
+          uint64_t o[V / 2];
 #pragma unroll
-          for (int i = 0; i < V / 2; ++i) o2[i] = f2(o[2 * i], o[2 * i + 1]);
-          cur.p[e] = raw_make<T, 16>(o2);
-#pragma unroll
-          for (int i = 0; i < V; i += 2)   // channels behind rot stay as they are, bit by bit
-            if (cp + i >= a.rot) {
-              if constexpr (sizeof(T) == 4) cur.p[e].w[i + 1] = was.w[i + 1];
-              cur.p[e].w[i * sizeof(T) / 4] = was.w[i * sizeof(T) / 4];
-            }
+          for (int i = 0; i < V / 2; ++i) {   // channels behind rot stay as they are, bit by bit
+            const uint64_t u = raw_pair<T>(cur.p[e], i);
+            o[i] = pair + i < half ? fma2(u, both(w[i].x), mul2(f2(f2_hi(u), f2_lo(u)), f2(-w[i].y, w[i].y))) : u;
+          }
+          cur.p[e] = raw_make<T, 16>(o);
         }
         raw_store<16>(y + cp, cur.p[e]);
       } else {
@@ -806,6 +794,7 @@ __device__ __forceinline__ void for_rows(const Lane& l, int rl, int C, int es, c
 template <typename T, int VB, int ACT, bool ONE>
 __global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_norm_apply(const __grid_constant__ RowArgs p) {
   constexpr int V = VB / sizeof(T), NP = (V + 1) / 2;
+  extern __shared__ float sm[];
   const NormArgs& a = p.a;
   const Lane l = lane_of<V>(p, a.N);
   if (!l.on) return;
@@ -817,20 +806,12 @@ __global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_nor
   const size_t base = (size_t)l.b * a.N * a.C + l.c;
   const T* x = static_cast<const T*>(a.x) + base;
   T* y = static_cast<T*>(a.y) + base;
-  for (int r = l.r0 + l.ty; r < l.r1; r += p.rl * kNRows) {
-    Raw<VB> v[kNRows];
+  for_rows<VB, 1>(l, p.rl, a.C, sizeof(T), x, x, sm, [&](int r, const Raw<VB>& v, const Raw<VB>&) {
+    uint64_t o[NP];
 #pragma unroll
-    for (int e = 0; e < kNRows; ++e)
-      if (r + e * p.rl < l.r1) v[e] = raw_load<VB>(x + (size_t)(r + e * p.rl) * a.C);
-#pragma unroll
-    for (int e = 0; e < kNRows; ++e)
-      if (r + e * p.rl < l.r1) {
-        uint64_t o[NP];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) o[i] = act2<ACT>(fma2(add2(raw_pair<T>(v[e], i), k.nm[i]), k.ga[i], k.be[i]));
-        raw_store<VB>(y + (size_t)(r + e * p.rl) * a.C, raw_make<T, VB>(o));
-      }
-  }
+    for (int i = 0; i < NP; ++i) o[i] = act2<ACT>(fma2(add2(raw_pair<T>(v, i), k.nm[i]), k.ga[i], k.be[i]));
+    raw_store<VB>(y + (size_t)r * a.C, raw_make<T, VB>(o));
+  });
 }
 
 // per-channel sums of dz and dz xhat over a chunk's rows: of one sample, or (FLAT) of all samples' rows in turn
@@ -1091,9 +1072,9 @@ void large_forward(const Plan& p, cudaStream_t st) {
   k_norm_stats<T, VB><<<grid, kNT, row_smem<T, VB>(r), st>>>(r);
   k_norm_group<<<r.a.B * r.a.G, kNT, 0, st>>>(r);
   if (r.a.C / r.a.G % (VB / sizeof(T)) == 0)
-    k_norm_apply<T, VB, ACT, true><<<grid, kNT, 0, st>>>(r);
+    k_norm_apply<T, VB, ACT, true><<<grid, kNT, kAhead * kNT * VB, st>>>(r);
   else
-    k_norm_apply<T, VB, ACT, false><<<grid, kNT, 0, st>>>(r);
+    k_norm_apply<T, VB, ACT, false><<<grid, kNT, kAhead * kNT * VB, st>>>(r);
 }
 template <typename T, int VB, int ACT, bool FLAT>
 void channel_sums(const Plan& p, cudaStream_t st) {
