@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(4 * CB) k_decay_core(const __grid_constant__ C
   constexpr int NT = 4 * CB, TJ = CB / 4, NQ = kCC / TJ;
   const DecayArgs& a = ca.a;
   const int jx = blockIdx.z % a.njobs, seg = blockIdx.z / a.njobs;
+  if (STATE) let_next_start();
   const DecayJob& jb = a.job[jx];
   const int c0 = blockIdx.y * CB, u = blockIdx.x, b = u / a.heads, h = u % a.heads, t = threadIdx.x;
   if (c0 >= jb.db) return;
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(4 * CB) k_decay_core(const __grid_constant__ C
     const float* src = STATE ? nullptr : split ? ca.seg_init[jx] : jb.init;
     const size_t at = split ? ((size_t)u * ca.segs + seg) * dd : u * dd;
     const float f0 = L > 0 && !split && jb.init_decays ? expf(ld) : 1.f;
+    if (!STATE) wait_for_previous();
     float4 v[DA * TJ / NT];   // read together
 #pragma unroll
     for (int i = 0; i < DA * TJ / NT; ++i) {
@@ -340,7 +342,9 @@ cudaError_t run_core(const CoreArgs& c, int db, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = raise_smem(k_decay_core<DA, STATE>, bytes, done);
   if (e != cudaSuccess) return e;
-  k_decay_core<DA, STATE><<<dim3(c.a.B * c.a.heads, ceil_div(db, CB), c.a.njobs * c.segs), 4 * CB, bytes, st>>>(c);
+  const dim3 grid(c.a.B * c.a.heads, ceil_div(db, CB), c.a.njobs * c.segs);
+  if (!STATE && c.segs > 1) return launch_next(k_decay_core<DA, STATE>, grid, 4 * CB, bytes, st, c);
+  k_decay_core<DA, STATE><<<grid, 4 * CB, bytes, st>>>(c);
   return cudaGetLastError();
 }
 template <bool STATE>

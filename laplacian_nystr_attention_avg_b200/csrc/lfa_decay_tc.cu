@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   const int da = jb.da, db = jb.db;
   const bool rev = jb.rev;
   const size_t dd = (size_t)da * db;
+  if (STATE) let_next_start();
   if (n <= 0) {
     if (!STATE && L == 0 && seg == 0 && jb.fin)
       for (size_t e = t; e < dd; e += C::kThreads) jb.fin[u * dd + e] = jb.init ? jb.init[u * dd + e] : 0.f;
@@ -525,6 +526,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
     uint64_t R[NR / 2];   // pairs of columns
     {
       const float* src = STATE ? nullptr : a.segs > 1 ? jb.seg_init : jb.init;
+      if (!STATE) wait_for_previous();   // for the segments' states; q, k, v, ... were there before them
       const float f0 = (a.segs > 1 || !jb.init_decays) ? 1.f : expf(ld);
       const size_t at = (a.segs > 1 ? (size_t)u * a.segs + seg : (size_t)u) * dd;
 #pragma unroll
@@ -672,6 +674,8 @@ struct PrefixArgs {
 };
 __global__ void __launch_bounds__(64) k_decay_prefix(const __grid_constant__ PrefixArgs a) {
   const int u = blockIdx.x, j = blockIdx.z, e = (blockIdx.y * 64 + threadIdx.x) * 4;
+  let_next_start();
+  wait_for_previous();
   if (e >= a.dd) return;
   const int L = unit_length(a.lengths, u / a.heads, a.N), nch = (L + kC - 1) / kC;
   const int segs = (nch + a.seg_chunks - 1) / a.seg_chunks, span = a.seg_chunks * kC;
@@ -719,7 +723,12 @@ cudaError_t run(const TcArgs& a, int units, int njobs, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = raise_smem(k_decay_tc<DP, STATE>, C::kSmem, done);
   if (e != cudaSuccess) return e;
-  k_decay_tc<DP, STATE><<<dim3(units, a.segs, njobs), C::kThreads, C::kSmem, st>>>(a);
+  const dim3 grid(units, a.segs, njobs);
+  // A forward's blocks set up and read their first tokens while the states are joined (1 x 8 x 65536 tokens: 108 ->
+  // 103 us). Not a backward's: three runs have more blocks than the states' two, and those that come up early on the
+  // SMs left free cost more than they win (289 us, 253 one after the other).
+  if (!STATE && a.segs > 1 && njobs == 1) return launch_next(k_decay_tc<DP, STATE>, grid, C::kThreads, C::kSmem, st, a);
+  k_decay_tc<DP, STATE><<<grid, C::kThreads, C::kSmem, st>>>(a);
   return cudaGetLastError();
 }
 template <bool STATE>
@@ -763,8 +772,7 @@ cudaError_t launch_prefix(const DecayArgs& a, const DecaySplit& sp, const Prefix
   p.segs = sp.segs;
   p.seg_chunks = sp.seg_chunks;
   p.dd = a.job[0].da * a.job[0].db;
-  k_decay_prefix<<<dim3(a.B * a.heads, ceil_div(p.dd, 256), n), 64, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_next(k_decay_prefix, dim3(a.B * a.heads, ceil_div(p.dd, 256), n), 64, 0, st, p);
 }
 
 size_t decay_workspace_floats(int B, int heads, int N, int dk, int dv, int njobs, int dtype) {

@@ -120,6 +120,25 @@ inline cudaError_t raise_smem(K kernel, int bytes, std::atomic<unsigned long lon
   return e;
 }
 
+// Kernels of one call that follow one another: the next one's blocks come up while the last of the one before run
+// (which says when, with let_next_start) and wait for its end and its results in wait_for_previous.
+template <typename... P, typename... A>
+inline cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t c = {};
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- small device helpers shared by the two files -------------------------------------------------
 // decays below exp(-1e4) are zero to every power but 0; the bound keeps 0 * inf out of exp(n ld)
 __device__ __forceinline__ float decay_log(float ld) { return ld < -1e4f ? -1e4f : ld; }

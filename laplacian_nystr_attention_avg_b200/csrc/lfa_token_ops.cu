@@ -94,7 +94,7 @@ __host__ __device__ __forceinline__ int rotary_units(int d, int rot) {
 }
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kRThreads, 3) k_rotary(const __grid_constant__ RotaryArgs a, int units, int tokens,
+__global__ void __launch_bounds__(kRThreads, MODE == 0 ? 3 : 5) k_rotary(const __grid_constant__ RotaryArgs a, int units, int tokens,
                                                       int heads_each) {
   constexpr int V = 16 / sizeof(T), NP = MODE == 0 ? V : MODE == 1 ? V / 2 : 1;   // pairs of a unit
   const int tl = threadIdx.x / units, unit = threadIdx.x - tl * units, tok = blockIdx.x * tokens + tl;
@@ -621,6 +621,7 @@ __global__ void __launch_bounds__(kNT) k_norm_stats(const __grid_constant__ RowA
   const Lane l = lane_of<V>(p, a.N);
   float m[V] = {}, q[V] = {};
   int cnt = 0;
+  let_next_start();
   if (l.on) {
     const T* x = static_cast<const T*>(a.x) + (size_t)l.b * a.N * a.C + l.c;
     for (int r = l.r0 + l.ty; r < l.r1; r += p.rl * kNRows) {
@@ -690,6 +691,8 @@ __global__ void __launch_bounds__(kNT) k_norm_group(const __grid_constant__ RowA
   const int b = blockIdx.x / a.G, g = blockIdx.x % a.G, dg = a.C / a.G, cells = p.chunks * dg;
   const float* part = p.part + (size_t)b * p.chunks * 2 * a.C + g * dg;
   const float total = (float)a.N * (float)dg;
+  let_next_start();
+  wait_for_previous();
   float s = 0.f;
   for (int e = threadIdx.x; e < cells; e += kNT) {
     const int k = e / dg;
@@ -800,6 +803,7 @@ __global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_nor
   if (!l.on) return;
   Chan<V> k;
   chan_affine(a, l.c, k);
+  wait_for_previous();
   chan_stats<V, ONE>(a, l.b, l.c, a.C / a.G, k);
 #pragma unroll
   for (int i = 0; i < NP; ++i) k.ga[i] = mul2(k.ga[i], k.rs[i]);
@@ -824,6 +828,7 @@ __global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_nor
   const Lane l = lane_of<V>(p, FLAT ? a.B * a.N : a.N);
   constexpr int NP = (V + 1) / 2;
   uint64_t s1[NP] = {}, s2[NP] = {};   // of dz, and of dz (x - mean) (FLAT: dz xhat)
+  let_next_start();
   if (l.on) {
     Chan<V> k;
     chan_affine(a, l.c, k);
@@ -880,6 +885,8 @@ __global__ void __launch_bounds__(kNT) k_norm_bjoin(const __grid_constant__ RowA
                                                      float* m12) {
   __shared__ float red[2][kNT];
   const NormArgs& a = p.a;
+  let_next_start();
+  wait_for_previous();
   if ((int)blockIdx.x < groups) {
     const int b = blockIdx.x / a.G, g = blockIdx.x % a.G, dg = a.C / a.G, cells = p.chunks * dg;
     const float* part = p.part + (size_t)b * p.chunks * 2 * a.C + g * dg;
@@ -932,6 +939,7 @@ __global__ void __launch_bounds__(kNT, ONE && ACT != LFA_ACT_GELU ? 4 : 2) k_nor
   Chan<V> k;
   chan_affine(a, l.c, k);
   chan_stats<V, ONE>(a, l.b, l.c, dg, k);
+  wait_for_previous();
   uint64_t m1[NP], m2[NP];   // minus the group's means of gamma dz and of gamma dz xhat
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
@@ -1070,11 +1078,11 @@ void large_forward(const Plan& p, cudaStream_t st) {
   const RowArgs& r = p.r;
   const dim3 grid(r.chunks * r.a.B, r.colblocks);
   k_norm_stats<T, VB><<<grid, kNT, row_smem<T, VB>(r), st>>>(r);
-  k_norm_group<<<r.a.B * r.a.G, kNT, 0, st>>>(r);
+  launch_next(k_norm_group, r.a.B * r.a.G, kNT, 0, st, r);
   if (r.a.C / r.a.G % (VB / sizeof(T)) == 0)
-    k_norm_apply<T, VB, ACT, true><<<grid, kNT, kAhead * kNT * VB, st>>>(r);
+    launch_next(k_norm_apply<T, VB, ACT, true>, grid, kNT, kAhead * kNT * VB, st, r);
   else
-    k_norm_apply<T, VB, ACT, false><<<grid, kNT, kAhead * kNT * VB, st>>>(r);
+    launch_next(k_norm_apply<T, VB, ACT, false>, grid, kNT, kAhead * kNT * VB, st, r);
 }
 template <typename T, int VB, int ACT, bool FLAT>
 void channel_sums(const Plan& p, cudaStream_t st) {
@@ -1085,16 +1093,16 @@ void channel_sums(const Plan& p, cudaStream_t st) {
   else
     k_norm_bsum<T, VB, ACT, false, FLAT><<<grid, kNT, ahead_smem<T, VB>(r), st>>>(r);
   const int groups = FLAT ? 0 : r.a.B * r.a.G, chan = r.a.dgamma ? ceil_div(r.a.C, 8) : 0;
-  k_norm_bjoin<<<groups + chan, kNT, 0, st>>>(r, groups, (FLAT ? 1 : r.a.B) * r.chunks, r.a.ws + p.m12);
+  launch_next(k_norm_bjoin, groups + chan, kNT, 0, st, r, groups, (FLAT ? 1 : r.a.B) * r.chunks, r.a.ws + p.m12);
 }
 template <typename T, int VB, int ACT>
 void large_backward(const Plan& p, cudaStream_t st) {
   channel_sums<T, VB, ACT, false>(p, st);
   const dim3 grid(p.r.chunks * p.r.a.B, p.r.colblocks);
   if (p.r.a.C / p.r.a.G % (VB / sizeof(T)) == 0)
-    k_norm_dx<T, VB, ACT, true><<<grid, kNT, ahead_smem<T, VB>(p.r), st>>>(p.r, p.r.a.ws + p.m12);
+    launch_next(k_norm_dx<T, VB, ACT, true>, grid, kNT, ahead_smem<T, VB>(p.r), st, p.r, p.r.a.ws + p.m12);
   else
-    k_norm_dx<T, VB, ACT, false><<<grid, kNT, ahead_smem<T, VB>(p.r), st>>>(p.r, p.r.a.ws + p.m12);
+    launch_next(k_norm_dx<T, VB, ACT, false>, grid, kNT, ahead_smem<T, VB>(p.r), st, p.r, p.r.a.ws + p.m12);
 }
 
 // f.template operator()<T, VB, ACT>() for the vector's bytes and the activation
