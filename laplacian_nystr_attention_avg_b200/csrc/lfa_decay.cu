@@ -23,9 +23,11 @@ namespace {
 // A block takes CB columns of one segment of a unit's tokens and walks it 64 tokens at a time, everything staged in
 // shared memory; the state R [da][CB] lives there. A thread has a 4 x 4 tile of each product, which makes 64
 // multiply-adds per eight 16-byte reads; above the diagonal nothing is computed, by the rows of a warp.
-// STATE: the segment's own state only.
+// STATE: the segment's own state only. Bound by the fp32 multiply-adds and the shared-memory reads that feed them
+// (64 units x 784 tokens, dk 32, dv 64: 69 us in three launches, issue slots half full, two blocks an SM; at three,
+// with 80 registers, 64 us, but the backward 245 instead of 192). Not taken: 32 columns a block (174 us), operands
+// transposed for packed multiply-adds (75 us beside 58 in the main launch alone).
 constexpr int kCC = 64;   // tokens per step
-
 constexpr int CB = 64;    // columns of z a block takes
 
 template <int DA>
@@ -57,7 +59,7 @@ struct CoreArgs {
 };
 
 template <int DA, bool STATE>
-__global__ void __launch_bounds__(4 * CB) k_decay_core(const __grid_constant__ CoreArgs ca) {
+__global__ void __launch_bounds__(4 * CB, DA == 128 ? 1 : 2) k_decay_core(const __grid_constant__ CoreArgs ca) {
   extern __shared__ float4 smem_f4[];
   CoreSmem<DA>& s = *reinterpret_cast<CoreSmem<DA>*>(smem_f4);
   constexpr int NT = 4 * CB, TJ = CB / 4, NQ = kCC / TJ;
@@ -267,7 +269,9 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float4 v
 
 // ---- one token --------------------------------------------------------------------------------------
 // One CTA per (row, head): S [dk][dv] is read and written once, columns across the lanes (float4), rows across
-// the warps; o = scale q S' from the warps' partial sums, joined in shared memory in a fixed order.
+// the warps; o = scale q S' from the warps' partial sums, joined in shared memory in a fixed order. Bound by the
+// state's bytes: 192 rows x 16 heads of 128 x 128 (406 MB) in 62.5 us, 6.5 TB/s, the copy bandwidth. A row's slot is
+// compared with those of all rows before it, so that two rows never write one state.
 constexpr int kStepT = 256;
 
 template <typename T>
@@ -354,7 +358,7 @@ cudaError_t run_core(const CoreArgs& c, cudaStream_t st) {
     da = c.a.job[j].da > da ? c.a.job[j].da : da;
     db = c.a.job[j].db > db ? c.a.job[j].db : db;
   }
-  return da <= 64 ? run_core<64, STATE>(c, db, st) : run_core<128, STATE>(c, db, st);
+  return da <= 32 ? run_core<32, STATE>(c, db, st) : da <= 64 ? run_core<64, STATE>(c, db, st) : run_core<128, STATE>(c, db, st);
 }
 
 cudaError_t launch_core(const DecayArgs& a, cudaStream_t st) {

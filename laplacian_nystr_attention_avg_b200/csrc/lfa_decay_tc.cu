@@ -7,14 +7,21 @@
 //   Oz = P z,  Ox = x bf16(R)               (M 128, N db; K 128 and K da)
 //   O  = Oz + c_inter l^i Ox                (epilogue warps, fp32, rounded once)
 //   D  = (y c_state l^(n-j))^T z            (M da, N db, K 128 tokens), R' = l^n R + D   (state warps)
-// The decayed rows of y enter as two bf16 parts (value and remainder, one product each: about 2^-17; a third part
-// left 1.4e-6 instead of 3.9e-6 of a state's norm, the rest being the tensor cores' own sums, and cost 16 to 20 % of
-// the time). D starts from zero in every chunk and is added to R by CUDA cores: tensor-core accumulation truncates
-// and would drift over thousands of chunks. All widths are padded to DP = 64 or 128 by TMA's zero fill.
+// The decayed rows of y enter as two bf16 parts (value and remainder, one product each): a state is 3.9e-6 of its norm
+// off, after 8 tokens as after 4096, beside the 2^-8 of every bf16 output that is read from it (a third part left
+// 1.4e-6, the rest being the tensor cores' own sums, and cost 16 to 20 % of the time). D starts from zero in every
+// chunk and is added to R by CUDA cores: tensor-core accumulation truncates and would drift over thousands of chunks.
+// All widths are padded to DP = 64 or 128 by TMA's zero fill.
 //
 // Warps: 4 or 8 for P, 4 or 8 for y's decayed rows, 8 for R and the epilogue, one each to issue TMA loads, the
 // products of the state and those of the output. Every hand-over is an mbarrier; every wait is bounded (on expiry
 // the device's status word is set, the CTA stops waiting for anything and drains what it has in flight).
+//
+// What bounds it: 128 units x 4096 tokens take 115 us at 128 channels (83 at the copy bandwidth, with 128 of 148 SMs
+// at work; 144 units 116 of 94) and 67 us at 64 channels (42): there a chunk takes 3.0 k cycles, in which issue slots
+// are half full, shared memory 65 % busy and the tensor pipe 32 %, the longest chains being P's warps and D -> R -> D.
+// Not taken: 8 P warps at 128 channels, their registers from the others (117 us); a second set of O instead of the
+// second set of S at 64.
 //
 // Few units over long sequences: segments run at once. k_decay_tc<.., true> sums up each segment's own
 // state, k_decay_prefix carries them over the segments, and the main kernel starts every segment from its state.
@@ -321,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       mbar_init(bars + i, i >= kEmptyY && i < kEmptyX                                    ? C::kYW + (STATE ? 0 : 1)
                           : i >= kEmptyZ && i < kSFull                                   ? (STATE ? 1 : 2)
                           : (i >= kYdReady && i < kPartFree) || i == kZClean             ? C::kYW
-                          : i >= kSRead && i <= kPReady                                  ? (STATE ? 1 : C::kOwnP ? C::kPW - 1 : C::kPW)
+                          : i >= kSRead && i <= kPReady                                  ? (C::kPW ? C::kPW - C::kOwnP : 1)
                           : i == kDRead || i == kRbReady || i == kOFree                  ? 8
                                                                                          : 1);
     mbar_init_fence();
@@ -663,7 +670,8 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   }
 }
 
-// States before each segment from the segments' own sums, in place: st [jobs][units][segs][dd].
+// States before each segment from the segments' own sums, in place: st [jobs][units][segs][dd]. Reads and writes every
+// state once; a few microseconds of launch and latency (8 units x 18 segments of 64 x 64: 7.7 us, 2.4 MB each way).
 struct PrefixArgs {
   float* st;
   const float* init[2];   // state before the run (the forward's S0, the reverse run's dS_out), or null
@@ -741,12 +749,12 @@ cudaError_t run(const TcArgs& a, int dp, int units, int njobs, cudaStream_t st) 
 // bf16: one CTA fills an SM. With fewer than 148 of them the sequences are cut so that about 148 run at once, in
 // segments of at least 4 chunks (below that the extra launches and the second reading of y and z cost more).
 // fp32: blocks of 256 threads share an SM, and arithmetic bounds them, so units of fewer blocks than SMs are cut
-// for two blocks an SM, down to single chunks.
+// for two rounds of two blocks an SM, down to single chunks (64 units x 784 tokens, dk 64: one round 109 us, two 96).
 DecaySplit decay_split(int B, int heads, int N, int njobs, int dtype) {
   const int nch = ceil_div(N, kC);
   const long long ctas = (long long)B * heads * njobs;
   int segs = 1;
-  if (ctas < 148) segs = (int)((dtype == LFA_BF16 ? 148 : 296) / ctas);
+  if (ctas < 148) segs = (int)((dtype == LFA_BF16 ? 148 : 592) / ctas);
   const int most = dtype == LFA_BF16 ? nch / 4 : nch;
   if (segs > most) segs = most;
   if (segs < 1) segs = 1;

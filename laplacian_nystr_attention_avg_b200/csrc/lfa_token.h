@@ -143,7 +143,6 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 // decays below exp(-1e4) are zero to every power but 0; the bound keeps 0 * inf out of exp(n ld)
 __device__ __forceinline__ float decay_log(float ld) { return ld < -1e4f ? -1e4f : ld; }
 
-
 // r exp(x), rounded once for x near 0 and to a relative few 2^-24 everywhere
 struct Decay {
   float em, mul;

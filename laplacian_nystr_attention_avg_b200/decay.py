@@ -143,14 +143,10 @@ def _cur(device: int) -> int:
 _plans = {}
 
 
-def _sig(t):
-    return None if t is None else (t.size(), t.stride(), t.dtype, t.get_device())
-
-
 def _plan(kind, extra, tensors, check):
     """check()'s answer for arguments of these shapes (errors are raised anew each time)."""
     try:
-        key = (kind, extra, tuple([_sig(t) for t in tensors]))
+        key = (kind, extra, *[None if t is None else (t.shape, t.stride(), t.dtype, t.get_device()) for t in tensors])
         plan = _plans.get(key)
     except (AttributeError, TypeError, RuntimeError):
         key = plan = None
