@@ -72,9 +72,10 @@ __device__ __forceinline__ Raw<VB> raw_make(const uint64_t* v) {
 // ---- rotary positions -------------------------------------------------------------------------------
 // Pair i of a token at position p turns by th = p f_i: (a, b) -> mscale (a cos th - b sin th, a sin th + b cos th).
 // th is reduced in turns in 64 bits (p f / 2 pi minus its nearest whole number), so that far positions keep their
-// angle; the rest is fp32. Bound by the bytes: 4 x 4096 tokens, 2 x 16 heads of 128 (268 MB) in 50 us, 5.4 TB/s (a plain
-// copy of them: 47), whether 64, 96 or 128 channels turn. A thread has one token and one unit of a head's channels (V pairs in two 16-byte
-// vectors, V / 2 pairs in one, or a single pair), forms their cosines and sines once, and goes over the heads.
+// angle; the rest is fp32. A thread has one token and one unit of a head's channels (V pairs in two 16-byte vectors,
+// V / 2 pairs in one, or a single pair), forms their cosines and sines once, and goes over the heads.
+// Bound by the bytes: 4 x 4096 tokens, 2 x 16 heads of 128 (268 MB) in 50 us, 5.4 TB/s, whether 64, 96 or 128 channels
+// turn; a plain copy of them takes 47.
 constexpr int kRThreads = 256;
 constexpr int kWave = 3 * 148;   // blocks of 256 threads with 80 registers that run at once
 constexpr int kRHeads = 2;   // heads read at once, one such group ahead
@@ -222,11 +223,12 @@ void run_rotary(const RotaryArgs& a, cudaStream_t st) {
 // once: a team of threads per (sample, group) forms the mean, the variance about it and the output. Larger ones
 // take three launches: per-channel sums of row chunks, their combination per group, and the output; the second
 // reading comes from the 126 MB L2 as far as the tensor fits there. All sums are joined in a fixed order.
-// Measured, bf16 with silu: 8192 x 1024 in 16 groups (33.6 MB) 13 us, 2.6 TB/s, and 65536 rows 63 us, 4.3 TB/s: issue
-// slots 70 % full, exponentials and reciprocals 49 %. Large, 32 x 3136 x 256 in 32 groups (51 MB a tensor): forward
-// 44 us, sums 19 and output 20 of it; backward 56 us, sums 26, output 24. These wait for memory latency and the
-// activation's two special-function instructions per element (half their pipe) in turn; the join is a few
-// microseconds of latency, most of it under the neighbours (three launches apart: 49 and 64 us).
+// Measured, bf16 with silu: 8192 x 1024 in 16 groups (33.6 MB) 13 us, of which a launch and four dependent rounds a
+// warp are most; 65536 rows 59 us, 4.5 TB/s, where exponentials and reciprocals alone take 30 (without silu 46 us,
+// the copy bandwidth). Large, 32 x 3136 x 256 in 32 groups (51 MB a tensor): forward 44 us, sums 19 and output 20 of
+// it; backward 56 us, sums 26, output 24. These wait for memory latency and the activation's two special-function
+// instructions per element (half their pipe) in turn; the join is a few microseconds of latency, most of it under
+// the neighbours (three launches apart: 49 and 64 us).
 constexpr int kNT = 256;         // threads per block
 constexpr int kNRows = 8;        // rows a thread has in flight
 constexpr int kNormWave = 4 * 148;   // blocks that run at once
@@ -393,9 +395,9 @@ template <typename T, int VB, int ACT, bool BACKWARD>
 __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __grid_constant__ SmallArgs s, int teams) {
   constexpr int V = VB / sizeof(T), U = 2;
   const NormArgs& a = s.a;
-  const int tl = threadIdx.x & (s.T - 1), team = blockIdx.x * (kNT / s.T) + threadIdx.x / s.T;
-  const long long total = (long long)a.B * a.G;
-  const int g = team % a.G, dg = a.C / a.G;
+  const int shift = __ffs(s.T) - 1, tl = threadIdx.x & (s.T - 1), team = (int)((blockIdx.x * kNT + threadIdx.x) >> shift);
+  const int total = a.B * a.G;   // up to 2^30, and teams up to 2^28
+  const int b0 = team / a.G, g = team - b0 * a.G, dg = a.C / a.G;
   const bool has = tl < s.nvec;
   long long off;
   int c;
@@ -405,34 +407,44 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
   load_pairs<V>(a.gamma, g * dg + c, 1.f, ga);
   load_pairs<V>(a.beta, g * dg + c, 0.f, be);
   const float n = (float)(s.nvec * V), inv = 1.f / n;
+  const bool two_power = (s.nvec * V & (s.nvec * V - 1)) == 0;   // 1 / n is exact
   const long long step = (long long)(teams / a.G) * a.N * a.C;   // elements from one sample of this thread to its next
-  long long at = (long long)(team / a.G) * a.N * a.C + g * dg + off;
-  const T* x = static_cast<const T*>(a.x);
-  const T* dy = static_cast<const T*>(a.dy);
-  T* y = static_cast<T*>(a.y);
-  // the block's threads stay together (they shuffle), whatever teams still have a sample
+  const long long at = (long long)b0 * a.N * a.C + g * dg + off;
+  const T* x = static_cast<const T*>(a.x) + at;
+  const T* dy = static_cast<const T*>(a.dy) + at;
+  T* y = static_cast<T*>(a.y) + at;
+  // lanes of the team (uniform: a block's threads stay together, whatever teams still have a sample)
+  auto join = [&](float (&v)[U]) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < s.T)
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
+  };
   Raw<VB> nv[U], nw[U];
   float nm[U], nr[U];
-  auto load = [&](long long id, long long from) {   // U samples; zeros where there is none
+  auto load = [&](int id) {   // U samples, and on to the next; zeros where there is none
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long iu = id + (long long)u * teams;
+      const int iu = id + u * teams;
       const bool on = iu < total;
 #pragma unroll
       for (int i = 0; i < (VB + 3) / 4; ++i) nv[u].w[i] = nw[u].w[i] = 0u;
       if (on && has) {
-        nv[u] = raw_load<VB>(x + from + u * step);
-        if (BACKWARD) nw[u] = raw_load<VB>(dy + from + u * step);
+        nv[u] = raw_load<VB>(x);
+        if (BACKWARD) nw[u] = raw_load<VB>(dy);
       }
       if (BACKWARD) {
         nm[u] = on ? a.mean[iu] : 0.f;
         nr[u] = on ? a.rstd[iu] : 0.f;
       }
+      x += step;
+      dy += step;
     }
   };
-  load(team, at);
-  for (long long id0 = (long long)blockIdx.x * (kNT / s.T); id0 < total; id0 += (long long)U * teams, at += U * step) {
-    const long long id = id0 + threadIdx.x / s.T;
+  load(team);
+  int id = team;
+  for (int id0 = (int)(blockIdx.x * kNT) >> shift; id0 < total; id0 += U * teams, id += U * teams, y += U * step) {
     Raw<VB> v[U], w[U];
     float m[U], rs[U];
 #pragma unroll
@@ -442,7 +454,7 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
       m[u] = nm[u];
       rs[u] = nr[u];
     }
-    load(id + (long long)U * teams, at + U * step);   // the next ones, meanwhile
+    load(id + U * teams);   // the next ones, meanwhile
     if constexpr (!BACKWARD) {
       uint64_t d[U][NP];
 #pragma unroll
@@ -455,12 +467,10 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
         }
         m[u] = f2_lo(t) + f2_hi(t);
       }
-      for (int o = s.T >> 1; o > 0; o >>= 1)
-#pragma unroll
-        for (int u = 0; u < U; ++u) m[u] += __shfl_xor_sync(0xffffffffu, m[u], o);
+      join(m);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        m[u] = __fdiv_rn(m[u], n);   // exact for constant groups
+        m[u] = two_power ? m[u] * inv : __fdiv_rn(m[u], n);   // exact for constant groups
         uint64_t t = 0;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -469,13 +479,11 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
         }
         rs[u] = has ? f2_lo(t) + f2_hi(t) : 0.f;
       }
-      for (int o = s.T >> 1; o > 0; o >>= 1)
-#pragma unroll
-        for (int u = 0; u < U; ++u) rs[u] += __shfl_xor_sync(0xffffffffu, rs[u], o);
+      join(rs);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         rs[u] = rsqrtf(fmaf(rs[u], inv, a.eps));
-        const long long iu = id + (long long)u * teams;
+        const int iu = id + u * teams;
         if (iu < total) {
           if (tl == 0 && a.mean) {
             a.mean[iu] = m[u];
@@ -484,7 +492,7 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
           if (has) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) d[u][i] = act2<ACT>(fma2(mul2(d[u][i], both(rs[u])), ga[i], be[i]));
-            raw_store<VB>(y + at + u * step, raw_make<T, VB>(d[u]));
+            raw_store<VB>(y + u * step, raw_make<T, VB>(d[u]));
           }
         }
       }
@@ -504,19 +512,15 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
         s1[u] = f2_lo(t1) + f2_hi(t1);
         s2[u] = f2_lo(t2) + f2_hi(t2);
       }
-      for (int o = s.T >> 1; o > 0; o >>= 1)
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          s1[u] += __shfl_xor_sync(0xffffffffu, s1[u], o);
-          s2[u] += __shfl_xor_sync(0xffffffffu, s2[u], o);
-        }
+      join(s1);
+      join(s2);
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (has && id + (long long)u * teams < total) {
+        if (has && id + u * teams < total) {
           const uint64_t m1 = both(-s1[u] * inv), m2 = both(-s2[u] * inv);
 #pragma unroll
           for (int i = 0; i < NP; ++i) d[u][i] = mul2(both(rs[u]), fma2(xh[u][i], m2, add2(d[u][i], m1)));
-          raw_store<VB>(y + at + u * step, raw_make<T, VB>(d[u]));
+          raw_store<VB>(y + u * step, raw_make<T, VB>(d[u]));
         }
     }
   }
