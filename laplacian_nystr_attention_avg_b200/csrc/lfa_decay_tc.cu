@@ -66,8 +66,8 @@ struct Cfg {
   static constexpr int kTile = DP / 64 * kPanelB;   // bytes of a token tile
   // rings of tiles. At 128 channels five fit: x is done with first (S, then Ox), y and z are held longer
   static constexpr int kNY = DP == 64 ? 3 : 2;
-  static constexpr int kNX = STATE ? 0 : DP == 64 ? 3 : 1;
-  static constexpr int kNZ = DP == 64 ? 3 : 2;
+  static constexpr int kNX = STATE ? 0 : DP == 64 ? 4 : 1;
+  static constexpr int kNZ = DP == 64 ? 4 : 2;
   static constexpr int kOffX = kNY * kTile;
   static constexpr int kOffZ = kOffX + kNX * kTile;
   static constexpr int kOffPart = kOffZ + kNZ * kTile;
@@ -111,8 +111,8 @@ struct Cfg {
   static_assert(kTd + DP <= kTmem, "tensor memory");
 };
 enum Bar {
-  kFullY = 0, kFullX = 3, kFullZ = 6, kEmptyY = 9, kEmptyX = 12, kEmptyZ = 15, kSFull = 18, kSRead = 20,
-  kPReady = 22, kYdReady, kPartFree = kYdReady + 2, kDFull = kPartFree + 2, kDRead, kRbReady, kXDone, kOFull, kOFree,
+  kFullY = 0, kFullX = 4, kFullZ = 8, kEmptyY = 12, kEmptyX = 16, kEmptyZ = 20, kSFull = 24, kSRead = 26,
+  kPReady = 28, kYdReady, kPartFree = kYdReady + 2, kDFull = kPartFree + 2, kDRead, kRbReady, kXDone, kOFull, kOFree,
   kZClean, kFin, kNumBars = kFin + 2
 };
 static_assert(kNumBars * 8 <= 368, "barriers overlap the TMEM slot");
@@ -360,9 +360,14 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       for (int k = 1; k < n; ++k) {
         if (!load(&jb.y, 0, C::kNY, kFullY, kEmptyY, k)) break;
         ++ny;
+        // x before z where its ring is as deep: its slot is free sooner, and S needs it sooner than P z needs z
+        if constexpr (C::kNX > 1) {
+          if (!load(&jb.x, C::kOffX, C::kNX, kFullX, kEmptyX, k)) break;
+          ++nx;
+        }
         if (!load(&jb.z, C::kOffZ, C::kNZ, kFullZ, kEmptyZ, k)) break;
         ++nz;
-        if constexpr (!STATE) {
+        if constexpr (C::kNX == 1) {
           if (!load(&jb.x, C::kOffX, C::kNX, kFullX, kEmptyX, k)) break;
           ++nx;
         }
