@@ -18,10 +18,11 @@
 // the device's status word is set, the CTA stops waiting for anything and drains what it has in flight).
 //
 // What bounds it: 128 units x 4096 tokens take 115 us at 128 channels (83 at the copy bandwidth, with 128 of 148 SMs
-// at work; 144 units 116 of 94) and 67 us at 64 channels (42): there a chunk takes 3.0 k cycles, in which issue slots
+// at work; 144 units 116 of 94) and 64 us at 64 channels (42): there a chunk takes 3.0 k cycles, in which issue slots
 // are half full, shared memory 65 % busy and the tensor pipe 32 %, the longest chains being P's warps and D -> R -> D.
 // Not taken: 8 P warps at 128 channels, their registers from the others (117 us); a second set of O instead of the
-// second set of S at 64.
+// second set of S at 64; a unit's three backward runs on neighbouring SMs (they read the same tiles at the same time:
+// 188 instead of 178 us for 128 units x 2048 tokens x 128, 120 instead of 104 at 64).
 //
 // Few units over long sequences: segments run at once. k_decay_tc<.., true> sums up each segment's own
 // state, k_decay_prefix carries them over the segments, and the main kernel starts every segment from its state.
