@@ -159,6 +159,11 @@ def _plan(kind, extra, tensors, check):
     return plan
 
 
+def _number(x):
+    """A scale as the value it has now: one held in a tensor may change under the same object."""
+    return None if x is None else float(x)
+
+
 def _workspace(nbytes: int, device: torch.device) -> Optional[torch.Tensor]:
     """A call's workspace (torch allocations are 512-byte aligned). None where it uses none, or refuses its
     configuration: the call itself then says why."""
@@ -217,7 +222,7 @@ def decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: 
         cfg.o_stride[:] = _tokens(_new(v, lengths) if O is None else O, "O", v.shape, q.dtype, device)[:3]
         return cfg, device, state, lib.lfa_decay_workspace_size(cfg, 0)
 
-    cfg, device, state, nbytes = _plan("forward", scale, (q, k, v, log_decay, S0, lengths, O, S_out), check)
+    cfg, device, state, nbytes = _plan("forward", _number(scale), (q, k, v, log_decay, S0, lengths, O, S_out), check)
     if O is None:
         O = _new(v, lengths)
     if S_out is None and return_state:
@@ -256,8 +261,8 @@ def decay_backward(q, k, v, log_decay, dO, *, scale=None, S0=None, lengths=None,
                     raise ValueError(f"{name}: strides {st}, expected {like.stride()}")
         return cfg, device, state, lib.lfa_decay_workspace_size(cfg, 1)
 
-    cfg, device, state, nbytes = _plan("backward", scale, (q, k, v, log_decay, dO, S0, lengths, dS_out, dQ, dK, dV, dS0),
-                                       check)
+    cfg, device, state, nbytes = _plan("backward", _number(scale),
+                                       (q, k, v, log_decay, dO, S0, lengths, dS_out, dQ, dK, dV, dS0), check)
     dQ, dK, dV = (_strided_like(like, lengths) if t is None else t for t, like in ((dQ, q), (dK, k), (dV, v)))
     if dS0 is None and return_state:
         dS0 = torch.empty(state, dtype=torch.float32, device=device)
@@ -299,7 +304,7 @@ def decay_step(q, k, v, log_decay, S, *, scale=None, slots=None, O=None, stream=
             _require(slots, "slots", (B,), torch.int32, device)
         return cfg, device.index, S.shape[0]
 
-    cfg, device, n_slots = _plan("step", scale, (q, k, v, log_decay, S, slots, O), check)
+    cfg, device, n_slots = _plan("step", _number(scale), (q, k, v, log_decay, S, slots, O), check)
     if O is None:
         O = torch.empty_like(v)
     _check(load().lfa_decay_step(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), S.data_ptr(),
@@ -390,7 +395,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, x2:
             cfg.y2_stride[:] = _tokens(y2, "out2", x2.shape, x.dtype, device)[:3]
         return cfg, device.index
 
-    cfg, device = _plan("rotary", (layout, mscale, inverse), (x, positions, freqs, x2, out, out2), check)
+    cfg, device = _plan("rotary", (layout, float(mscale), bool(inverse)), (x, positions, freqs, x2, out, out2), check)
     if out is None:
         out = torch.empty_like(x)
     if out2 is None and x2 is not None:
@@ -434,7 +439,7 @@ def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = Non
             _require(out, "out", x.shape, x.dtype, device)
         return cfg, device, lib.lfa_group_norm_workspace_size(cfg, 0)
 
-    cfg, device, nbytes = _plan("norm", (groups, eps, act), (x, gamma, beta, out), check)
+    cfg, device, nbytes = _plan("norm", (int(groups), float(eps), act), (x, gamma, beta, out), check)
     if out is None:
         out = torch.empty_like(x)
     ws = _workspace(nbytes, device)
@@ -463,7 +468,7 @@ def group_norm_backward(x, dy, mean, rstd, groups: int, gamma=None, beta=None, *
             _require(dx, "dx", x.shape, x.dtype, device)
         return cfg, device, lib.lfa_group_norm_workspace_size(cfg, 1)
 
-    cfg, device, nbytes = _plan("norm_backward", (groups, eps, act), (x, dy, mean, rstd, gamma, beta, dx), check)
+    cfg, device, nbytes = _plan("norm_backward", (int(groups), float(eps), act), (x, dy, mean, rstd, gamma, beta, dx), check)
     if dx is None:
         dx = torch.empty_like(x)
     ws = _workspace(nbytes, device)

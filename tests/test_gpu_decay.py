@@ -402,3 +402,12 @@ def test_refused_on_the_device():
     with pytest.raises(ValueError):
         decay.decay_backward(q, k, v, ld, v, dQ=torch.empty_like(q).transpose(1, 2).contiguous().transpose(1, 2))
     assert torch.isfinite(decay.decay_forward(q, k, v, ld)[0]).all()
+
+
+def test_scale_held_in_a_tensor():
+    """A changed value counts, though the object stays."""
+    q, k, v, ld, _, _, _ = _inputs(1, 2, 40, 16, 16, F32)
+    scale = torch.tensor(0.5)
+    first = decay.decay_forward(q, k, v, ld, scale=scale)[0]
+    scale.mul_(2)
+    assert torch.equal(decay.decay_forward(q, k, v, ld, scale=scale)[0], 2 * first)
