@@ -411,3 +411,25 @@ def test_scale_held_in_a_tensor():
     first = decay.decay_forward(q, k, v, ld, scale=scale)[0]
     scale.mul_(2)
     assert torch.equal(decay.decay_forward(q, k, v, ld, scale=scale)[0], 2 * first)
+
+
+def test_two_graphs_replayed_at_once():
+    """Each captured graph has a workspace of its own (sequences long enough to be cut in segments)."""
+    sets = [_inputs(1, 4, 2500, 64, 64, BF, seed=20 + i) for i in range(2)]
+    calls = [lambda s=s: decay.decay_forward(s[0], s[1], s[2], s[3], S0=s[4], return_state=True) +
+             decay.decay_backward(s[0], s[1], s[2], s[3], s[2], S0=s[4]) for s in sets]
+    want = [f() for f in calls]
+    graphs, got, streams = [], [], [torch.cuda.Stream() for _ in sets]
+    for f in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(f())
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for w, o in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, o) if a is not None)

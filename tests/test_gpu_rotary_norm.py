@@ -325,3 +325,30 @@ def test_layer_bf16_ragged_runs_and_trains():
         torch.cuda.synchronize()
         assert all(torch.isfinite(t).all() for t in (y, S, *grads))
         assert (grads[0][1] == 0).all() and (grads[0][2, 131:] == 0).all()
+
+
+def test_norm_graphs_replayed_at_once():
+    """Large groups, forward and backward, in two graphs on two streams."""
+    g = torch.Generator("cuda").manual_seed(8)
+    sets = [[torch.randn((4, 1500, 64), generator=g, device="cuda").to(BF) for _ in range(2)] for _ in range(2)]
+    ga, be = (torch.randn(64, generator=g, device="cuda") for _ in range(2))
+
+    def call(x, dy):
+        y, m, r = decay.group_norm(x, 4, ga, be, act="silu")
+        return (y, m, r) + decay.group_norm_backward(x, dy, m, r, 4, ga, be, act="silu")
+
+    want = [call(*s) for s in sets]
+    graphs, got, streams = [], [], [torch.cuda.Stream() for _ in sets]
+    for s in sets:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            got.append(call(*s))
+        graphs.append(gr)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+    torch.cuda.synchronize()
+    for w, o in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, o))
