@@ -224,8 +224,8 @@ void run_rotary(const RotaryArgs& a, cudaStream_t st) {
 // take three launches: per-channel sums of row chunks, their combination per group, and the output; the second
 // reading comes from the 126 MB L2 as far as the tensor fits there. All sums are joined in a fixed order.
 // Measured, bf16 with silu: 8192 x 1024 in 16 groups (33.6 MB) 13 us, of which a launch and four dependent rounds a
-// warp are most; 65536 rows 59 us, 4.5 TB/s, where exponentials and reciprocals alone take 30 (without silu 46 us,
-// the copy bandwidth). Large, 32 x 3136 x 256 in 32 groups (51 MB a tensor): forward 44 us, sums 19 and output 20 of
+// warp are most; 65536 rows 57 us, 4.7 TB/s, where exponentials and reciprocals alone take 30 (without silu 46 us,
+// the copy bandwidth), and backward 95 us (402 MB: 62; with the sums of dgamma and dbeta in a launch before: 169). Large, 32 x 3136 x 256 in 32 groups (51 MB a tensor): forward 44 us, sums 19 and output 20 of
 // it; backward 56 us, sums 26, output 24. These wait for memory latency and the activation's two special-function
 // instructions per element (half their pipe) in turn; the join is a few microseconds of latency, most of it under
 // the neighbours (three launches apart: 49 and 64 us).
@@ -315,6 +315,8 @@ struct SmallArgs {
   NormArgs a;
   int T, dv, nvec;     // threads of a team (0: the block), vectors of a group in a row and in all
   uint32_t magic;      // j / dv = umulhi(j, magic) for dv > 1
+  int blocks;          // of k_norm_rows (one vector a thread)
+  float* part;         // its backward: channel sums [team / G][row of the group][2][C], or null
 };
 
 // Where a team's vector j lies: element offset from the group's first element, and its first channel in the group
@@ -390,7 +392,9 @@ __global__ void __launch_bounds__(kNT) k_norm_small(const __grid_constant__ Smal
 }
 
 // The same for groups of one vector per thread (T a power of two): a thread keeps its channels over all the samples it
-// takes (every teams-th (sample, group); teams is a multiple of G), U at once and the next U on their way.
+// takes (every teams-th (sample, group); teams is a multiple of G), U at once and the next U on their way; backward it
+// sums its channels' dgamma and dbeta as it goes. (Twice the blocks, or U = 4 on three a SM, were slower: 8192 x 1024
+// 16.6 and 17.3 us beside 15.1.)
 template <typename T, int VB, int ACT, bool BACKWARD>
 __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __grid_constant__ SmallArgs s, int teams) {
   constexpr int V = VB / sizeof(T), U = 2;
@@ -421,6 +425,8 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
 #pragma unroll
         for (int u = 0; u < U; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
   };
+  uint64_t sb[NP] = {}, sg[NP] = {};   // backward: this thread's share of dbeta and dgamma
+  if (BACKWARD) let_next_start();
   Raw<VB> nv[U], nw[U];
   float nm[U], nr[U];
   auto load = [&](int id) {   // U samples, and on to the next; zeros where there is none
@@ -499,13 +505,17 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
     } else {
       uint64_t d[U][NP], xh[U][NP];
       float s1[U], s2[U];
+      // (samples there are none of have x = dy = 0, and so have threads without a vector)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         uint64_t t1 = 0, t2 = 0;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           xh[u][i] = mul2(add2(raw_pair<T>(v[u], i), both(-m[u])), both(rs[u]));
-          d[u][i] = mul2(mul2(ga[i], raw_pair<T>(w[u], i)), slope2<ACT>(fma2(xh[u][i], ga[i], be[i])));
+          const uint64_t dz = mul2(raw_pair<T>(w[u], i), slope2<ACT>(fma2(xh[u][i], ga[i], be[i])));
+          sb[i] = add2(sb[i], dz);
+          sg[i] = fma2(dz, xh[u][i], sg[i]);
+          d[u][i] = mul2(ga[i], dz);
           t1 = add2(t1, d[u][i]);   // dy is zero in threads without a vector and beside a lone channel
           t2 = fma2(d[u][i], xh[u][i], t2);
         }
@@ -522,6 +532,15 @@ __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __gri
           for (int i = 0; i < NP; ++i) d[u][i] = mul2(both(rs[u]), fma2(xh[u][i], m2, add2(d[u][i], m1)));
           raw_store<VB>(y + u * step, raw_make<T, VB>(d[u]));
         }
+    }
+  }
+  if (BACKWARD && s.part && has) {
+    const int row = s.dv > 1 ? (int)__umulhi((uint32_t)tl, s.magic) : tl;
+    float* o = s.part + ((size_t)b0 * a.N + row) * 2 * a.C + g * dg + c;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      o[i] = (i & 1) ? f2_hi(sb[i / 2]) : f2_lo(sb[i / 2]);
+      o[a.C + i] = (i & 1) ? f2_hi(sg[i / 2]) : f2_lo(sg[i / 2]);
     }
   }
 }
@@ -1014,8 +1033,19 @@ Plan plan_norm(int B, int N, int C, int G, int es, bool backward) {
       p.E = cap;
     }
   }
-  // rows in chunks
   RowArgs& r = p.r;
+  if (p.small && p.E == 1) {   // k_norm_rows: at most one wave of blocks, with a number of teams that G divides
+    const int per = kNT / p.s.T, wave = backward ? 2 * 148 : kNormWave;
+    int unit = G;   // G / gcd(G, per)
+    for (int d = per; d > 1; d /= 2)
+      if (unit % 2 == 0) unit /= 2;
+    const long long need = ((long long)B * G + per - 1) / per;
+    p.s.blocks = (int)(((need < wave ? need : wave) + unit - 1) / unit * unit);
+    r.chunks = (int)((long long)p.s.blocks * per / G) * N;   // records of channel sums
+    if (backward) p.floats = (size_t)r.chunks * 2 * C;
+    return p;
+  }
+  // rows in chunks
   const int VB = p.small ? vec_bytes(C, es) : (p.VB = vec_bytes(C, es)), cv = C * es / VB;
   r.cw = cv <= 256 ? cv : 128;
   r.rl = kNT / r.cw;
@@ -1037,18 +1067,9 @@ Plan plan_norm(int B, int N, int C, int G, int es, bool backward) {
   return p;
 }
 
-// blocks of k_norm_rows: at most one wave, with a number of teams that G divides
 template <typename T, int VB, int ACT, bool BACKWARD>
 void rows_launch(const Plan& p, cudaStream_t st) {
-  const int per = kNT / p.s.T, G = p.s.a.G;
-  int unit = G;   // blocks whose teams are a multiple of G: G / gcd(G, per)
-  for (int d = per; d > 1; d /= 2)
-    if (unit % 2 == 0) unit /= 2;
-  const long long teams = (long long)p.s.a.B * G, need = (teams + per - 1) / per;
-  const int wave = BACKWARD ? 2 * 148 : kNormWave;
-  long long blocks = need < wave ? need : wave;
-  blocks = (blocks + unit - 1) / unit * unit;
-  k_norm_rows<T, VB, ACT, BACKWARD><<<(unsigned)blocks, kNT, 0, st>>>(p.s, (int)(blocks * per));
+  k_norm_rows<T, VB, ACT, BACKWARD><<<p.s.blocks, kNT, 0, st>>>(p.s, p.s.blocks * (kNT / p.s.T));
 }
 template <typename T, int VB, int ACT>
 void small_forward(const Plan& p, cudaStream_t st) {
@@ -1183,6 +1204,12 @@ void run_norm_backward(const NormArgs& a, cudaStream_t st) {
   p.r.part = a.ws;
   if (!p.small) {
     by_vec<T>(p.VB, a.act, LargeBackward<T>{p, st});
+    return;
+  }
+  if (p.E == 1) {   // dx's threads keep their channels over all samples, and sum dgamma and dbeta on the way
+    if (a.dgamma) p.s.part = a.ws;
+    by_vec<T>(p.VB, a.act, SmallDx<T>{p, st});
+    if (a.dgamma) launch_next(k_norm_bjoin, ceil_div(a.C, 8), kNT, 0, st, p.r, 0, p.r.chunks, (float*)nullptr);
     return;
   }
   if (a.dgamma) by_vec<T>(vec_bytes(a.C, sizeof(T)), a.act, FlatSums<T>{p, st});   // before dx, which may overwrite dy
