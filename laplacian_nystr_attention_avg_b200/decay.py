@@ -87,14 +87,24 @@ def _tokens(t: torch.Tensor, name: str, shape, dtype, device) -> Tuple[int, ...]
     return st
 
 
+def _size(n, name: str) -> int:
+    """A size that the library's 32-bit fields hold (ctypes would keep the low 32 bits of any other)."""
+    n = int(n)
+    if not -1 << 31 <= n < 1 << 31:
+        raise ValueError(f"{name}: {n} does not fit 32 bits")
+    return n
+
+
 def _first(t: torch.Tensor, name: str, dims: int) -> torch.device:
-    """The tensor that sets a call's dtype and device."""
+    """The tensor that sets a call's sizes, dtype and device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dim() != dims:
         raise ValueError(f"{name}: expected {dims} dimensions, got shape {tuple(t.shape)}")
     if t.numel() == 0:
         raise ValueError(f"{name}: empty (shape {tuple(t.shape)})")
+    for n in t.shape:
+        _size(n, f"{name}: a size")
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16 or float32")
     if t.device.type != "cuda":
@@ -177,7 +187,7 @@ def _decay_config(q, k, v, log_decay, lengths, scale):
     B, heads, N, dk = q.shape
     if not isinstance(v, torch.Tensor) or v.dim() != 4:
         raise ValueError("v: expected a 4-dimensional tensor")
-    dv = v.shape[3]
+    dv = _size(v.shape[3], "v: channels")
     cfg = DecayConfig(B, heads, N, dk, dv, _DTYPES[q.dtype], dk ** -0.5 if scale is None else float(scale))
     cfg.q_stride[:] = _tokens(q, "q", (B, heads, N, dk), q.dtype, device)[:3]
     cfg.k_stride[:] = _tokens(k, "k", (B, heads, N, dk), q.dtype, device)[:3]
@@ -290,7 +300,7 @@ def decay_step(q, k, v, log_decay, S, *, scale=None, slots=None, O=None, stream=
         B, heads, dk = q.shape
         if not isinstance(v, torch.Tensor) or v.dim() != 3:
             raise ValueError("v: expected a 3-dimensional tensor")
-        dv = v.shape[2]
+        dv = _size(v.shape[2], "v: channels")
         if not isinstance(S, torch.Tensor) or S.dim() != 4 or S.shape[0] < 1:
             raise ValueError("S: expected a [n_slots, heads, dk, dv] tensor")
         cfg = DecayConfig(B, heads, 1, dk, dv, _DTYPES[q.dtype], dk ** -0.5 if scale is None else float(scale))
@@ -302,7 +312,7 @@ def decay_step(q, k, v, log_decay, S, *, scale=None, slots=None, O=None, stream=
         _require(S, "S", (S.shape[0], heads, dk, dv), torch.float32, device)
         if slots is not None:
             _require(slots, "slots", (B,), torch.int32, device)
-        return cfg, device.index, S.shape[0]
+        return cfg, device.index, _size(S.shape[0], "S: slots")
 
     cfg, device, n_slots = _plan("step", _number(scale), (q, k, v, log_decay, S, slots, O), check)
     if O is None:
@@ -384,8 +394,8 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, x2:
             raise ValueError("x2: expected a [B, heads2, N, d] tensor")
         if x2 is None and out2 is not None:
             raise ValueError("out2 without x2")
-        heads2 = 0 if x2 is None else x2.shape[1]
-        cfg = RotaryConfig(B, N, d, 2 * freqs.shape[0], heads, heads2, _DTYPES[x.dtype], layout == "interleaved",
+        heads2 = 0 if x2 is None else _size(x2.shape[1], "x2: heads")
+        cfg = RotaryConfig(B, N, d, _size(2 * freqs.shape[0], "freqs: channels"), heads, heads2, _DTYPES[x.dtype], layout == "interleaved",
                            bool(inverse), float(mscale))
         cfg.x_stride[:] = _tokens(x, "x", (B, heads, N, d), x.dtype, device)[:3]
         cfg.y_stride[:] = _tokens(torch.empty_like(x) if out is None else out, "out", x.shape, x.dtype, device)[:3]
@@ -408,6 +418,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, x2:
 # ---- group norm ----------------------------------------------------------------------------------------
 
 def _norm_config(x, groups, gamma, beta, eps, act):
+    groups = _size(groups, "groups")
     device = _first(x, "x", 3)
     if act not in ACTIVATIONS:
         raise ValueError(f"act: {act!r}")
@@ -418,7 +429,7 @@ def _norm_config(x, groups, gamma, beta, eps, act):
     for name, t in (("gamma", gamma), ("beta", beta)):
         if t is not None:
             _require(t, name, (C,), torch.float32, device)
-    return NormConfig(B, N, C, int(groups), _DTYPES[x.dtype], ACTIVATIONS[act], float(eps)), device
+    return NormConfig(B, N, C, groups, _DTYPES[x.dtype], ACTIVATIONS[act], float(eps)), device
 
 
 def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,

@@ -255,3 +255,24 @@ def test_broadcast_tensors_are_refused(shape, strides):
         decay._tokens(t, "q", shape, torch.float32, t.device)
     one = torch.zeros(8).as_strided((1, 1, 1, 8), (0, 0, 0, 1))   # a single row is not broadcast
     assert decay._tokens(one, "q", (1, 1, 1, 8), torch.float32, one.device) == (0, 0, 0, 1)
+
+
+def test_sizes_past_32_bits_are_refused():
+    """The library's fields are 32-bit ints: 2^32 + 1 must not come in as 1. (Meta tensors hold no memory.)"""
+    def of(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    many, ld = (1 << 32) + 1, of(1, dtype=torch.float32)
+    calls = [lambda: decay.group_norm(of(many, 1, 8), 1), lambda: decay.group_norm(of(2, 3, 8), (1 << 32) + 4),
+             lambda: decay.group_norm(of(2, 3, 8), -(1 << 32) + 4),
+             lambda: decay.group_norm_backward(of(1, many, 8), of(1, many, 8), ld, ld, 1),
+             lambda: decay.rotary(of(1, 1, many, 8), None, None),
+             lambda: decay.decay_forward(of(many, 1, 1, 8), of(many, 1, 1, 8), of(many, 1, 1, 8), ld),
+             lambda: decay.decay_backward(of(1, many, 1, 8), None, None, ld, None),
+             lambda: decay.decay_step(of(1, many, 8), None, None, ld, None)]
+    for call in calls:
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    assert decay._size((1 << 31) - 1, "n") == (1 << 31) - 1 and decay._size(-(1 << 31), "n") == -(1 << 31)
+    with pytest.raises(ValueError, match="empty"):
+        decay.group_norm(of(0, 1, 8), 1)
