@@ -1040,10 +1040,16 @@ Plan plan_norm(int B, int N, int C, int G, int es, bool backward) {
     for (int d = per; d > 1; d /= 2)
       if (unit % 2 == 0) unit /= 2;
     const long long need = ((long long)B * G + per - 1) / per;
-    p.s.blocks = (int)(((need < wave ? need : wave) + unit - 1) / unit * unit);
-    r.chunks = (int)((long long)p.s.blocks * per / G) * N;   // records of channel sums
-    if (backward) p.floats = (size_t)r.chunks * 2 * C;
-    return p;
+    // Many groups with few factors of two: more than a wave, or (backward) mostly records of channels that no sample
+    // filled. These take the teams that know nothing of each other.
+    if (unit <= wave && (!backward || unit <= need)) {
+      const long long up = (need + unit - 1) / unit * unit;
+      p.s.blocks = (int)(up <= wave ? up : wave / unit * unit);
+      r.chunks = (int)((long long)p.s.blocks * per / G) * N;   // records of channel sums
+      if (backward) p.floats = (size_t)r.chunks * 2 * C;
+      return p;
+    }
+    p.E = cap;
   }
   // rows in chunks
   const int VB = p.small ? vec_bytes(C, es) : (p.VB = vec_bytes(C, es)), cv = C * es / VB;

@@ -268,6 +268,44 @@ def test_more_than_32_bits_of_elements():
     assert torch.equal(z[:, :, rows], w)
 
 
+MANY = [(8191, 1, 1024, 16), (8191, 1, 768, 12), (5003, 1, 1280, 20), (120011, 1, 40, 5), (40009, 1, 24, 3), (700, 1, 2392, 299),
+        (3, 1, 4099, 4099)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("B,N,C,G", MANY)
+def test_group_norm_of_many_tokens(B, N, C, G, act, dtype):
+    """Several rounds of samples a thread with a ragged tail, and group counts that are no power of two: the
+    tolerances of the shapes above."""
+    test_group_norm(B, N, C, G, act, dtype)
+    test_group_norm_backward(B, N, C, G, act, dtype)
+
+
+def test_tokens_past_32_bits_of_elements():
+    """2.3e9 elements in groups of one vector a thread: rows from both ends against the same rows alone (a sample's
+    arithmetic does not depend on its place), and dgamma, dbeta of the three rows whose dy is not zero."""
+    B, C, G = 2200000, 1024, 16
+    g = torch.Generator("cuda").manual_seed(12)
+    rows = torch.tensor([0, 1, B // 2, B - 1], device="cuda")
+    few = torch.randn((4, 1, C), generator=g, device="cuda").to(BF)
+    dfew = torch.randn((4, 1, C), generator=g, device="cuda").to(BF)
+    ga, be = 1 + 0.3 * torch.randn(C, generator=g, device="cuda"), 0.3 * torch.randn(C, generator=g, device="cuda")
+    x, dy = (torch.zeros((B, 1, C), dtype=BF, device="cuda") for _ in range(2))
+    x[rows], dy[rows] = few, dfew
+    y, mean, rstd = decay.group_norm(x, G, ga, be, act="silu")
+    want, m, r = decay.group_norm(few, G, ga, be, act="silu")
+    assert torch.equal(y[rows], want) and torch.equal(mean[rows], m) and torch.equal(rstd[rows], r)
+    dx, dg, db = decay.group_norm_backward(x, dy, mean, rstd, G, ga, be, act="silu", dx=y)
+    w, wg, wb = decay.group_norm_backward(few, dfew, m, r, G, ga, be, act="silu")
+    assert torch.equal(dx[rows], w)
+    # four terms each, joined in another order: three roundings of a partial sum, at most the sum of absolute terms
+    xh = ((few.double().view(4, G, -1) - m.double()[..., None]) * r.double()[..., None]).view(4, 1, C)
+    adz = 1.13 * dfew.double().abs()
+    assert ((dg - wg).double().abs() <= 8 * U * (adz * xh.abs()).sum((0, 1))).all()
+    assert ((db - wb).double().abs() <= 8 * U * adz.sum((0, 1))).all()
+
+
 # ---- the layer -----------------------------------------------------------------------------------------
 
 def _layer(B, N, H, dk, dv, seed=0):

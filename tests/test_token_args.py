@@ -276,3 +276,23 @@ def test_sizes_past_32_bits_are_refused():
     assert decay._size((1 << 31) - 1, "n") == (1 << 31) - 1 and decay._size(-(1 << 31), "n") == -(1 << 31)
     with pytest.raises(ValueError, match="empty"):
         decay.group_norm(of(0, 1, 8), 1)
+
+
+@pytest.mark.parametrize("G", [3, 5, 6, 12, 20, 40, 96])
+@pytest.mark.parametrize("dtype,es", [(lfa.LFA_BF16, 2), (lfa.LFA_F32, 4)])
+def test_per_token_norm_backward_takes_one_wave(lib, G, dtype, es):
+    """The backward's workspace holds 2 C sums per record, and a block (256 threads in teams of T, a team per group of
+    one token) fills 256 / T / G records. At most 2 blocks an SM run at once: more would leave a few to run alone."""
+    n = 64
+    T = n * es // 16   # one 16-byte vector a thread
+    c = _nc(B=20000, N=1, C=n * G, groups=G, dtype=dtype)
+    records = (lib.lfa_group_norm_workspace_size(c, 1) - 256) // (2 * n * G * 4)
+    assert 0.9 * 296 <= records * G / (256 // T) <= 296
+
+
+@pytest.mark.parametrize("B,C,G,dtype,es", [(1, 131064, 16383, lfa.LFA_BF16, 2), (1, (1 << 20) - 1, (1 << 20) - 1, lfa.LFA_F32, 4),
+                                            (3, 8 * 299, 299, lfa.LFA_BF16, 2), (1, 24, 3, lfa.LFA_BF16, 2), (2, 4099, 4099, lfa.LFA_BF16, 2)])
+def test_norm_backward_workspace_follows_the_data(lib, B, C, G, dtype, es):
+    """Channel sums are two floats per channel and record; there are never more than twice as many records as rows."""
+    n = lib.lfa_group_norm_workspace_size(_nc(B=B, N=1, C=C, groups=G, dtype=dtype), 1)
+    assert 256 < n <= 512 + 2 * B * 2 * C * 4
