@@ -306,6 +306,50 @@ def test_tokens_past_32_bits_of_elements():
     assert ((db - wb).double().abs() <= 8 * U * adz.sum((0, 1))).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("B,N,C,G", [(1, 1, 4096, 512), (2, 49, 4096, 64), (2, 1024, 4096, 8)])
+def test_activations_from_end_to_end(B, N, C, G, act, dtype):
+    """gamma = 0 leaves z = beta, so y = act(beta), and with dy = 1 in one row dbeta = act'(beta), in all three ways
+    through the data. Relative to themselves (U = 2^-24; subnormal results to fp32's smallest step, some of them in
+    the factors): silu in fp32: expf 2 units of 2U, 1 + e and the reciprocal 3U, three products 3U: 16 U; its slope is
+    p + z p q of factors like that: 32 U of the two terms. gelu: the tail's smooth factor 2^-21, expf 2 units of 2U, its
+    argument z^2 / 2 rounded twice, z^2 U, products 4U: (24 + 2 z^2) U in value and slope. In bf16, half a step, and
+    ex2 of a rounded argument: |z| U more for silu, z^2 U for gelu, whose smooth factor is within 2^-16; silu below
+    z = -87, where the exponential leaves fp32, is within 1e-35 of its value."""
+    beta = torch.cat([torch.linspace(-14, 14, C // 2), torch.linspace(-101, 100, C - C // 2)]).cuda()
+    g = torch.Generator("cuda").manual_seed(7)
+    x = torch.randn((B, N, C), generator=g, device="cuda").to(dtype)
+    gamma = torch.zeros(C, device="cuda")
+    y, mean, rstd = decay.group_norm(x, G, gamma, beta, act=act)
+    z = beta.double()
+    if act == "silu":
+        p, q = torch.sigmoid(z), torch.sigmoid(-z)
+        value, terms, each = z * p, (p, z * p * q), 32 * U + 0 * z
+        if dtype == BF:
+            each = each + 4 * z.abs() * U
+    else:
+        cdf = 0.5 * torch.special.erfc(-z * 0.5 ** 0.5)
+        value, terms = z * cdf, (cdf, z * torch.exp(-0.5 * z * z) * 0.3989422804014327)
+        each = (24 + 2 * z * z) * U
+        if dtype == BF:
+            each = each + 2 * z * z * U + 2.0 ** -16
+    tiny = 2.0 ** -140 if dtype == F32 else 1e-35
+    ref = value.expand(B, N, C)
+    bound = each * value.abs() + (2.0 ** -8 * value.abs() if dtype == BF else 0) + tiny
+    bad = (y.double() - ref).abs() > bound
+    assert not bad.any(), f"{int(bad.sum())}, z from {float(z.expand(B, N, C)[bad].min())} to {float(z.expand(B, N, C)[bad].max())}"
+    dy = torch.zeros((B, N, C), dtype=dtype, device="cuda")
+    dy[-1, -1] = 1
+    _, _, dbeta = decay.group_norm_backward(x, dy, mean, rstd, G, gamma, beta, act=act)
+    slope = terms[0] + terms[1]
+    size = terms[0].abs() + terms[1].abs()
+    if act == "silu" and dtype == BF:   # p (1 - p) from the rounded p: 2 U |z| p
+        size = size + z.abs() * terms[0] * U / each
+    bad = (dbeta.double() - slope).abs() > each * size + tiny
+    assert not bad.any(), f"{int(bad.sum())}, z from {float(z[bad].min())} to {float(z[bad].max())}"
+
+
 # ---- the layer -----------------------------------------------------------------------------------------
 
 def _layer(B, N, H, dk, dv, seed=0):
