@@ -195,7 +195,9 @@ __global__ void __launch_bounds__(4 * CB, DA == 128 ? 1 : 2) k_decay_core(const 
           acc[p] = make_float4(acc[p].x * f, acc[p].y * f, acc[p].z * f, acc[p].w * f);
         }
         __syncwarp();   // P's rows are used by the warp that wrote them
-        for (int j = rev ? w0 : 0; j < (rev ? nv : w1); j += 4) {   // z is zero behind the end
+        // tokens j .. j + 3; z is zero behind the end. On the diagonal (j = i0) the other side's z is left out, not
+        // multiplied by zero: it need not be finite
+        auto add = [&](int j, auto on) {
           float4 w[4], z[4];
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
@@ -205,7 +207,19 @@ __global__ void __launch_bounds__(4 * CB, DA == 128 ? 1 : 2) k_decay_core(const 
 #pragma unroll
           for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int p = 0; p < 4; ++p) fma4(acc[p], part(w[p], q), z[q]);
+            for (int p = 0; p < 4; ++p)
+              if (on(p, q)) fma4(acc[p], part(w[p], q), z[q]);
+        };
+        const auto all = [](int, int) { return true; };
+        static_assert(TJ == 16, "a warp has eight rows, two tiles of four");
+        if (!rev) {
+          for (int j = 0; j < w0; j += 4) add(j, all);
+          if (i0 > w0) add(w0, all);
+          add(i0, [](int p, int q) { return q <= p; });
+        } else {
+          add(i0, [](int p, int q) { return q >= p; });
+          if (i0 == w0) add(w0 + 4, all);
+          for (int j = w1; j < nv; j += 4) add(j, all);
         }
 #pragma unroll
         for (int p = 0; p < 4; ++p)

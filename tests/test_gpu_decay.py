@@ -433,3 +433,75 @@ def test_two_graphs_replayed_at_once():
     torch.cuda.synchronize()
     for w, o in zip(want, got):
         assert all(torch.equal(a, b) for a, b in zip(w, o) if a is not None)
+
+
+ONE_SIDED = [F32]
+ODD = [float("nan"), float("inf"), -float("inf")]
+
+
+def _clean_rows(got, ref, T, rows, N, dtype, what, columns=None):
+    got, ref, T = (t[..., rows, :] if columns is None else t[..., rows, :][..., columns] for t in (got, ref, T))
+    if got.numel():
+        _check_rows(got, ref, T, N, dtype, what)
+
+
+@pytest.mark.parametrize("dtype", ONE_SIDED)
+@pytest.mark.parametrize("B,H,N,dk,dv", [(1, 2, 300, 64, 48), (1, 2, 290, 128, 128), (2, 3, 140, 24, 16), (1, 1, 1400, 40, 72)])
+@pytest.mark.parametrize("at", [0, 1, 40, 127, 130, 139])
+def test_forward_does_not_see_later_tokens(B, H, N, dk, dv, at, dtype):
+    """NaN and infinities at one token leave what the formula forms without it: the outputs before it and, for a
+    single channel of v, the other channels; for q, every other token."""
+    q, k, v, ld, S0, _, _ = _inputs(B, H, N, dk, dv, dtype, "bnhd", seed=at)
+    scale = dk ** -0.5
+    ro, rS = R.decay_forward(q.double(), k.double(), v.double(), ld, scale, S0.double(), None)
+    To, TS = R.decay_forward(q.double().abs(), k.double().abs(), v.double().abs(), ld, scale, S0.double().abs(), None)
+    n = torch.arange(N, device="cuda")
+    for i, odd in enumerate(ODD):
+        for name in "qkv":
+            t = {"q": q, "k": k, "v": v}[name].clone(memory_format=torch.preserve_format)
+            c = (5 * i + at) % t.shape[3]
+            others = torch.arange(t.shape[3], device="cuda") != c
+            t[:, :, at, c] = odd
+            if name != "v":
+                t[:, :, at] = odd
+            o, S = decay.decay_forward(*(t if name == m else x for m, x in (("q", q), ("k", k), ("v", v))), ld, S0=S0,
+                                       return_state=True)
+            _clean_rows(o, ro, To, n != at if name == "q" else n < at, N, dtype, f"{name} {odd}")
+            assert not torch.isfinite(o[:, :, at]).all()
+            if name == "v":
+                _clean_rows(o, ro, To, n >= 0, N, dtype, f"other channels, {odd}", others)
+                _check_state(S[..., others], rS[..., others], TS[..., others], N, dtype, "S, other channels")
+            if name == "q":
+                _check_state(S, rS, TS, N, dtype, "S")
+    assert decay.decay_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ONE_SIDED)
+@pytest.mark.parametrize("B,H,N,dk,dv", [(1, 2, 300, 64, 48), (1, 2, 290, 128, 128), (2, 3, 140, 24, 16), (1, 1, 1400, 40, 72)])
+@pytest.mark.parametrize("at", [0, 1, 40, 127, 130, 139])
+def test_backward_does_not_see_the_other_side(B, H, N, dk, dv, at, dtype):
+    """One token's NaN or infinities: dq before it, dk and dv behind it, and what does not meet it at all."""
+    q, k, v, ld, S0, _, g = _inputs(B, H, N, dk, dv, dtype, "bnhd", seed=at)
+    dO = _mk((B, H, N, dv), dtype, g, "bnhd")
+    dS = torch.randn(S0.shape, generator=g, device="cuda")
+    at_once = [q, k, v, dO]
+    q64, k64, v64, dO64 = (t.double() for t in at_once)
+    ref = R.decay_grads(q64, k64, v64, ld, dk ** -0.5, S0.double(), None, dO64, dS.double())
+    T = R.decay_grads(q64.abs(), k64.abs(), v64.abs(), ld, dk ** -0.5, S0.double().abs(), None, dO64.abs(), dS.double().abs())
+    n = torch.arange(N, device="cuda")
+    before, behind, rest = n < at, n > at, n != at
+    good = {"q": (n >= 0, behind, behind), "k": (before, n >= 0, rest), "v": (before, rest, n >= 0),
+            "dO": (rest, behind, behind)}
+    for i, odd in enumerate(ODD):
+        for j, name in enumerate(("q", "k", "v", "dO")):
+            t = [x.clone(memory_format=torch.preserve_format) if m == j else x for m, x in enumerate(at_once)]
+            if i == 0:
+                t[j][:, :, at] = odd
+            else:
+                t[j][:, :, at, (5 * i + at) % t[j].shape[3]] = odd
+            got = decay.decay_backward(t[0], t[1], t[2], ld, t[3], S0=S0, dS_out=dS, return_state=True)
+            for what, x, r, a, rows in zip(("dq", "dk", "dv"), got, ref, T, good[name]):
+                _clean_rows(x, r, a, rows, N, dtype, f"{what}, {name} {odd}")
+            if name in "kv":
+                _check_state(got[3], ref[3], T[3], N, dtype, "dS0")
+    assert decay.decay_status() == 0
