@@ -9,7 +9,8 @@
 //   D  = (y c_state l^(n-j))^T z            (M da, N db, K 128 tokens), R' = l^n R + D   (state warps)
 // The decayed rows of y enter as two bf16 parts (value and remainder, one product each): a state is 3.9e-6 of its norm
 // off, after 8 tokens as after 4096, beside the 2^-8 of every bf16 output that is read from it (a third part left
-// 1.4e-6, the rest being the tensor cores' own sums, and cost 16 to 20 % of the time). D starts from zero in every
+// 1.4e-6, the rest being the tensor cores' own sums, and cost 16 to 20 % of the time). An infinity has a NaN as its
+// remainder: states and outputs that the formula makes infinite may be NaN. D starts from zero in every
 // chunk and is added to R by CUDA cores: tensor-core accumulation truncates and would drift over thousands of chunks.
 // All widths are padded to DP = 64 or 128 by TMA's zero fill.
 //
@@ -27,6 +28,8 @@
 // Few units over long sequences: segments run at once. k_decay_tc<.., true> sums up each segment's own
 // state, k_decay_prefix carries them over the segments, and the main kernel starts every segment from its state.
 #include <string.h>
+
+#include <type_traits>
 
 #include "lfa_internal.h"
 #include "lfa_sm100.cuh"
@@ -53,6 +56,8 @@ struct TcJob {
   float* local;           // state kernel: sums of each segment, [units][segs]
   int da, db, rev, trans, init_decays, fin_sub;
   int wide;               // O's rows are whole, aligned 32-byte sectors
+  const __nv_bfloat16 *X, *Y, *Z;   // what the maps read, for before_odd
+  long long xs[3], ys[3], zs[3];
   float c_inter, c_intra, c_state;
 };
 struct TcArgs {
@@ -195,6 +200,7 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
 }
 __device__ __forceinline__ uint32_t packf2(uint64_t v) { return pack2(f2_lo(v), f2_hi(v)); }
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // The P warps of a run of n chunks: P = c_intra l^|i-j| S on the causal side, in bf16 (thread = token row i; with
 // two warps for a quarter of the rows, they take its blocks of 32 columns in turn). pi holds c_intra l^n after 32
@@ -278,6 +284,167 @@ __device__ __forceinline__ void weights(int n, const Waiter& wait, uint64_t* bar
   }
 }
 
+__device__ __forceinline__ void unpack8(const void* p, float* v) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = bf_lo(w[e]);
+    v[2 * e + 1] = bf_hi(w[e]);
+  }
+}
+
+// P is zero on the other side of the diagonal, but a z there that is not finite makes 0 z a NaN in its column, for all
+// rows of its chunk; from the next chunk on the state carries it, as the recurrence does. So the rows that must not see
+// it are those of the same chunk before the run comes to a column's first such z. They are formed again here, in fp32
+// from the tensors themselves, at the end of a segment whose last row is not finite (which both ways make it). One of
+// `warps` warps takes every so many sets of 8 columns: the state before the chunk, then the chunk's rows, a row a lane.
+// Looking at the last row alone keeps this out of the chunks (a check in every epilogue cost them 12 %); the barrier
+// at the end costs 1 x 8 x 65536 tokens 3 us of 103, the other listed sizes nothing that shows. A NaN in one channel of
+// the last of 4096 tokens takes 2.6 ms, tensors that are not finite from the run's start the time of a look.
+__device__ __forceinline__ void before_odd(const TcArgs& a, int warp, int warps, unsigned char* mem) {
+  const TcJob& jb = a.job[blockIdx.z];
+  const int u = blockIdx.x, seg = blockIdx.y, b = u / a.heads, h = u % a.heads, lane = threadIdx.x & 31;
+  const int L = unit_length(a.lengths, b, a.N), da = jb.da, db = jb.db;
+  const int t_lo = seg * a.seg_chunks * kC, t_hi = min(L, t_lo + a.seg_chunks * kC), T = t_hi - t_lo;
+  const bool rev = jb.rev;
+  const float ld = decay_log(a.log_decay[h]);
+  auto tok = [&](int p) { return rev ? t_hi - 1 - p : t_lo + p; };   // of place p in the run
+  const __nv_bfloat16* X = jb.X + b * jb.xs[0] + h * jb.xs[1];
+  const __nv_bfloat16* Y = jb.Y + b * jb.ys[0] + h * jb.ys[1];
+  for (int c0 = 8 * warp; c0 < db; c0 += 8 * warps) {
+    const __nv_bfloat16* Z = jb.Z + b * jb.zs[0] + h * jb.zs[1] + c0;
+    auto z_row = [&](int p) { return *reinterpret_cast<const uint4*>(Z + tok(p) * jb.zs[2]); };
+    // y and the columns of z of 32 places, in this warp's memory
+    unsigned char* ym = mem + warp * 32 * (2 * kDecayMaxD + 16);
+    unsigned char* zm = ym + 32 * 2 * kDecayMaxD;
+    auto stage = [&](int p, int n) {
+      __syncwarp();
+      for (int e = lane; e < n * (da / 8); e += 32) {
+        const int r = e / (da / 8), c = e % (da / 8) * 8;
+        *reinterpret_cast<uint4*>(ym + 2 * (r * kDecayMaxD + c)) = *reinterpret_cast<const uint4*>(Y + tok(p + r) * jb.ys[2] + c);
+      }
+      if (lane < n) *reinterpret_cast<uint4*>(zm + 16 * lane) = z_row(p + lane);
+      __syncwarp();
+    };
+    int first[8];   // the columns' first such places
+#pragma unroll
+    for (int e = 0; e < 8; ++e) first[e] = T;
+    uint32_t found = 0;
+    for (int p = 0; p < T && found != 255u; p += 32) {
+      uint32_t m = 0;
+      if (p + lane < T) {
+        const uint4 v = z_row(p + lane);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          m |= ((w[e] & 0x7f80u) == 0x7f80u ? 1u << 2 * e : 0u) | ((w[e] & 0x7f800000u) == 0x7f800000u ? 2u << 2 * e : 0u);
+      }
+      if (__any_sync(0xffffffffu, m != 0)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t lanes = __ballot_sync(0xffffffffu, m >> e & 1);
+          if (lanes && first[e] == T) {
+            first[e] = p + __ffs(lanes) - 1;
+            found |= 1u << e;
+          }
+        }
+      }
+    }
+    // where their chunks begin, in the run
+    int from[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      from[e] = first[e] == T ? T : rev ? t_hi - min((tok(first[e]) / kC + 1) * kC, t_hi) : first[e] / kC * kC;
+    for (;;) {   // the columns of one chunk at a time
+      int start = T, end = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (from[e] < first[e]) start = min(start, from[e]);
+      if (start == T) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (from[e] == start) end = max(end, first[e]);
+      float R[4][8];   // rows lane, lane + 32, ..
+      const float* src = a.segs > 1 ? jb.seg_init : jb.init;
+      const size_t at = (a.segs > 1 ? (size_t)u * a.segs + seg : (size_t)u) * da * db;
+      const float f0 = a.segs > 1 || !jb.init_decays ? 1.f : expf(ld);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = lane + 32 * i;
+          R[i][e] = src && r < da ? f0 * src[at + (jb.trans ? (size_t)(c0 + e) * da + r : (size_t)r * db + c0 + e)] : 0.f;
+        }
+      for (int p0 = 0; p0 < start; p0 += kC) {
+        const int n = min(kC, start - p0);
+        const Decay dec(ld * n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) R[i][e] = dec(R[i][e]);
+        for (int m0 = 0; m0 < n; m0 += 32) {
+          const int nm = min(32, n - m0);
+          stage(p0 + m0, nm);
+          for (int m = 0; m < nm; ++m) {
+            const float w = jb.c_state * expf(ld * (n - m0 - m));
+            float z[8];
+            unpack8(zm + 16 * m, z);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = lane + 32 * i;
+              const float y = r < da ? w * __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(ym)[m * kDecayMaxD + r]) : 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) R[i][e] = fmaf(y, z[e], R[i][e]);
+            }
+          }
+        }
+      }
+      for (int p0 = start; p0 < end; p0 += 32) {
+        const int pr = p0 + lane;
+        const __nv_bfloat16* x = X + tok(min(pr, end - 1)) * jb.xs[2];
+        float acc[8] = {}, o[8] = {};
+        for (int q0 = start; q0 < min(p0 + 32, end); q0 += 32) {
+          const int nq = min(32, end - q0);
+          stage(q0, nq);
+          for (int m = 0; m < nq; ++m) {
+            float s = 0.f;
+            for (int k = 0; k < da; k += 8) {
+              float xv[8], yv[8];
+              unpack8(x + k, xv);
+              unpack8(ym + 2 * (m * kDecayMaxD + k), yv);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) s = fmaf(xv[e], yv[e], s);
+            }
+            if (q0 + m <= pr) {
+              const float w = jb.c_intra * expf(ld * (pr - q0 - m)) * s;
+              float z[8];
+              unpack8(zm + 16 * m, z);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, z[e], acc[e]);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          for (int r = 0; r < min(32, da - 32 * i); ++r) {
+            const float xr = __bfloat162float(x[32 * i + r]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = fmaf(xr, __shfl_sync(0xffffffffu, R[i][e], r), o[e]);
+          }
+        const float f = jb.c_inter * expf(ld * (pr - start));
+        __nv_bfloat16* O = jb.O + b * jb.os[0] + h * jb.os[1] + tok(min(pr, end - 1)) * jb.os[2] + c0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (from[e] == start && pr < first[e]) O[e] = __float2bfloat16_rn(fmaf(f, o[e], acc[e]));
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (from[e] == start) from[e] = first[e];
+    }
+  }
+}
+
 template <int DP, bool STATE>
 __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const __grid_constant__ TcArgs a) {
   using C = Cfg<DP, STATE>;
@@ -306,6 +473,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffBar + 368);
   volatile int* gave_up = reinterpret_cast<volatile int*>(sm + C::kOffBar + 372);
+  volatile int* odd = gave_up + 1;   // the segment's last row is not finite
   float* pb = reinterpret_cast<float*>(sm + C::kOffPb);        // rev: l^c, else l^(31-c), c = 0 .. 31
   float* pi = reinterpret_cast<float*>(sm + C::kOffPi) + 32;   // c_intra l^0 .. c_intra l^127 after 32 zeros
   uint2* wt = reinterpret_cast<uint2*>(sm + C::kOffWt);        // c_state l^n in two bf16 parts, each twice in a word
@@ -334,6 +502,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
                                                                                          : 1);
     mbar_init_fence();
     *gave_up = 0;
+    *odd = 0;
     // the first chunk is under way while the rest is set up
     load(&jb.y, 0, C::kNY, kFullY, kEmptyY, 0);
     load(&jb.z, C::kOffZ, C::kNZ, kFullZ, kEmptyZ, 0);
@@ -354,6 +523,15 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // the two warps that issue the products, at their end: they have the registers
+  auto mend = [&](int which) {
+    __syncwarp();
+    named_bar_sync(2, 320);
+    if (*odd) {
+      if (!*gave_up) before_odd(a, which, 2, sm);   // the tiles are done with
+      named_bar_sync(2, 320);
+    }
+  };
   if (warp == C::kLoad) {
     if (lane == 0) {
       // y, z, x of every chunk in turn, each tensor in a ring of its own
@@ -430,6 +608,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
       }
       commit_by(lead, bars + kFin);
       wait.drain(kFin, 0);
+      mend(0);
     }
   } else if (warp == C::kMma) {
     const uint32_t lead = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -465,6 +644,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
     }
     commit_by(lead, bars + kFin + 1);
     wait.drain(kFin + 1, 0);
+    if (!STATE) mend(1);
   } else if (!STATE && warp < C::kY0) {
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsP));
     if (rev)
@@ -584,7 +764,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
     __nv_bfloat16* o = STATE ? nullptr : jb.O + b * jb.os[0] + h * jb.os[1] + col + (long long)(chunk(0) * kC + i) * ts;
     const long long o_step = (rev ? -kC : kC) * ts;
     float f = STATE ? 0.f : c_inter * expf(ld * (rev ? kC - 1 - i : i));
-    auto epilogue = [&](int k) {
+    auto epilogue = [&](int k, auto last) {
       const int nv = valid(chunk(k));
       float fk = f;
       if (rev && nv < kC) fk = i < nv ? c_inter * expf(ld * (nv - 1 - i)) : 0.f;
@@ -607,9 +787,14 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
 #pragma unroll
         for (int g = 0; g < NT; g += 16) {
           uint32_t w[8];
+          uint64_t nan = 0;   // stays zero unless an output is not finite
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            w[e] = packf2(fma2(ff, f2(x[g + 2 * e], x[g + 2 * e + 1]), f2(z[g + 2 * e], z[g + 2 * e + 1])));
+          for (int e = 0; e < 8; ++e) {
+            const uint64_t v = fma2(ff, f2(x[g + 2 * e], x[g + 2 * e + 1]), f2(z[g + 2 * e], z[g + 2 * e + 1]));
+            if (decltype(last)::value) nan = fma2(v, 0ull, nan);
+            w[e] = packf2(v);
+          }
+          if (decltype(last)::value && i < nv && f2_lo(nan) + f2_hi(nan) != 0.f) *odd = 1;
           if (i < nv && c0 + g < left) {
             if (wide) {
               st_global_32(o + c0 + g, w);
@@ -635,10 +820,14 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + kRbReady);
-        if (k > 0) epilogue(k - 1);
+        if (k > 0) epilogue(k - 1, std::false_type());
       }
     }
-    if (!STATE) epilogue(n - 1);
+    if (!STATE) {
+      epilogue(n - 1, std::true_type());
+      named_bar_sync(2, 320);
+      if (*odd) named_bar_sync(2, 320);   // before_odd needs the state that may be written in place
+    }
     if (STATE || ends) {
       update(n - 1);
       float* dst = STATE ? jb.local + ((size_t)u * a.segs + seg) * dd : jb.fin + u * dd;
@@ -849,6 +1038,12 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
     if (!maps(&o, a, j, true)) return cudaErrorInvalidValue;
     o.O = static_cast<__nv_bfloat16*>(j.O);
     memcpy(o.os, j.os, sizeof(o.os));
+    o.X = static_cast<const __nv_bfloat16*>(j.X);
+    o.Y = static_cast<const __nv_bfloat16*>(j.Y);
+    o.Z = static_cast<const __nv_bfloat16*>(j.Z);
+    memcpy(o.xs, j.xs, sizeof(o.xs));
+    memcpy(o.ys, j.ys, sizeof(o.ys));
+    memcpy(o.zs, j.zs, sizeof(o.zs));
     o.init = j.init;
     o.seg_init = a.ws + (i == 0 ? 0 : states);
     o.fin = j.fin;

@@ -435,7 +435,7 @@ def test_two_graphs_replayed_at_once():
         assert all(torch.equal(a, b) for a, b in zip(w, o) if a is not None)
 
 
-ONE_SIDED = [F32]
+ONE_SIDED = [F32, BF]
 ODD = [float("nan"), float("inf"), -float("inf")]
 
 
