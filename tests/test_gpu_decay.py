@@ -505,3 +505,31 @@ def test_backward_does_not_see_the_other_side(B, H, N, dk, dv, at, dtype):
             if name in "kv":
                 _check_state(got[3], ref[3], T[3], N, dtype, "dS0")
     assert decay.decay_status() == 0
+
+
+LONG = [(40, 64, "bnhd"), (72, 128, "packed"), (128, 24, "bhnd"), (64, 16, "packed")]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv,order", LONG)
+def test_segments_of_unequal_widths(dk, dv, order, dtype):
+    """Long and ragged sequences of few units, cut in segments, with dk and dv apart: forward and backward."""
+    lengths = [2300, 1281, 0, 1]
+    _run_forward(4, 2, 2300, dk, dv, dtype, order, True, lengths, "slow", seed=dk)
+    _run_backward(4, 2, 2300, dk, dv, dtype, order, True, lengths, "slow", seed=dv)
+
+
+def test_bf16_gradients_beyond_32_bits():
+    """All tensors in one buffer, batches more than 2^31 elements apart, gradients among them."""
+    d, H, N, far = 64, 2, 150, (1 << 31) + 64
+    g = torch.Generator("cuda").manual_seed(10)
+    buf = torch.empty(far + 8 * H * N * d, dtype=BF, device="cuda")
+    t = [buf.as_strided((2, H, N, d), (far, N * d, d, 1), i * H * N * d) for i in range(7)]
+    for x in t[:4]:
+        x.copy_(torch.randn((2, H, N, d), generator=g, device="cuda"))
+    q, k, v, dO, dQ, dK, dV = t
+    ld = _log_decay(H)
+    got = decay.decay_backward(q, k, v, ld, dO, dQ=dQ, dK=dK, dV=dV)
+    want = decay.decay_backward(q.contiguous(), k.contiguous(), v.contiguous(), ld, dO.contiguous())
+    for a, b, into in zip(got, want, (dQ, dK, dV)):
+        assert a is into and torch.equal(a, b)

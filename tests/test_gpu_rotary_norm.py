@@ -350,6 +350,32 @@ def test_activations_from_end_to_end(B, N, C, G, act, dtype):
     assert not bad.any(), f"{int(bad.sum())}, z from {float(z[bad].min())} to {float(z[bad].max())}"
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,N,C,G", [(5, 1, 64, 4), (3, 49, 40, 4), (2, 257, 72, 9), (3, 130, 10, 1), (2, 3136, 64, 32), (1, 6000, 24, 3)])
+def test_values_that_are_not_finite_stay_in_their_group(B, N, C, G, dtype):
+    """NaN and infinities in one group of one sample, of x or dy: every other group as without them, bit by bit, and
+    dgamma, dbeta of the other groups' channels."""
+    x, gamma, beta, g = _norm_inputs(B, N, C, dtype, True, 0.5, 3)
+    dy = torch.randn((B, N, C), generator=g, device="cuda").to(dtype)
+    at, n = G // 2, C // G
+    mine = torch.zeros((B, N, C), dtype=torch.bool, device="cuda")
+    mine[-1, :, at * n:(at + 1) * n] = True
+    y, m, r = decay.group_norm(x, G, gamma, beta, act="silu")
+    grads = decay.group_norm_backward(x, dy, m, r, G, gamma, beta, act="silu")
+    for odd in (float("nan"), float("inf"), -float("inf")):
+        bad = x.clone()
+        bad[-1, N // 2, at * n] = odd
+        y1, m1, r1 = decay.group_norm(bad, G, gamma, beta, act="silu")
+        assert torch.equal(y1[~mine], y[~mine]) and not torch.isfinite(y1[mine]).any()
+        assert torch.equal(torch.isfinite(m1), torch.isfinite(r1)) and int((~torch.isfinite(m1)).sum()) == 1
+        bad_dy = dy.clone()
+        bad_dy[-1, N // 2, at * n] = odd
+        for args in ((bad, dy, m1, r1), (x, bad_dy, m, r)):
+            dx, dg, db = decay.group_norm_backward(*args, G, gamma, beta, act="silu")
+            assert torch.equal(dx[~mine], grads[0][~mine]) and not torch.isfinite(dx[mine]).any()
+            assert torch.equal(dg[~mine[-1, 0]], grads[1][~mine[-1, 0]]) and torch.equal(db[~mine[-1, 0]], grads[2][~mine[-1, 0]])
+
+
 # ---- the layer -----------------------------------------------------------------------------------------
 
 def _layer(B, N, H, dk, dv, seed=0):
@@ -434,3 +460,50 @@ def test_norm_graphs_replayed_at_once():
     torch.cuda.synchronize()
     for w, o in zip(want, got):
         assert all(torch.equal(a, b) for a, b in zip(w, o))
+
+
+def test_layer_bf16_ragged_values():
+    """Every stage of a ragged bf16 batch against the 64-bit form of the same stage on its valid rows: rotation, the
+    norm of o (the tolerances above), o (2^-8 of the sum of absolute terms twice over: weights and state, output), then
+    the gradients of the whole backward from the saved tensors. Its roundings to bf16, each at most 2^-8 of what it
+    rounds: dO, the weights or state, dq / dk / dv, the rotation. Independent of each other, so normwise within
+    sqrt(4) 2^-8 (the rounding errors' own average, 2^-8 / sqrt 3, is the margin)."""
+    B, N, H, dk, dv = 3, 300, 4, 64, 48
+    mod, q, k, v, pos, g = _layer(B, N, H, dk, dv, 2)
+    q, k, v = (t.to(BF) for t in (q, k, v))
+    lens = [300, 0, 131]
+    lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    S0 = torch.randn((B, H, dk, dv), generator=g, device="cuda")
+    y, S, saved = mod.forward(q, k, v, pos, S0=S0, lengths=lengths)
+    qr, kr, _, o = saved[:4]
+    valid = torch.arange(N, device="cuda")[None, :] < lengths[:, None]
+    for src, out in ((q, qr), (k, kr)):
+        ref = R.rotate(src.transpose(1, 2).double(), pos, mod.freqs, True, mod.mscale, False)
+        T = mod.mscale * 2 * src.double().abs().transpose(1, 2).amax(-1, keepdim=True)
+        assert ((out.double() - ref).abs() <= 8 * U * T + 2.0 ** -8 * ref.abs()).all()
+    a = [t.double() for t in (qr, kr, v.transpose(1, 2))]
+    ro, rS = R.decay_forward(*a, mod.log_decay, dk ** -0.5, S0.double(), lengths)
+    To, TS = R.decay_forward(*(t.abs() for t in a), mod.log_decay, dk ** -0.5, S0.double().abs(), lengths)
+    assert ((o.transpose(1, 2).double() - ro).abs() <= 2.0 ** -8 * (ro.abs() + To * (1 + 2.0 ** -6))).all()
+    assert ((S.double() - rS).abs() <= 2.0 ** -15 * TS).all()
+    ry, _, _ = R.group_norm(o.double().view(B * N, 1, H * dv), H, mod.gamma.double(), mod.beta.double(), mod.eps, mod.act)
+    err, xh, _, _ = _xhat_error(o.double().view(B * N, 1, H * dv), H, mod.eps)
+    bound = 2 * (err * mod.gamma.double().abs() + 16 * U * (xh.abs() + 1)) + 16 * U * ry.abs() + 2.0 ** -8 * ry.abs()
+    assert ((y.view(B * N, 1, -1).double() - ry).abs() <= bound).all()
+
+    dy = torch.randn((B, N, H * dv), generator=g, device="cuda").to(BF) * valid[..., None]
+    dS = torch.randn(S.shape, generator=g, device="cuda")
+    got = mod.backward(saved, dy, dS)
+    leaf_o, ga, be = o.double().view(B * N, 1, -1).requires_grad_(), mod.gamma.double().requires_grad_(), mod.beta.double().requires_grad_()
+    z, _, _ = R.group_norm(leaf_o, H, ga, be, mod.eps, mod.act)
+    do, dga, dbe = torch.autograd.grad((z * dy.double().view(B * N, 1, -1)).sum(), (leaf_o, ga, be))
+    do = do.view(B, N, H, dv).transpose(1, 2)
+    dq, dk_, dv_, dS0 = R.decay_grads(*a, mod.log_decay, dk ** -0.5, S0.double(), lengths, do, dS.double())
+    dq, dk_ = (R.rotate(t, pos, mod.freqs, True, mod.mscale, True) for t in (dq, dk_))
+    want = [dq.transpose(1, 2), dk_.transpose(1, 2), dv_.transpose(1, 2), dS0, dga, dbe]
+    for name, x, w, tol in zip(("dq", "dk", "dv", "dS0", "dgamma", "dbeta"), got, want, [2 * 2.0 ** -8] * 4 + [2.0 ** -16] * 2):
+        assert x.shape == w.shape
+        rel = float((x.double() - w).norm() / w.norm())
+        assert rel <= tol, f"{name}: {rel:.2e}"
+        if name in ("dq", "dk", "dv"):
+            assert (x[~valid] == 0).all(), name
