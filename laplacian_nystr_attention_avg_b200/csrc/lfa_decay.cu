@@ -376,7 +376,7 @@ cudaError_t run_core(const CoreArgs& c, cudaStream_t st) {
 }
 
 cudaError_t launch_core(const DecayArgs& a, cudaStream_t st) {
-  const DecaySplit sp = decay_split(a.B, a.heads, a.N, a.njobs, LFA_F32);
+  const DecaySplit sp = decay_split(a, LFA_F32);
   CoreArgs c;
   memset(&c, 0, sizeof(c));
   c.a = a;

@@ -941,22 +941,42 @@ cudaError_t run(const TcArgs& a, int dp, int units, int njobs, cudaStream_t st) 
 
 }  // namespace
 
-// bf16: one CTA fills an SM. With fewer than 148 of them the sequences are cut so that about 148 run at once, in
-// segments of at least 4 chunks (below that the extra launches and the second reading of y and z cost more).
-// fp32: blocks of 256 threads share an SM, and arithmetic bounds them, so units of fewer blocks than SMs are cut
-// for two rounds of two blocks an SM, down to single chunks (64 units x 784 tokens, dk 64: one round 109 us, two 96).
-DecaySplit decay_split(int B, int heads, int N, int njobs, int dtype) {
+// How the sequences are cut. bf16: one CTA fills an SM; fewer than 148 of them (units x runs) are cut so that about 148
+// run at once, in segments of at least 4 chunks (below that the extra launches and the second reading of y and z cost
+// more). 4096 tokens of 74 units in two segments 103 us at 128 channels, 70 at 64; 80 units uncut 111 and 66.
+// fp32: blocks (64 columns of a unit's run) are bound by arithmetic, and the states take it to 1.5 (backward 1.3) times.
+// So fewer than 148 runs are cut, into about 592 segments in all, if uncut blocks would leave more than
+// that idle. At more than 64 rows of the state one block fills an SM (dk = dv = 128, forward, 1024 tokens: 147 units
+// uncut 652 us, cut 852; 64 units 328 and 415; 36 units x 2048 cut 476, uncut 647; backward 24 units x 2048 uncut 648,
+// cut 815, 36 units 1150 cut, 1287 uncut). Below, two share one, and both together do a third more (64 units x 784
+// tokens, dk = dv = 64: cut 94 us, uncut 151; 147 units of dk 32 uncut 102, cut 118).
+DecaySplit decay_split(int B, int heads, int N, int dk, int dv, int njobs, int dtype) {
   const int nch = ceil_div(N, kC);
-  const long long ctas = (long long)B * heads * njobs;
-  int segs = 1;
-  if (ctas < 148) segs = (int)((dtype == LFA_BF16 ? 148 : 592) / ctas);
-  const int most = dtype == LFA_BF16 ? nch / 4 : nch;
-  if (segs > most) segs = most;
+  const long long units = (long long)B * heads, runs = units * njobs;
+  long long segs = 1;
+  if (dtype == LFA_BF16) {
+    if (runs < 148) segs = 148 / runs;
+    segs = segs < nch / 4 ? segs : nch / 4;
+  } else if (runs < 148) {
+    // a forward's run has dk rows and dv columns; a backward's have dv, dv, dk rows and dk, dk, dv columns
+    const bool bwd = njobs > 1;
+    const int rows = bwd && dv > dk ? dv : dk, ck = ceil_div(dk, 64), cv = ceil_div(dv, 64);
+    const long long blocks = units * (bwd ? 2 * ck + cv : cv);
+    const long long whole = bwd ? units * (2 * ck * dv + cv * dk) / rows : blocks;   // as many of `rows` rows
+    const long long full = rows > 64 ? (blocks + 147) / 148 * 148 : 196;
+    if (bwd ? 13 * whole < 10 * full : 3 * whole < 2 * full) segs = 592 / runs;
+    segs = segs < nch ? segs : nch;
+  }
   if (segs < 1) segs = 1;
   DecaySplit s;
-  s.seg_chunks = ceil_div(nch, segs);
+  s.seg_chunks = ceil_div(nch, (int)segs);
   s.segs = ceil_div(nch, s.seg_chunks);
   return s;
+}
+DecaySplit decay_split(const DecayArgs& a, int dtype) {
+  const DecayJob& j = a.job[0];   // the forward's run, or dQ's with k in z's place
+  return a.njobs > 1 ? decay_split(a.B, a.heads, a.N, j.db, j.da, a.njobs, dtype)
+                     : decay_split(a.B, a.heads, a.N, j.da, j.db, a.njobs, dtype);
 }
 
 cudaError_t launch_prefix(const DecayArgs& a, const DecaySplit& sp, const PrefixRun* r, int n, cudaStream_t st) {
@@ -979,7 +999,7 @@ cudaError_t launch_prefix(const DecayArgs& a, const DecaySplit& sp, const Prefix
 }
 
 size_t decay_workspace_floats(int B, int heads, int N, int dk, int dv, int njobs, int dtype) {
-  const DecaySplit s = decay_split(B, heads, N, njobs, dtype);
+  const DecaySplit s = decay_split(B, heads, N, dk, dv, njobs, dtype);
   return s.segs > 1 ? (size_t)(njobs > 1 ? 2 : 1) * B * heads * s.segs * dk * dv : 0;
 }
 
@@ -996,7 +1016,7 @@ cudaError_t decay_take_status(int* out, cudaStream_t st) {
 }
 
 cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
-  const DecaySplit sp = decay_split(a.B, a.heads, a.N, a.njobs, LFA_BF16);
+  const DecaySplit sp = decay_split(a, LFA_BF16);
   const int units = a.B * a.heads;
   TcArgs t;
   memset(&t, 0, sizeof(t));

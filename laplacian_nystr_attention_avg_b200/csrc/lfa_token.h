@@ -47,7 +47,8 @@ struct DecayArgs {
 struct DecaySplit {
   int segs, seg_chunks;
 };
-DecaySplit decay_split(int B, int heads, int N, int njobs, int dtype);
+DecaySplit decay_split(int B, int heads, int N, int dk, int dv, int njobs, int dtype);
+DecaySplit decay_split(const DecayArgs& a, int dtype);
 size_t decay_workspace_floats(int B, int heads, int N, int dk, int dv, int njobs, int dtype);
 
 struct DecayStepArgs {

@@ -296,3 +296,15 @@ def test_norm_backward_workspace_follows_the_data(lib, B, C, G, dtype, es):
     """Channel sums are two floats per channel and record; there are never more than twice as many records as rows."""
     n = lib.lfa_group_norm_workspace_size(_nc(B=B, N=1, C=C, groups=G, dtype=dtype), 1)
     assert 256 < n <= 512 + 2 * B * 2 * C * 4
+
+
+@pytest.mark.parametrize("units,N,dk,dv,bwd,segs", [
+    (147, 1024, 128, 128, 0, 1), (64, 1024, 128, 128, 0, 1), (37, 1024, 128, 128, 0, 8), (8, 8000, 128, 128, 0, 63),
+    (24, 2048, 128, 128, 1, 1), (36, 2048, 128, 128, 1, 4), (147, 784, 32, 64, 0, 1), (64, 784, 64, 64, 0, 7),
+    (64, 784, 32, 64, 0, 7), (12, 2048, 64, 128, 1, 16), (30, 2048, 128, 64, 1, 6), (30, 2048, 64, 128, 1, 6)])
+def test_fp32_segments_count_blocks(lib, units, N, dk, dv, bwd, segs):
+    """A block takes 64 columns of a unit's run, and at more than 64 rows of the state one fills an SM: units whose
+    blocks fill most of the SMs by themselves are not cut. The workspace holds one state (backward: two) per segment of a cut call."""
+    n = lib.lfa_decay_workspace_size(_dc(B=units, heads=1, N=N, dk=dk, dv=dv, dtype=lfa.LFA_F32), bwd)
+    states = units * segs * dk * dv * 4 * (2 if bwd else 1)
+    assert n == 256 + (states if segs > 1 else 0)
