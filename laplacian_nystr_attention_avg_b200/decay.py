@@ -538,7 +538,7 @@ class DecayAttention:
         B, N, heads, dv = v.shape
         flat = (B * N, 1, heads * dv)
         with _in(v.get_device(), stream):
-            do, dgamma, dbeta = group_norm_backward(o.view(flat), dy.reshape(flat), mean, rstd, heads, self.gamma,
+            do, dgamma, dbeta = group_norm_backward(o.view(flat), dy.reshape(flat).contiguous(), mean, rstd, heads, self.gamma,
                                                     self.beta, eps=self.eps, act=self.act)
             dq, dk, dvt, dS0 = decay_backward(qr, kr, v.transpose(1, 2), self.log_decay,
                                               do.view(v.shape).transpose(1, 2), scale=self.scale, S0=S0,

@@ -507,3 +507,14 @@ def test_layer_bf16_ragged_values():
         assert rel <= tol, f"{name}: {rel:.2e}"
         if name in ("dq", "dk", "dv"):
             assert (x[~valid] == 0).all(), name
+
+
+def test_layer_takes_gradients_of_any_layout():
+    """dy of a sum is one broadcast number, and a slice of a wider tensor has gaps: as their contiguous copies."""
+    B, N, H, dk, dv = 2, 70, 4, 32, 64
+    mod, q, k, v, pos, g = _layer(B, N, H, dk, dv, 3)
+    y, S, saved = mod.forward(q, k, v, pos)
+    wide = torch.randn((B, N, 2 * H * dv), generator=g, device="cuda")
+    for dy in (torch.ones((), device="cuda").expand(B, N, H * dv), wide[..., H * dv:], wide.view(B, 2 * H * dv, N)[:, :H * dv].transpose(1, 2)):
+        got, want = mod.backward(saved, dy), mod.backward(saved, dy.contiguous())
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
