@@ -77,7 +77,7 @@ __device__ __forceinline__ Raw<VB> raw_make(const uint64_t* v) {
 // Bound by the bytes: 4 x 4096 tokens, 2 x 16 heads of 128 (268 MB) in 50 us, 5.4 TB/s, whether 64, 96 or 128 channels
 // turn; a plain copy of them takes 47.
 constexpr int kRThreads = 256;
-constexpr int kWave = 3 * 148;   // blocks of 256 threads with 80 registers that run at once
+constexpr int rotary_blocks(int mode) { return mode == 0 ? 3 : 5; }   // an SM at a time: 80 registers a thread, or 48
 constexpr int kRHeads = 2;   // heads read at once, one such group ahead
 
 __device__ __forceinline__ float2 turn(const RotaryArgs& a, double pos, int i) {
@@ -96,7 +96,7 @@ __host__ __device__ __forceinline__ int rotary_units(int d, int rot) {
 }
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kRThreads, MODE == 0 ? 3 : 5) k_rotary(const __grid_constant__ RotaryArgs a, int units, int tokens,
+__global__ void __launch_bounds__(kRThreads, rotary_blocks(MODE)) k_rotary(const __grid_constant__ RotaryArgs a, int units, int tokens,
                                                       int heads_each) {
   constexpr int V = 16 / sizeof(T), NP = MODE == 0 ? V : MODE == 1 ? V / 2 : 1;   // pairs of a unit
   const int tl = threadIdx.x / units, unit = threadIdx.x - tl * units, tok = blockIdx.x * tokens + tl;
@@ -194,8 +194,9 @@ void rotary_launch(const RotaryArgs& a, cudaStream_t st) {
   const int units = rotary_units<T, MODE>(a.d, a.rot), tokens = kRThreads / units;   // units <= 256
   const int tiles = ceil_div(a.B * a.N, tokens), all = a.heads + a.heads2;
   // Heads are split over blocks, which form the angles once each (worth about three heads): as many parts as give
-  // the shortest run of whole waves, three blocks an SM at a time (4 x 4096 tokens, 32 heads: one part 57 us in
-  // 1.5 waves, two 51 us in 3).
+  // the shortest run of whole waves (half layout, 4 x 4096 tokens, 32 heads: one part 57 us in 1.5 waves, two 51 us
+  // in 3).
+  constexpr int kWave = rotary_blocks(MODE) * 148;
   int each = all;
   long long best = 0;
   for (int parts = 1; parts <= all; ++parts) {
