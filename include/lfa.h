@@ -356,8 +356,8 @@ const char* lfa_forward_path(lfa_handle h);
  * use (-inf: only the token itself). States are fp32 [B][heads][dk][dv], contiguous.
  * Arithmetic: fp32 tensors on CUDA cores in fp32. bf16 tensors: the token products are bf16-operand
  * tensor-core products with fp32 accumulation, in which the decayed q.k weights and the state that q
- * meets are rounded to bf16 once; the carried state is fp32 and takes k's decayed rows as the sum of
- * two bf16 parts, so that it is about 4e-6 of its norm off, however long the sequence.
+ * meets are rounded to bf16 once; the carried state is fp32 and takes k's decayed rows as the sum of bf16 parts:
+ * a state that is returned (S_out, dS0) is about 5e-7 of its norm off, however long the sequence.
  * Values that are not finite: whatever the formula makes of them is not finite either (an infinity may come out as
  * a NaN); nothing else is touched, outputs before such a token (gradients on the side that does not meet it) included. */
 typedef struct {

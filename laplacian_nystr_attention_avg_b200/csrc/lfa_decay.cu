@@ -419,6 +419,8 @@ int state_runs(const DecayArgs& a, DecayJob* jobs, PrefixRun* p) {
     p[i].init = j.init;
     p[i].rev = j.rev;
     p[i].init_decays = j.init_decays;
+    p[i].fin = nullptr;
+    p[i].fin_sub = 0;
     jobs[i] = j;
   }
   return n;

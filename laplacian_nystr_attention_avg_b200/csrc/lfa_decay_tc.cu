@@ -7,11 +7,13 @@
 //   Oz = P z,  Ox = x bf16(R)               (M 128, N db; K 128 and K da)
 //   O  = Oz + c_inter l^i Ox                (epilogue warps, fp32, rounded once)
 //   D  = (y c_state l^(n-j))^T z            (M da, N db, K 128 tokens), R' = l^n R + D   (state warps)
-// The decayed rows of y enter as two bf16 parts (value and remainder, one product each): a state is 3.9e-6 of its norm
-// off, after 8 tokens as after 4096, beside the 2^-8 of every bf16 output that is read from it (a third part left
-// 1.4e-6, the rest being the tensor cores' own sums, and cost 16 to 20 % of the time). An infinity has a NaN as its
-// remainder: states and outputs that the formula makes infinite may be NaN. D starts from zero in every
-// chunk and is added to R by CUDA cores: tensor-core accumulation truncates and would drift over thousands of chunks.
+// The decayed rows of y enter as bf16 parts, one product each. Where R only meets x, which rounds it to bf16, two parts
+// leave 4e-6 of its norm. Runs that return a state take three, the 24 bits of an fp32 product: such a state is 0.5e-6
+// off, after 8 tokens as after 4096, of which the tensor cores' own sums are the most. (8 x 16 x 4096 tokens x 128: 141
+// us with a state, 121 without; at 64 channels 90 and 72, where the third product has zeros in half of its rows; in
+// segments only the states' kernel has it: 1 x 8 x 65536 118 and 107.) An infinity has a NaN as its remainder: states and
+// outputs that the formula makes infinite may be NaN. D starts from zero in every chunk and is added to R by CUDA cores:
+// tensor-core accumulation truncates and would drift over thousands of chunks.
 // All widths are padded to DP = 64 or 128 by TMA's zero fill.
 //
 // Warps: 4 or 8 for P, 4 or 8 for y's decayed rows, 8 for R and the epilogue, one each to issue TMA loads, the
@@ -25,8 +27,9 @@
 // second set of S at 64; a unit's three backward runs on neighbouring SMs (they read the same tiles at the same time:
 // 188 instead of 178 us for 128 units x 2048 tokens x 128, 120 instead of 104 at 64).
 //
-// Few units over long sequences: segments run at once. k_decay_tc<.., true> sums up each segment's own
-// state, k_decay_prefix carries them over the segments, and the main kernel starts every segment from its state.
+// Few units over long sequences: segments run at once. k_decay_tc<.., true, ..> sums up each segment's own
+// state, k_decay_prefix carries them over the segments and writes the state after the last, and the main kernel starts
+// every segment from its state.
 #include <string.h>
 
 #include <type_traits>
@@ -55,6 +58,7 @@ struct TcJob {
   float* fin;
   float* local;           // state kernel: sums of each segment, [units][segs]
   int da, db, rev, trans, init_decays, fin_sub;
+  int third;              // y's decayed rows in three parts (PARTS 3)
   int wide;               // O's rows are whole, aligned 32-byte sectors
   const __nv_bfloat16 *X, *Y, *Z;   // what the maps read, for before_odd
   long long xs[3], ys[3], zs[3];
@@ -67,7 +71,7 @@ struct TcArgs {
   int heads, N, segs, seg_chunks;
 };
 
-template <int DP, bool STATE>
+template <int DP, bool STATE, int PARTS>
 struct Cfg {
   static constexpr int kTile = DP / 64 * kPanelB;   // bytes of a token tile
   // rings of tiles. At 128 channels five fit: x is done with first (S, then Ox), y and z are held longer
@@ -77,16 +81,18 @@ struct Cfg {
   static constexpr int kOffX = kNY * kTile;
   static constexpr int kOffZ = kOffX + kNX * kTile;
   static constexpr int kOffPart = kOffZ + kNZ * kTile;
-  // y's decayed rows are formed in steps of kStep tokens, kVec 16-byte vectors per thread, in two buffers of two parts
-  static constexpr int kStep = 4096 / DP;
+  // y's decayed rows are formed in steps of kStep tokens, kVec 16-byte vectors per thread, in two buffers of PARTS parts
+  static constexpr int kStep = (PARTS == 3 && !STATE ? 2048 : 4096) / DP;
   static constexpr int kSteps = kC / kStep;
   static constexpr int kYW = STATE && DP == 64 ? 8 : 4;   // warps that form them
   static constexpr int kVec = kStep * DP / 8 / (32 * kYW);
   static constexpr int kPart = kStep * DP * 2;             // bytes of one part of a step
   // DP 64: the two parts share the product's 128 rows (M = 64 runs at half the speed): rows 64 .. 127 of D, and of R
   // with it, are the second part's. Their sum is formed in x R's product (two tiles of R) and where a state is written.
+  // A third part has 16 tokens of zeros for company.
   static constexpr bool kStack = DP == 64;
-  static constexpr int kOffR = kOffPart + 4 * kPart;
+  static constexpr int kOffZero = kOffPart + 2 * PARTS * kPart;
+  static constexpr int kOffR = kOffZero + (kStack && PARTS == 3 ? 16 * 128 : 0);
   static constexpr int kOffBar = kOffR + (STATE ? 0 : DP * DP * 2 * (kStack ? 2 : 1));
   static constexpr int kOffPb = kOffBar + 384;
   static constexpr int kOffPi = kOffPb + 4 * 32;
@@ -181,8 +187,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// y w for a pair y of bf16 and w = w.x + w.y in bf16 parts, as a + b in bf16: a = y w.x rounded; its remainder
-// y w.x - a is a bf16 itself (8 by 8 bits make 16). About 2^-17 of y w is left out.
+__device__ __forceinline__ uint32_t packf2(uint64_t v) { return pack2(f2_lo(v), f2_hi(v)); }
+// y w for a pair y of bf16 as a sum of bf16 parts. Two: w = w.x + w.y in bf16 parts; a = y w.x rounded, its remainder
+// y w.x - a is a bf16 itself (8 by 8 bits make 16), and about 2^-17 of y w is left out. Three: w in fp32, the
+// product's 24 bits in turn.
 __device__ __forceinline__ __nv_bfloat162 as_b2(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); }
 __device__ __forceinline__ uint32_t as_u(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 __device__ __forceinline__ void split(uint32_t y, uint2 w, uint32_t& a, uint32_t& b) {
@@ -191,6 +199,15 @@ __device__ __forceinline__ void split(uint32_t y, uint2 w, uint32_t& a, uint32_t
   a = as_u(hi);
   b = as_u(__hfma2(y2, wy, __hfma2(y2, wx, __hneg2(hi))));
 }
+__device__ __forceinline__ void split3(uint32_t y, uint2 w, uint32_t& a, uint32_t& b, uint32_t& c) {
+  const uint64_t less = f2(-1.f, -1.f);
+  uint64_t v = mul2(f2(y << 16, y & 0xffff0000u), f2(w.x, w.y));
+  a = packf2(v);
+  v = fma2(f2(a << 16, a & 0xffff0000u), less, v);
+  b = packf2(v);
+  v = fma2(f2(b << 16, b & 0xffff0000u), less, v);
+  c = packf2(v);
+}
 
 // one 32-byte store (a whole sector)
 __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
@@ -198,7 +215,6 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
                "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-__device__ __forceinline__ uint32_t packf2(uint64_t v) { return pack2(f2_lo(v), f2_hi(v)); }
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -445,9 +461,9 @@ __device__ __forceinline__ void before_odd(const TcArgs& a, int warp, int warps,
   }
 }
 
-template <int DP, bool STATE>
-__global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const __grid_constant__ TcArgs a) {
-  using C = Cfg<DP, STATE>;
+template <int DP, bool STATE, int PARTS>
+__global__ void __launch_bounds__(Cfg<DP, STATE, PARTS>::kThreads, 1) k_decay_tc(const __grid_constant__ TcArgs a) {
+  using C = Cfg<DP, STATE, PARTS>;
   extern __shared__ __align__(1024) unsigned char sm[];
   const TcJob& jb = a.job[blockIdx.z];
   const int u = blockIdx.x, seg = blockIdx.y, b = u / a.heads, h = u % a.heads;
@@ -458,12 +474,14 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   const bool rev = jb.rev;
   const size_t dd = (size_t)da * db;
   if (STATE) let_next_start();
+  const bool third = PARTS == 3 && jb.third;
   if (n <= 0) {
+    if (!STATE) wait_for_previous();   // a call is over when all its launches are
     if (!STATE && L == 0 && seg == 0 && jb.fin)
       for (size_t e = t; e < dd; e += C::kThreads) jb.fin[u * dd + e] = jb.init ? jb.init[u * dd + e] : 0.f;
     return;
   }
-  if (STATE && (rev ? seg == 0 : c_hi == nch)) return;   // nothing follows this segment
+  if (STATE && !jb.fin && (rev ? seg == 0 : c_hi == nch)) return;   // nothing follows this segment
   const bool ends = !STATE && jb.fin && (rev ? seg == 0 : c_hi == nch);
 
   if ((smem_u32(sm) & 1023u) != 0) {   // the swizzle needs it; the declaration asks for it
@@ -476,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
   volatile int* odd = gave_up + 1;   // the segment's last row is not finite
   float* pb = reinterpret_cast<float*>(sm + C::kOffPb);        // rev: l^c, else l^(31-c), c = 0 .. 31
   float* pi = reinterpret_cast<float*>(sm + C::kOffPi) + 32;   // c_intra l^0 .. c_intra l^127 after 32 zeros
-  uint2* wt = reinterpret_cast<uint2*>(sm + C::kOffWt);        // c_state l^n in two bf16 parts, each twice in a word
+  uint2* wt = reinterpret_cast<uint2*>(sm + C::kOffWt);        // c_state l^n: two bf16 parts, each twice in a word; or fp32 twice
   const float ld = decay_log(a.log_decay[h]);
   const Waiter wait{bars, gave_up};
   // chunk of step k, and its valid tokens
@@ -517,7 +535,11 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
     }
     if (i < kC) pi[i] = jb.c_intra * w;
     const float f = jb.c_state * w, f1 = f - bf_lo(pack2(f, f));
-    wt[i] = make_uint2(pack2(f, f), pack2(f1, f1));
+    wt[i] = third ? make_uint2(__float_as_uint(f), __float_as_uint(f)) : make_uint2(pack2(f, f), pack2(f1, f1));
+  }
+  if (C::kStack && PARTS == 3) {
+    for (int i = t; i < 16 * 128 / 16; i += C::kThreads) *reinterpret_cast<uint4*>(sm + C::kOffZero + 16 * i) = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -631,11 +653,16 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
         tc_fence_after();
         if (carry) {
 #pragma unroll
-          for (int p = 0; p < (C::kStack ? 1 : 2); ++p)
+          for (int p = 0; p < PARTS; p += C::kStack ? 2 : 1) {
+            if (p == 2 && !third) break;
 #pragma unroll
-            for (int kk = 0; kk < C::kStep / 16; ++kk)
-              mma_by(lead, tm + C::kTd, d_part + (2 * buf + p) * (C::kPart / 16) + kk * 128,
-                     z + (s * C::kStep + 16 * kk) * 8, id_d, s + p + kk > 0);
+            for (int kk = 0; kk < C::kStep / 16; ++kk) {
+              const int at = (PARTS * buf + p) * C::kPart + kk * 2048;
+              uint64_t part = d_part + at / 16;
+              if (C::kStack && p == 2) part = desc_sw128(base + C::kOffPart + at, C::kOffZero - C::kOffPart - at, 1024);
+              mma_by(lead, tm + C::kTd, part, z + (s * C::kStep + 16 * kk) * 8, id_d, s + p + kk > 0);
+            }
+          }
         }
         commit_by(lead, bars + kPartFree + buf);
       }
@@ -660,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
     const uint32_t at = (ch >> 3) * kPanelB + sw128(rr, ch & 7);   // rows RS apart have the same place in the swizzle
     unsigned char* d0 = sm + C::kOffPart + (ch >> 3) * (C::kStep * 128) + sw128(rr, ch & 7);
     for (int k = 0; k < n; ++k) {
-      const int c = chunk(k), nv = valid(c), sub = (!STATE && c == nch - 1) ? jb.fin_sub : 0;
+      const int c = chunk(k), nv = valid(c), sub = c == nch - 1 ? jb.fin_sub : 0;
       const unsigned char* y = sm + (k % C::kNY) * C::kTile + at;
       unsigned char* z = sm + C::kOffZ + (k % C::kNZ) * C::kTile + at;
       const uint2* w0 = wt + (rev ? 1 : nv) - sub;   // row r: r weights on (rev) or back
@@ -687,14 +714,23 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
             }
         }
         if (g >= 2) wait(kPartFree + buf, (g >> 1) - 1);
-        unsigned char* d = d0 + 2 * buf * C::kPart;
+        unsigned char* d = d0 + PARTS * buf * C::kPart;
 #pragma unroll
         for (int e = 0; e < C::kVec; ++e) {
           uint4 hi, lo;
-          split(v[e].x, w[e], hi.x, lo.x);
-          split(v[e].y, w[e], hi.y, lo.y);
-          split(v[e].z, w[e], hi.z, lo.z);
-          split(v[e].w, w[e], hi.w, lo.w);
+          if (third) {
+            uint4 rest;
+            split3(v[e].x, w[e], hi.x, lo.x, rest.x);
+            split3(v[e].y, w[e], hi.y, lo.y, rest.y);
+            split3(v[e].z, w[e], hi.z, lo.z, rest.z);
+            split3(v[e].w, w[e], hi.w, lo.w, rest.w);
+            *reinterpret_cast<uint4*>(d + e * RS * 128 + 2 * C::kPart) = rest;
+          } else {
+            split(v[e].x, w[e], hi.x, lo.x);
+            split(v[e].y, w[e], hi.y, lo.y);
+            split(v[e].z, w[e], hi.z, lo.z);
+            split(v[e].w, w[e], hi.w, lo.w);
+          }
           *reinterpret_cast<uint4*>(d + e * RS * 128) = hi;
           *reinterpret_cast<uint4*>(d + e * RS * 128 + C::kPart) = lo;
         }
@@ -735,7 +771,7 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
     }
     Decay dec(ld * kC);
     auto update = [&](int k) {   // R after the chunk of step k
-      const int c = chunk(k), tokens = valid(c) - (!STATE && c == nch - 1 ? jb.fin_sub : 0);
+      const int c = chunk(k), tokens = valid(c) - (c == nch - 1 ? jb.fin_sub : 0);
       if (tokens < kC || k == 1) dec = Decay(ld * tokens);   // step 0 may have been the ragged one
       const uint64_t em = f2(dec.em, dec.em), mu = f2(dec.mul, dec.mul);
       wait(kDFull, k);
@@ -870,6 +906,8 @@ __global__ void __launch_bounds__(Cfg<DP, STATE>::kThreads, 1) k_decay_tc(const 
 struct PrefixArgs {
   float* st;
   const float* init[2];   // state before the run (the forward's S0, the reverse run's dS_out), or null
+  float* fin[2];          // state after it, from the last segment's own too, or null
+  int fin_sub[2];
   int rev[2], init_decays[2];
   const float* log_decay;
   const int* lengths;
@@ -882,13 +920,12 @@ __global__ void __launch_bounds__(64) k_decay_prefix(const __grid_constant__ Pre
   if (e >= a.dd) return;
   const int L = unit_length(a.lengths, u / a.heads, a.N), nch = (L + kC - 1) / kC;
   const int segs = (nch + a.seg_chunks - 1) / a.seg_chunks, span = a.seg_chunks * kC;
-  if (segs == 0) return;
   const float ld = decay_log(a.log_decay[u % a.heads]);
   float* st = a.st + ((size_t)j * gridDim.x + u) * a.segs * a.dd + e;
   float4 r = make_float4(0, 0, 0, 0);
-  if (a.init[j]) {
-    const float f = a.init_decays[j] ? expf(ld) : 1.f;
-    r = *reinterpret_cast<const float4*>(a.init[j] + (size_t)u * a.dd + e);
+  if (a.init[j]) r = *reinterpret_cast<const float4*>(a.init[j] + (size_t)u * a.dd + e);
+  if (a.init_decays[j] && segs > 0) {
+    const float f = expf(ld);
     r.x *= f; r.y *= f; r.z *= f; r.w *= f;
   }
   constexpr int kAhead = 8;   // segments read at once: the chain over them is arithmetic only
@@ -896,15 +933,15 @@ __global__ void __launch_bounds__(64) k_decay_prefix(const __grid_constant__ Pre
     float4 own[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      if (i0 + i + 1 < segs)   // the run's last segment has no sum: nothing follows it
+      if (i0 + i + (a.fin[j] ? 0 : 1) < segs)   // the run's last segment has a sum only for a state after it
         own[i] = *reinterpret_cast<const float4*>(st + (size_t)(a.rev[j] ? segs - 1 - i0 - i : i0 + i) * a.dd);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (i0 + i < segs) {
         const int p = a.rev[j] ? segs - 1 - i0 - i : i0 + i;
         *reinterpret_cast<float4*>(st + (size_t)p * a.dd) = r;
-        if (i0 + i + 1 < segs) {
-          const Decay dec(ld * min(span, L - p * span));
+        if (i0 + i + (a.fin[j] ? 0 : 1) < segs) {
+          const Decay dec(ld * (min(span, L - p * span) - (p == segs - 1 ? a.fin_sub[j] : 0)));
           r.x = dec(r.x) + own[i].x;
           r.y = dec(r.y) + own[i].y;
           r.z = dec(r.z) + own[i].z;
@@ -912,6 +949,7 @@ __global__ void __launch_bounds__(64) k_decay_prefix(const __grid_constant__ Pre
         }
       }
   }
+  if (a.fin[j]) *reinterpret_cast<float4*>(a.fin[j] + (size_t)u * a.dd + e) = r;
 }
 
 bool maps(TcJob* t, const DecayArgs& a, const DecayJob& j, bool with_x) {
@@ -920,23 +958,24 @@ bool maps(TcJob* t, const DecayArgs& a, const DecayJob& j, bool with_x) {
          make_tmap_tokens_bf16(&t->z, j.Z, j.db, a.N, a.heads, a.B, j.zs, kC);
 }
 
-template <int DP, bool STATE>
+template <int DP, bool STATE, int PARTS>
 cudaError_t run(const TcArgs& a, int units, int njobs, cudaStream_t st) {
-  using C = Cfg<DP, STATE>;
+  using C = Cfg<DP, STATE, PARTS>;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = raise_smem(k_decay_tc<DP, STATE>, C::kSmem, done);
+  const cudaError_t e = raise_smem(k_decay_tc<DP, STATE, PARTS>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   const dim3 grid(units, a.segs, njobs);
   // A forward's blocks set up and read their first tokens while the states are joined (1 x 8 x 65536 tokens: 108 ->
   // 103 us). Not a backward's: three runs have more blocks than the states' two, and those that come up early on the
   // SMs left free cost more than they win (289 us, 253 one after the other).
-  if (!STATE && a.segs > 1 && njobs == 1) return launch_next(k_decay_tc<DP, STATE>, grid, C::kThreads, C::kSmem, st, a);
-  k_decay_tc<DP, STATE><<<grid, C::kThreads, C::kSmem, st>>>(a);
+  if (!STATE && a.segs > 1 && njobs == 1) return launch_next(k_decay_tc<DP, STATE, PARTS>, grid, C::kThreads, C::kSmem, st, a);
+  k_decay_tc<DP, STATE, PARTS><<<grid, C::kThreads, C::kSmem, st>>>(a);
   return cudaGetLastError();
 }
 template <bool STATE>
-cudaError_t run(const TcArgs& a, int dp, int units, int njobs, cudaStream_t st) {
-  return dp == 64 ? run<64, STATE>(a, units, njobs, st) : run<128, STATE>(a, units, njobs, st);
+cudaError_t run(const TcArgs& a, int dp, int parts, int units, int njobs, cudaStream_t st) {
+  if (dp == 64) return parts == 2 ? run<64, STATE, 2>(a, units, njobs, st) : run<64, STATE, 3>(a, units, njobs, st);
+  return parts == 2 ? run<128, STATE, 2>(a, units, njobs, st) : run<128, STATE, 3>(a, units, njobs, st);
 }
 
 }  // namespace
@@ -987,6 +1026,8 @@ cudaError_t launch_prefix(const DecayArgs& a, const DecaySplit& sp, const Prefix
     p.init[i] = r[i].init;
     p.rev[i] = r[i].rev;
     p.init_decays[i] = r[i].init_decays;
+    p.fin[i] = r[i].fin;
+    p.fin_sub[i] = r[i].fin_sub;
   }
   p.log_decay = a.log_decay;
   p.lengths = a.lengths;
@@ -1026,10 +1067,11 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
   t.N = a.N;
   t.segs = sp.segs;
   t.seg_chunks = sp.seg_chunks;
-  int dp = 64;
+  int dp = 64, parts = 2;   // three parts of y's decayed rows where a state is returned
   for (int i = 0; i < a.njobs; ++i) {
     const DecayJob& j = a.job[i];
     if (j.da > 64 || j.db > 64) dp = 128;
+    if (j.fin) parts = 3;
   }
   const int dd = a.job[0].da * a.job[0].db;
   // states before the segments: run 0 forwards, and for the backward its last run (y = q, z = dO)
@@ -1046,8 +1088,12 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
       o.rev = jobs[i].rev;
       o.c_state = jobs[i].c_state;
       o.local = a.ws + i * states;
+      o.fin = p[i].fin = jobs[i].fin;
+      o.fin_sub = jobs[i].fin ? jobs[i].fin_sub : 0;
+      p[i].fin_sub = o.fin_sub;
+      o.third = jobs[i].fin != nullptr;
     }
-    cudaError_t e = run<true>(t, dp, units, ns, st);
+    cudaError_t e = run<true>(t, dp, parts, units, ns, st);
     if (e != cudaSuccess) return e;
     e = launch_prefix(a, sp, p, ns, st);
     if (e != cudaSuccess) return e;
@@ -1066,7 +1112,8 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
     memcpy(o.zs, j.zs, sizeof(o.zs));
     o.init = j.init;
     o.seg_init = a.ws + (i == 0 ? 0 : states);
-    o.fin = j.fin;
+    o.fin = sp.segs > 1 ? nullptr : j.fin;   // the join writes it
+    o.third = o.fin != nullptr;
     o.wide = j.db % 16 == 0 && (reinterpret_cast<uintptr_t>(j.O) & 31u) == 0 && (j.os[0] | j.os[1] | j.os[2]) % 16 == 0;
     o.da = j.da;
     o.db = j.db;
@@ -1078,7 +1125,7 @@ cudaError_t launch_decay_tc(const DecayArgs& a, cudaStream_t st) {
     o.c_intra = j.c_intra;
     o.c_state = j.c_state;
   }
-  return run<false>(t, dp, units, a.njobs, st);
+  return run<false>(t, dp, sp.segs > 1 ? 2 : parts, units, a.njobs, st);
 }
 
 }  // namespace lfa

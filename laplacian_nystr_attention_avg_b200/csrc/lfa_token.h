@@ -93,10 +93,12 @@ struct NormArgs {
 };
 
 cudaError_t launch_decay(const DecayArgs& a, int dtype, cudaStream_t st);
-// The end states of a call's segments, carried over the segments (in place in a.ws): initial state and direction.
+// The end states of a call's segments, carried over the segments (in place in a.ws): initial state, direction, and
+// where the state after the run goes, if the last segment's own state is there too.
 struct PrefixRun {
   const float* init;
-  int rev, init_decays;
+  float* fin;
+  int rev, init_decays, fin_sub;
 };
 int state_runs(const DecayArgs& a, DecayJob* jobs, PrefixRun* p);
 cudaError_t launch_prefix(const DecayArgs& a, const DecaySplit& sp, const PrefixRun* p, int n, cudaStream_t st);

@@ -533,3 +533,26 @@ def test_bf16_gradients_beyond_32_bits():
     want = decay.decay_backward(q.contiguous(), k.contiguous(), v.contiguous(), ld, dO.contiguous())
     for a, b, into in zip(got, want, (dQ, dK, dV)):
         assert a is into and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("B,H,N,dk,dv,lengths", [
+    (1, 2, 8, 64, 64, None), (1, 2, 128, 128, 128, None), (1, 2, 4096, 64, 64, None), (2, 3, 1000, 40, 72, [1000, 333]),
+    (1, 2, 500, 128, 24, None), (1, 1, 9000, 64, 64, None), (3, 2, 5000, 72, 128, [5000, 0, 700]), (160, 1, 300, 64, 48, None)])
+def test_returned_states_of_bf16_tensors_are_fp32(B, H, N, dk, dv, lengths):
+    """k's decayed rows keep the 24 bits of their fp32 products (2^-24), so what is left is the tensor cores' sums: three
+    parts of 128 tokens in products of 16 make 24 accumulations a chunk, each cutting off 2^-24 on average of a partial
+    sum, whose norm is at most the sum's for independent terms. 24 2^-24 of the norm, whether the chunks' states add up
+    in one run or in segments."""
+    q, k, v, ld, S0, L, g = _inputs(B, H, N, dk, dv, BF, "bnhd", True, lengths, "slow", seed=N)
+    dO = _mk((B, H, N, dv), BF, g, "bnhd")
+    _poison(dO, L)
+    dS = torch.randn(S0.shape, generator=g, device="cuda")
+    _, S = decay.decay_forward(q, k, v, ld, S0=S0, lengths=L, return_state=True)
+    dS0 = decay.decay_backward(q, k, v, ld, dO, S0=S0, lengths=L, dS_out=dS, return_state=True)[3]
+    q, k, v, dO = (_clean(t, L) for t in (q, k, v, dO))
+    want = R.decay_forward(q, k, v, ld, dk ** -0.5, S0.double(), L)[1]
+    grads = R.decay_grads(q, k, v, ld, dk ** -0.5, S0.double(), L, dO, dS.double())
+    for name, got, ref in (("S", S, want), ("dS0", dS0, grads[3])):
+        for b in range(B):
+            rel = float((got[b].double() - ref[b]).norm() / ref[b].norm())
+            assert rel <= 24 * 2.0 ** -24, f"{name}[{b}]: {rel:.2e}"
