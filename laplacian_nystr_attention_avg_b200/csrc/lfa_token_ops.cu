@@ -236,20 +236,34 @@ constexpr int kNormWave = 4 * 148;   // blocks that run at once
 constexpr int kMaxChunks = 64;   // row chunks per sample (large groups)
 
 // The activations, in pairs. p = 1 / (1 + exp(-z)) and q = 1 - p are formed from exp(-|z|), so that neither loses its
-// small end; fp32 tensors take CUDA's expf (2 units) and have p within 2^-21 of itself down to fp32's last number. bf16
-// tensors, whose output keeps 2^-8, take p alone as ex2 of z log2 e rounded once, |z| 2^-24 relative, 0 below z = -87:
-// two special-function instructions an element, which is what their rows wait for.
+// small end, and p is within 2^-20 of itself down to fp32's last number. bf16 tensors, whose output keeps 2^-8, take p
+// alone as ex2 of z log2 e rounded once, |z| 2^-24 relative, 0 below z = -87: two special-function instructions an
+// element, which is what their rows wait for.
 __device__ __forceinline__ float rcp_approx(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// exp(-x) for x >= 0, within 2^-20: the square of ex2 of t = -x log2 e / 2, rounded, so that results below 2^-126 are
+// left (the instruction has none), times exp of what t's rounding cut off. (0 from x = 104 on; x may be infinite.)
+__device__ __forceinline__ uint64_t exp_minus2(uint64_t x) {
+  x = f2(fminf(f2_lo(x), 200.f), fminf(f2_hi(x), 200.f));
+  constexpr float kHalf = 0.72134752044448170f;   // log2 e / 2, and what fp32 leaves of it
+  constexpr float kRest = (float)(0.72134752044448170 - (double)kHalf);
+  const uint64_t t = mul2(x, both(-kHalf));
+  const uint64_t cut = fma2(x, both(kRest), fma2(x, both(kHalf), t));   // minus what t lacks
+  const uint64_t h = f2(sm100::ex2_approx(f2_lo(t)), sm100::ex2_approx(f2_hi(t)));
+  return mul2(mul2(h, fma2(cut, both(-1.3862943611198906f), both(1.f))), h);
+}
 struct Pq {
-  float p, q;
+  uint64_t p, q;
 };
-__device__ __forceinline__ Pq sigmoid_full(float z) {
-  const float e = expf(-fabsf(z)), r = rcp_approx(1.f + e), s = e * r;   // r in [1/2, 1]
-  return z < 0.f ? Pq{s, r} : Pq{r, s};
+__device__ __forceinline__ Pq sigmoid_full2(uint64_t z) {
+  const float a = f2_lo(z), b = f2_hi(z);
+  const uint64_t e = exp_minus2(f2(fabsf(a), fabsf(b))), d = add2(e, both(1.f));
+  const uint64_t r = f2(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d))), s = mul2(e, r);   // r in [1/2, 1]
+  return Pq{f2(a < 0.f ? f2_lo(s) : f2_lo(r), b < 0.f ? f2_hi(s) : f2_hi(r)),
+            f2(a < 0.f ? f2_lo(r) : f2_lo(s), b < 0.f ? f2_hi(r) : f2_hi(s))};
 }
 __device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
   const uint64_t t = mul2(z, both(-1.4426950408889634f));
@@ -257,10 +271,10 @@ __device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
   return f2(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d)));
 }
 // The normal distribution's integral and exp(-z^2 / 2). With a = |z|, the tail beyond a is m(a) exp(-a^2 / 2) with a
-// smooth m, so it keeps its relative accuracy at any a (0.5 + 0.5 erf(z / sqrt 2) is off by more than half a step of bf16
-// from z = -4.3 on, of fp32 from z = -2.2). m = t (c0 + c1 t + ..), t = 1 / (1 + s a): the coefficients of least relative deviation for a <= 15, behind
-// which the exponential is zero; degree 5 leaves 2^-16.6, degree 8 in fp32 arithmetic 2^-21.5. 65536 x 1024 bf16 in
-// 16 groups: 74 us; with erff 98, with erfcf 148.
+// smooth m, so it keeps its relative accuracy at any a (0.5 + 0.5 erf(z / sqrt 2) is off by more than half a step of
+// bf16 from z = -4.3 on, of fp32 from z = -2.2). m = t (c0 + c1 t + ..), t = 1 / (1 + s a): the coefficients of least
+// relative deviation for a <= 15, behind which the exponential is zero; degree 5 leaves 2^-16.6, degree 8 in fp32
+// arithmetic 2^-21.5. 65536 x 1024 bf16 in 16 groups: 74 us; with erff 98, with erfcf 148.
 struct Normal {
   uint64_t cdf, e;
 };
@@ -276,7 +290,7 @@ __device__ __forceinline__ Normal normal2(uint64_t z) {
   const uint64_t t = f2(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d)));
   Normal n;
   if constexpr (kFull) {
-    n.e = f2(expf(-0.5f * zl * zl), expf(-0.5f * zh * zh));
+    n.e = exp_minus2(mul2(mul2(z, both(0.5f)), z));
   } else {
     const uint64_t w = mul2(mul2(z, z), both(-0.72134752044448170f));
     n.e = f2(sm100::ex2_approx(f2_lo(w)), sm100::ex2_approx(f2_hi(w)));
@@ -291,7 +305,7 @@ __device__ __forceinline__ Normal normal2(uint64_t z) {
 template <typename T, int ACT>
 __device__ __forceinline__ uint64_t act2(uint64_t z) {
   if (ACT == LFA_ACT_SILU) {
-    if constexpr (sizeof(T) == 4) return mul2(z, f2(sigmoid_full(f2_lo(z)).p, sigmoid_full(f2_hi(z)).p));
+    if constexpr (sizeof(T) == 4) return mul2(z, sigmoid_full2(z).p);
     return mul2(z, sigmoid2(z));
   }
   if (ACT == LFA_ACT_GELU) return mul2(z, normal2<T>(z).cdf);
@@ -301,9 +315,8 @@ template <typename T, int ACT>
 __device__ __forceinline__ uint64_t slope2(uint64_t z) {
   if (ACT == LFA_ACT_SILU) {   // p + z p q
     if constexpr (sizeof(T) == 4) {
-      const Pq a = sigmoid_full(f2_lo(z)), b = sigmoid_full(f2_hi(z));
-      const uint64_t p = f2(a.p, b.p);
-      return fma2(mul2(z, f2(a.q, b.q)), p, p);
+      const Pq s = sigmoid_full2(z);
+      return fma2(mul2(z, s.q), s.p, s.p);
     }
     const uint64_t p = sigmoid2(z);
     return fma2(mul2(z, p), fma2(p, both(-1.f), both(1.f)), p);
