@@ -1071,7 +1071,13 @@ struct Plan {
   size_t m12, stats;   // offsets in it
 };
 
-Plan plan_norm(int B, int N, int C, int G, int es, bool backward) {
+// Registers or three launches, by whether a warp's or block's team holds a group. Registers win forward wherever they
+// hold it (2000 x 16 x 512 in 8 groups, bf16: 29 us, 81 in three launches; 500 x 64 x 512 in 16: 25 and 46). A backward
+// with gamma has to read its rows again for the channels' sums, where dgamma and dbeta do not come from k_norm_rows.
+// With samples of 64 bytes a channel and groups of 1.5 KB the three launches are the shorter way: bf16, N = 64 in 16
+// groups 54 us, from registers 83, and N = 16 77 and 68; fp32, N = 16 in 8 groups 93 and 119, N = 4 138 and 118 (all
+// 8.2 M elements); 1000 x 32 x 256 in 32 groups of 1 KB 79 and 62. Without gamma registers take 52 for the first.
+Plan plan_norm(int B, int N, int C, int G, int es, bool backward, bool affine) {
   Plan p;
   memset(&p, 0, sizeof(p));
   const int dg = C / G;
@@ -1111,6 +1117,7 @@ Plan plan_norm(int B, int N, int C, int G, int es, bool backward) {
     }
     p.E = cap;
   }
+  if (p.small && backward && affine && N * es >= 64 && N * dg * es >= 1536) p.small = false;   // (p.small bounds N dg)
   // rows in chunks
   const int VB = p.small ? vec_bytes(C, es) : (p.VB = vec_bytes(C, es)), cv = C * es / VB;
   r.cw = cv <= 256 ? cv : 128;
@@ -1254,7 +1261,7 @@ struct LargeBackward {
 
 template <typename T>
 void run_norm(const NormArgs& a, cudaStream_t st) {
-  Plan p = plan_norm(a.B, a.N, a.C, a.G, sizeof(T), false);
+  Plan p = plan_norm(a.B, a.N, a.C, a.G, sizeof(T), false, a.gamma != nullptr);
   p.s.a = p.r.a = a;
   p.r.part = a.ws;
   if (!p.small && !a.mean) {
@@ -1265,7 +1272,7 @@ void run_norm(const NormArgs& a, cudaStream_t st) {
 }
 template <typename T>
 void run_norm_backward(const NormArgs& a, cudaStream_t st) {
-  Plan p = plan_norm(a.B, a.N, a.C, a.G, sizeof(T), true);
+  Plan p = plan_norm(a.B, a.N, a.C, a.G, sizeof(T), true, a.gamma != nullptr);
   p.s.a = p.r.a = a;
   p.r.part = a.ws;
   if (!p.small) {
@@ -1293,7 +1300,10 @@ cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t st) {
 }
 
 size_t norm_workspace_floats(int B, int N, int C, int G, int dtype, int backward) {
-  return plan_norm(B, N, C, G, dtype == LFA_BF16 ? 2 : 4, backward != 0).floats;
+  const int es = dtype == LFA_BF16 ? 2 : 4;
+  const size_t with = plan_norm(B, N, C, G, es, backward != 0, true).floats;
+  const size_t without = plan_norm(B, N, C, G, es, backward != 0, false).floats;
+  return with > without ? with : without;
 }
 
 cudaError_t launch_norm(const NormArgs& a, int dtype, cudaStream_t st) {
