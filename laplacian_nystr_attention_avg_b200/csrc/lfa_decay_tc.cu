@@ -928,19 +928,21 @@ __global__ void __launch_bounds__(64) k_decay_prefix(const __grid_constant__ Pre
     const float f = expf(ld);
     r.x *= f; r.y *= f; r.z *= f; r.w *= f;
   }
+  const int sums = a.fin[j] ? segs : segs - 1;   // the run's last segment has a sum only for a state after it
+  const long long step = a.rev[j] ? -(long long)a.dd : a.dd;
+  float* from = a.rev[j] ? st + (size_t)(segs > 0 ? segs - 1 : 0) * a.dd : st;
   constexpr int kAhead = 8;   // segments read at once: the chain over them is arithmetic only
   for (int i0 = 0; i0 < segs; i0 += kAhead) {
     float4 own[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      if (i0 + i + (a.fin[j] ? 0 : 1) < segs)   // the run's last segment has a sum only for a state after it
-        own[i] = *reinterpret_cast<const float4*>(st + (size_t)(a.rev[j] ? segs - 1 - i0 - i : i0 + i) * a.dd);
+      if (i0 + i < sums) own[i] = *reinterpret_cast<const float4*>(from + (i0 + i) * step);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (i0 + i < segs) {
         const int p = a.rev[j] ? segs - 1 - i0 - i : i0 + i;
-        *reinterpret_cast<float4*>(st + (size_t)p * a.dd) = r;
-        if (i0 + i + (a.fin[j] ? 0 : 1) < segs) {
+        *reinterpret_cast<float4*>(from + (i0 + i) * step) = r;
+        if (i0 + i < sums) {
           const Decay dec(ld * (min(span, L - p * span) - (p == segs - 1 ? a.fin_sub[j] : 0)));
           r.x = dec(r.x) + own[i].x;
           r.y = dec(r.y) + own[i].y;
@@ -980,9 +982,12 @@ cudaError_t run(const TcArgs& a, int dp, int parts, int units, int njobs, cudaSt
 
 }  // namespace
 
-// How the sequences are cut. bf16: one CTA fills an SM; fewer than 148 of them (units x runs) are cut so that about 148
-// run at once, in segments of at least 4 chunks (below that the extra launches and the second reading of y and z cost
-// more). 4096 tokens of 74 units in two segments 103 us at 128 channels, 70 at 64; 80 units uncut 111 and 66.
+// How the sequences are cut. bf16: one CTA fills an SM, and fewer than 148 of them (units x runs) are cut so that about
+// 148 run at once. A cut call takes 1.4 times as long for the chunks of its longest segment (the states' pass reads y and
+// z too) and about five chunks more for two launches and the join: it has to win more than that. Forward, 1024 tokens:
+// 8 units of 128 channels in 8 segments 23 us, uncut 29; 24 units in 4 segments 29.5 both; 40 units in 3 40, uncut 31;
+// 512 tokens 22 and 18. 8 units of 2048 tokens x 64 in 16 segments 18 us, in 4 22, uncut 31; 70 units of 2048 x 64 in 2
+// 35.5, uncut 32; 40 units of 2048 x 128 in 3 51, uncut 56.
 // fp32: blocks (64 columns of a unit's run) are bound by arithmetic, and the states take it to 1.5 (backward 1.3) times.
 // So fewer than 148 runs are cut, into about 592 segments in all, if uncut blocks would leave more than
 // that idle. At more than 64 rows of the state one block fills an SM (dk = dv = 128, forward, 1024 tokens: 147 units
@@ -995,7 +1000,8 @@ DecaySplit decay_split(int B, int heads, int N, int dk, int dv, int njobs, int d
   long long segs = 1;
   if (dtype == LFA_BF16) {
     if (runs < 148) segs = 148 / runs;
-    segs = segs < nch / 4 ? segs : nch / 4;
+    segs = segs < nch ? segs : nch;
+    if (7 * ceil_div(nch, (int)segs) + 25 >= 5 * nch) segs = 1;
   } else if (runs < 148) {
     // a forward's run has dk rows and dv columns; a backward's have dv, dv, dk rows and dk, dk, dv columns
     const bool bwd = njobs > 1;

@@ -308,3 +308,13 @@ def test_fp32_segments_count_blocks(lib, units, N, dk, dv, bwd, segs):
     n = lib.lfa_decay_workspace_size(_dc(B=units, heads=1, N=N, dk=dk, dv=dv, dtype=lfa.LFA_F32), bwd)
     states = units * segs * dk * dv * 4 * (2 if bwd else 1)
     assert n == 256 + (states if segs > 1 else 0)
+
+
+@pytest.mark.parametrize("units,N,d,bwd,segs", [
+    (8, 1024, 128, 0, 8), (8, 512, 128, 0, 1), (24, 1024, 128, 0, 4), (24, 1024, 128, 1, 1), (40, 1024, 64, 0, 1),
+    (40, 2048, 128, 0, 3), (70, 1024, 64, 0, 1), (70, 2048, 64, 0, 1), (74, 4096, 128, 0, 2), (8, 2048, 64, 0, 16), (8, 65536, 64, 0, 18),
+    (147, 65536, 64, 0, 1), (148, 65536, 64, 0, 1), (1, 128, 64, 0, 1)])
+def test_bf16_segments_win_their_cost(lib, units, N, d, bwd, segs):
+    """Segments cost two launches, a join and a second reading: no call is cut for less."""
+    n = lib.lfa_decay_workspace_size(_dc(B=units, heads=1, N=N, dk=d, dv=d), bwd)
+    assert n == 256 + (units * segs * d * d * 4 * (2 if bwd else 1) if segs > 1 else 0)
