@@ -24,9 +24,9 @@ namespace {
 // shared memory; the state R [da][CB] lives there. A thread has a 4 x 4 tile of each product, which makes 64
 // multiply-adds per eight 16-byte reads; above the diagonal nothing is computed, by the rows of a warp.
 // STATE: the segment's own state only. Bound by the fp32 multiply-adds and the shared-memory reads that feed them
-// (64 units x 784 tokens, dk 32, dv 64: 69 us in three launches, issue slots half full, two blocks an SM; at three,
-// with 80 registers, 64 us, but the backward 245 instead of 192). Not taken: 32 columns a block (174 us), operands
-// transposed for packed multiply-adds (75 us beside 58 in the main launch alone).
+// (64 units x 784 tokens, dk 32, dv 64: 65 us in three launches, issue slots half full, two blocks an SM; with three,
+// at 80 registers, the backward took 245 instead of 192). Not taken: 32 columns a block (174 us), operands transposed
+// for packed multiply-adds (75 us beside 58 in the main launch alone, when that was written).
 constexpr int kCC = 64;   // tokens per step
 constexpr int CB = 64;    // columns of z a block takes
 

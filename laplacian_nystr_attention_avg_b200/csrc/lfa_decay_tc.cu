@@ -9,11 +9,11 @@
 //   D  = (y c_state l^(n-j))^T z            (M da, N db, K 128 tokens), R' = l^n R + D   (state warps)
 // The decayed rows of y enter as bf16 parts, one product each. Where R only meets x, which rounds it to bf16, two parts
 // leave 4e-6 of its norm. Runs that return a state take three, the 24 bits of an fp32 product: such a state is 0.5e-6
-// off, after 8 tokens as after 4096, of which the tensor cores' own sums are the most. (8 x 16 x 4096 tokens x 128: 141
-// us with a state, 121 without; at 64 channels 90 and 72, where the third product has zeros in half of its rows; in
-// segments only the states' kernel has it: 1 x 8 x 65536 118 and 107.) An infinity has a NaN as its remainder: states and
-// outputs that the formula makes infinite may be NaN. D starts from zero in every chunk and is added to R by CUDA cores:
-// tensor-core accumulation truncates and would drift over thousands of chunks.
+// off, after 8 tokens as after 4096, of which the tensor cores' own sums are the most. (8 x 16 x 4096 tokens x 128: 140
+// us with a state, 118 without; at 64 channels 94 and 72, where the third product has zeros in half of its rows; of
+// segments only the states' kernel has it: 1 x 8 x 65536 x 64 112 and 107.) An infinity has a NaN as its remainder:
+// states and outputs that the formula makes infinite may be NaN. D starts from zero in every chunk and is added to R by
+// CUDA cores: tensor-core accumulation truncates and would drift over thousands of chunks.
 // All widths are padded to DP = 64 or 128 by TMA's zero fill.
 //
 // Warps: 4 or 8 for P, 4 or 8 for y's decayed rows, 8 for R and the epilogue, one each to issue TMA loads, the

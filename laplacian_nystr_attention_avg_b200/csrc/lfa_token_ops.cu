@@ -75,7 +75,8 @@ __device__ __forceinline__ Raw<VB> raw_make(const uint64_t* v) {
 // angle; the rest is fp32. A thread has one token and one unit of a head's channels (V pairs in two 16-byte vectors,
 // V / 2 pairs in one, or a single pair), forms their cosines and sines once, and goes over the heads.
 // Bound by the bytes: 4 x 4096 tokens, 2 x 16 heads of 128 (268 MB) in 50 us, 5.4 TB/s, whether 64, 96 or 128 channels
-// turn; a plain copy of them takes 47.
+// turn, in either layout; a plain copy of them takes 47. A half layout whose rot / 2 is no whole number of vectors goes
+// element by element: 142 us (20 of 128 channels, bf16), 83 in fp32.
 constexpr int kRThreads = 256;
 constexpr int rotary_blocks(int mode) { return mode == 0 ? 3 : 5; }   // an SM at a time: 80 registers a thread, or 48
 constexpr int kRHeads = 2;   // heads read at once, one such group ahead
@@ -225,11 +226,12 @@ void run_rotary(const RotaryArgs& a, cudaStream_t st) {
 // take three launches: per-channel sums of row chunks, their combination per group, and the output; the second
 // reading comes from the 126 MB L2 as far as the tensor fits there. All sums are joined in a fixed order.
 // Measured, bf16 with silu: 8192 x 1024 in 16 groups (33.6 MB) 13 us, of which a launch and four dependent rounds a
-// warp are most; 65536 rows 57 us, 4.7 TB/s, where exponentials and reciprocals alone take 30 (without silu 46 us,
-// the copy bandwidth), and backward 95 us (402 MB: 62; with the sums of dgamma and dbeta in a launch before: 169). Large, 32 x 3136 x 256 in 32 groups (51 MB a tensor): forward 44 us, sums 19 and output 20 of
-// it; backward 56 us, sums 26, output 24. These wait for memory latency and the activation's two special-function
-// instructions per element (half their pipe) in turn; the join is a few microseconds of latency, most of it under
-// the neighbours (three launches apart: 49 and 64 us).
+// warp are most; 65536 rows 56 us, 4.8 TB/s, where exponentials and reciprocals alone take 30 (without silu 46 us,
+// the copy bandwidth), and backward 91 us (402 MB: 62; with the sums of dgamma and dbeta in a launch before: 169).
+// Large, 32 x 3136 x 256 in 32 groups (51 MB a tensor): forward 42 us, sums 19 and output 20 of it; backward 56 us,
+// sums 26, output 24. These wait for memory latency and the activation's two special-function instructions per element
+// (half their pipe) in turn; the join is a few microseconds of latency, most of it under the neighbours (three launches
+// apart: 49 and 64 us).
 constexpr int kNT = 256;         // threads per block
 constexpr int kNRows = 8;        // rows a thread has in flight
 constexpr int kNormWave = 4 * 148;   // blocks that run at once
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kNT) k_norm_small(const __grid_constant__ Smal
 // The same for groups of one vector per thread (T a power of two): a thread keeps its channels over all the samples it
 // takes (every teams-th (sample, group); teams is a multiple of G), U at once and the next U on their way; backward it
 // sums its channels' dgamma and dbeta as it goes. (Twice the blocks, or U = 4 on three a SM, were slower: 8192 x 1024
-// 16.6 and 17.3 us beside 15.1.)
+// 16.6 and 17.3 us when this took 15.1, now 13.)
 template <typename T, int VB, int ACT, bool BACKWARD>
 __global__ void __launch_bounds__(kNT, BACKWARD ? 2 : 4) k_norm_rows(const __grid_constant__ SmallArgs s, int teams) {
   constexpr int V = VB / sizeof(T), U = 2;
